@@ -260,6 +260,155 @@ int ada_lora_batch(const ada_lora_proj* projs, int32_t n_proj, int32_t nb, int32
                    const int32_t* idx, const float* gate, int32_t k, float scale,
                    void* workspace, int64_t workspace_bytes, int32_t dtype, void* stream);
 
+/*
+ * Activations of the linear and gated products.  GELU is the error-function form
+ * z Phi(z); GELU_TANH its tanh approximation 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))).
+ */
+typedef enum {
+  ADA_ACT_NONE = 0,
+  ADA_ACT_RELU = 1,
+  ADA_ACT_SILU = 2,
+  ADA_ACT_GELU = 3,
+  ADA_ACT_GELU_TANH = 4
+} ada_act;
+
+/*
+ * The projections of a layer for any number of rows (a prompt, a batch of requests, or one
+ * decode token), on the merged backbone or any other weights, and their gradients.
+ *   - Matrices are row-major with a row stride ld (elements, at least the row's length, at
+ *     most 2^36): row i of a matrix of c columns is elements [i ld, i ld + c).  Every
+ *     pointer and every row stride is 16-byte aligned.
+ *   - rows: 0 <= rows <= 2^22, odd ones included.  With rows = 0 the matrices of `rows`
+ *     rows may be NULL; the forward calls then write nothing, and the gradients summed
+ *     over rows are zeros.
+ *   - An output may not overlap an input or another output, except that y may be the
+ *     residual itself (same pointer and row stride; the residual stream updated in place).
+ *     Views of one buffer that interleave (column ranges of its rows) do not overlap when
+ *     their row strides are equal.  Overlaps return ADA_EINVAL.
+ *   - Sums and activations are fp32; each result is rounded to the storage type once.  The
+ *     backward calls round dz (dg, du) to the storage type once more, as an operand of the
+ *     matrix instructions (no effect in fp32); dbias sums the unrounded dz.
+ *   - `workspace`: caller-owned device memory, 16-byte aligned, of at least as many bytes as
+ *     the call's _workspace function returns (0: may be NULL).  Its contents need not be
+ *     set and mean nothing afterwards.  Calls that overlap in time need workspaces of
+ *     their own.
+ */
+typedef struct {
+  const void* x;         /* [rows][d_in]                                       */
+  const void* w;         /* [d_out][d_in]                                      */
+  const void* bias;      /* NULL or [d_out]                                    */
+  const void* residual;  /* NULL or [rows][d_out], added after the activation  */
+  void* y;               /* [rows][d_out]                                      */
+  void* pre;             /* NULL or [rows][d_out]: z, for the backward pass    */
+  int64_t ld_x;
+  int64_t ld_w;
+  int64_t ld_res;
+  int64_t ld_y;
+  int64_t ld_pre;
+  int64_t rows;
+  int32_t d_out;
+  int32_t d_in;
+} ada_linear_args;
+
+/* z = x w^T + bias;  y = act(z) + residual. */
+int ada_linear(const ada_linear_args* args, int32_t act, int32_t dtype, void* workspace,
+               int64_t workspace_bytes, void* stream);
+/* Bytes of workspace; negative status on bad sizes (here and in the three like it). */
+int64_t ada_linear_workspace(int64_t rows, int32_t d_out, int32_t d_in, int32_t dtype);
+
+typedef struct {
+  const void* dy;   /* [rows][d_out] gradient of y                                     */
+  const void* x;    /* [rows][d_in]; read for dw                                       */
+  const void* w;    /* [d_out][d_in]; read for dx                                      */
+  const void* pre;  /* [rows][d_out] z as ada_linear saved it; not read for ADA_ACT_NONE */
+  void* dx;         /* NULL or [rows][d_in]                                            */
+  void* dw;         /* NULL or [d_out][d_in]                                           */
+  void* dbias;      /* NULL or [d_out]                                                 */
+  int64_t ld_dy;
+  int64_t ld_x;
+  int64_t ld_w;
+  int64_t ld_pre;
+  int64_t ld_dx;
+  int64_t ld_dw;
+  int64_t rows;
+  int32_t d_out;
+  int32_t d_in;
+} ada_linear_grad_args;
+
+/*
+ * dz = dy act'(z);  dx = dz w;  dw = dz^T x;  dbias = sum over rows of dz; at least one of
+ * the three is asked for.  The gradient of the residual is dy.  relu'(0) = 0.  The
+ * gradients are overwritten, not added to.
+ */
+int ada_linear_backward(const ada_linear_grad_args* args, int32_t act, int32_t dtype,
+                        void* workspace, int64_t workspace_bytes, void* stream);
+int64_t ada_linear_backward_workspace(int64_t rows, int32_t d_out, int32_t d_in, int32_t act,
+                                      int32_t dtype);
+
+typedef struct {
+  const void* x;          /* [rows][d_in]                                        */
+  const void* w_gate;     /* [d_out][d_in]                                       */
+  const void* w_up;       /* [d_out][d_in]                                       */
+  const void* bias_gate;  /* NULL or [d_out]                                     */
+  const void* bias_up;    /* NULL or [d_out]                                     */
+  void* y;                /* [rows][d_out]                                       */
+  void* gate_pre;         /* NULL or [rows][d_out]: g, for the backward pass     */
+  void* up_pre;           /* NULL or [rows][d_out]: u                            */
+  int64_t ld_x;
+  int64_t ld_w_gate;
+  int64_t ld_w_up;
+  int64_t ld_y;
+  int64_t ld_gate_pre;
+  int64_t ld_up_pre;
+  int64_t rows;
+  int32_t d_out;
+  int32_t d_in;
+} ada_glu_args;
+
+/*
+ * Gated feed-forward pair: g = x w_gate^T + bias_gate, u = x w_up^T + bias_up,
+ * y = act(g) u, without g and u passing through memory (unless asked for).
+ */
+int ada_glu(const ada_glu_args* args, int32_t act, int32_t dtype, void* workspace,
+            int64_t workspace_bytes, void* stream);
+int64_t ada_glu_workspace(int64_t rows, int32_t d_out, int32_t d_in, int32_t dtype);
+
+typedef struct {
+  const void* dy;        /* [rows][d_out]                                     */
+  const void* x;         /* [rows][d_in]; read for dw_gate, dw_up             */
+  const void* w_gate;    /* [d_out][d_in]; read for dx                        */
+  const void* w_up;      /* [d_out][d_in]; read for dx                        */
+  const void* gate_pre;  /* [rows][d_out] g and u as ada_glu saved them       */
+  const void* up_pre;
+  void* dx;              /* NULL or [rows][d_in]                              */
+  void* dw_gate;         /* NULL or [d_out][d_in]                             */
+  void* dw_up;           /* NULL or [d_out][d_in]                             */
+  void* dbias_gate;      /* NULL or [d_out]                                   */
+  void* dbias_up;        /* NULL or [d_out]                                   */
+  int64_t ld_dy;
+  int64_t ld_x;
+  int64_t ld_w_gate;
+  int64_t ld_w_up;
+  int64_t ld_gate_pre;
+  int64_t ld_up_pre;
+  int64_t ld_dx;
+  int64_t ld_dw_gate;
+  int64_t ld_dw_up;
+  int64_t rows;
+  int32_t d_out;
+  int32_t d_in;
+} ada_glu_grad_args;
+
+/*
+ * dg = dy u act'(g), du = dy act(g);  dx = dg w_gate + du w_up, dw_gate = dg^T x,
+ * dw_up = du^T x, dbias_gate and dbias_up the sums of dg and du over rows; at least one
+ * of the five is asked for.
+ */
+int ada_glu_backward(const ada_glu_grad_args* args, int32_t act, int32_t dtype, void* workspace,
+                     int64_t workspace_bytes, void* stream);
+int64_t ada_glu_backward_workspace(int64_t rows, int32_t d_out, int32_t d_in, int32_t act,
+                                   int32_t dtype);
+
 /* Static text for a status code (never NULL). */
 const char* ada_status_string(int status);
 

@@ -9,6 +9,10 @@ from .api import (  # noqa: F401
     AdaModel,
     ada_decode_gemv,
     ada_decode_gemv_layer,
+    ada_glu,
+    ada_glu_backward,
+    ada_linear,
+    ada_linear_backward,
     ada_lora_apply,
     ada_lora_batch,
     ada_lora_layer,

@@ -12,7 +12,8 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import ADA_BF16, ADA_F32, AdaGemvProj, AdaLoraProj, AdaProj
+from ._lib import (ADA_BF16, ADA_F32, AdaGemvProj, AdaGluArgs, AdaGluGradArgs, AdaLinearArgs, AdaLinearGradArgs,
+                   AdaLoraProj, AdaProj)
 
 _DT = {torch.float32: ADA_F32, torch.bfloat16: ADA_BF16}
 
@@ -348,3 +349,255 @@ def ada_lora_batch(projs, idx, gate, scale: float, workspace=None, stream=None):
                                     float(scale), _dev(workspace, "workspace"),
                                     workspace.numel() * workspace.element_size(), _dtype(w0), _stream(stream))
     _check(st, "ada_lora_batch")
+
+
+# ---- linear and gated feed-forward products ----------------------------------------
+_ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+def _act(act: str) -> int:
+    try:
+        return _ACTS[act]
+    except KeyError:
+        raise ValueError(f"unknown activation {act!r}; expected one of {', '.join(_ACTS)}") from None
+
+
+def _mat(t, rows: int, cols: int, like: torch.Tensor, name: str):
+    """Pointer and row stride of a [rows, cols] matrix of like's dtype and device."""
+    if t is None:
+        return None, 0
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype} like the other tensors, got {t.dtype}")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, not {like.device}")
+    ld, unit = t.stride()
+    if unit != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return t.data_ptr(), ld if rows > 1 else cols
+
+
+def _vec(t, n: int, like: torch.Tensor, name: str):
+    """Pointer of an [n] vector of like's dtype and device."""
+    if t is None:
+        return None
+    if t.shape != (n,):
+        raise ValueError(f"{name} must be [{n}], got {list(t.shape)}")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype} like the other tensors, got {t.dtype}")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, not {like.device}")
+    if t.stride(0) != 1:
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _sizes(x: torch.Tensor, w: torch.Tensor):
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x must be [rows, d_in] and the weights [d_out, d_in]")
+    return x.shape[0], w.shape[0], w.shape[1]
+
+
+def _current(t: torch.Tensor):
+    if not t.is_cuda:
+        raise ValueError("tensors must be on the device")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {t.device}, but cuda:{torch.cuda.current_device()} is current")
+
+
+class _On:
+    """Allocations inside belong to the call's stream: made ready, and taken back, in its order."""
+
+    def __init__(self, stream):
+        self.ctx = None
+        if stream is not None:
+            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+            self.ctx = torch.cuda.stream(s)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _workspace(need: int, workspace, like: torch.Tensor, call: str):
+    """(pointer, bytes, tensor) of the caller's workspace, or of one allocated here."""
+    if need < 0:
+        _check(need, call)
+    if workspace is not None:
+        _contig(workspace, "workspace")
+        if workspace.device != like.device:
+            raise ValueError(f"workspace is on {workspace.device}, not {like.device}")
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    if need == 0:
+        return None, 0, None
+    workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+    return workspace.data_ptr(), need, workspace
+
+
+def linear_workspace_bytes(rows: int, d_out: int, d_in: int, dtype: torch.dtype) -> int:
+    """Bytes of workspace ada_linear needs at these sizes."""
+    n = int(_lib.load().ada_linear_workspace(rows, d_out, d_in, _DT[dtype]))
+    _check(min(n, 0), "ada_linear_workspace")
+    return n
+
+
+def glu_workspace_bytes(rows: int, d_out: int, d_in: int, dtype: torch.dtype) -> int:
+    """Bytes of workspace ada_glu needs at these sizes."""
+    n = int(_lib.load().ada_glu_workspace(rows, d_out, d_in, _DT[dtype]))
+    _check(min(n, 0), "ada_glu_workspace")
+    return n
+
+
+def linear_backward_workspace_bytes(rows: int, d_out: int, d_in: int, act: str, dtype: torch.dtype) -> int:
+    """Bytes of workspace ada_linear_backward needs at these sizes."""
+    n = int(_lib.load().ada_linear_backward_workspace(rows, d_out, d_in, _act(act), _DT[dtype]))
+    _check(min(n, 0), "ada_linear_backward_workspace")
+    return n
+
+
+def glu_backward_workspace_bytes(rows: int, d_out: int, d_in: int, act: str, dtype: torch.dtype) -> int:
+    """Bytes of workspace ada_glu_backward needs at these sizes."""
+    n = int(_lib.load().ada_glu_backward_workspace(rows, d_out, d_in, _act(act), _DT[dtype]))
+    _check(min(n, 0), "ada_glu_backward_workspace")
+    return n
+
+
+def ada_linear(x: torch.Tensor, w: torch.Tensor, bias=None, residual=None, act: str = "none", y=None, pre=None,
+               workspace=None, stream=None):
+    """y = act(x w^T + bias) + residual for x [rows, d_in], w [d_out, d_in] (rows of any
+    matrix may be strided); `pre`, if given, receives x w^T + bias for the backward pass.
+
+    act: "none", "relu", "silu", "gelu" (error function) or "gelu_tanh".  y may be the
+    residual itself.  A workspace and a y not passed are allocated on the call's stream."""
+    rows, d_out, d_in = _sizes(x, w)
+    dt, code, lib = _dtype(x), _act(act), _lib.load()
+    px, ldx = _mat(x, rows, d_in, x, "x")
+    pw, ldw = _mat(w, d_out, d_in, x, "w")
+    pb = _vec(bias, d_out, x, "bias")
+    pr, ldr = _mat(residual, rows, d_out, x, "residual")
+    pp, ldp = _mat(pre, rows, d_out, x, "pre")
+    if y is not None:
+        py, ldy = _mat(y, rows, d_out, x, "y")
+    _current(x)
+    with _On(stream):
+        if y is None:
+            y = torch.empty((rows, d_out), dtype=x.dtype, device=x.device)
+            py, ldy = y.data_ptr(), d_out
+        ws, nbytes, _keep = _workspace(lib.ada_linear_workspace(rows, d_out, d_in, dt), workspace, x,
+                                       "ada_linear_workspace")
+        args = AdaLinearArgs(px, pw, pb, pr, py, pp, ldx, ldw, ldr, ldy, ldp, rows, d_out, d_in)
+        _check(lib.ada_linear(args, code, dt, ws, nbytes, _stream(stream)), "ada_linear")
+    return y
+
+
+def ada_linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, pre=None, act: str = "none", dx=None,
+                        dw=None, dbias=None, want_dx: bool = True, want_dw: bool = True, want_dbias: bool = False,
+                        workspace=None, stream=None):
+    """(dx, dw, dbias) of ada_linear: dz = dy act'(pre), dx = dz w, dw = dz^T x, dbias the
+    sum of dz over rows; None for what is neither passed nor wanted.  `pre` is what
+    ada_linear saved (not needed for act "none")."""
+    rows, d_out, d_in = _sizes(x, w)
+    dt, code, lib = _dtype(x), _act(act), _lib.load()
+    if code == 0:
+        pre = None
+    elif pre is None:
+        raise ValueError("pre is needed for the slope of the activation")
+    pdy, lddy = _mat(dy, rows, d_out, x, "dy")
+    px, ldx = _mat(x, rows, d_in, x, "x")
+    pw, ldw = _mat(w, d_out, d_in, x, "w")
+    pp, ldp = _mat(pre, rows, d_out, x, "pre")
+    _mat(dx, rows, d_in, x, "dx")
+    _mat(dw, d_out, d_in, x, "dw")
+    _vec(dbias, d_out, x, "dbias")
+    _current(x)
+    with _On(stream):
+        if dx is None and want_dx:
+            dx = torch.empty((rows, d_in), dtype=x.dtype, device=x.device)
+        if dw is None and want_dw:
+            dw = torch.empty((d_out, d_in), dtype=x.dtype, device=x.device)
+        if dbias is None and want_dbias:
+            dbias = torch.empty(d_out, dtype=x.dtype, device=x.device)
+        pdx, lddx = _mat(dx, rows, d_in, x, "dx")
+        pdw, lddw = _mat(dw, d_out, d_in, x, "dw")
+        pdb = _vec(dbias, d_out, x, "dbias")
+        ws, nbytes, _keep = _workspace(lib.ada_linear_backward_workspace(rows, d_out, d_in, code, dt), workspace, x,
+                                       "ada_linear_backward_workspace")
+        args = AdaLinearGradArgs(pdy, px, pw, pp, pdx, pdw, pdb, lddy, ldx, ldw, ldp, lddx, lddw, rows, d_out, d_in)
+        _check(lib.ada_linear_backward(args, code, dt, ws, nbytes, _stream(stream)), "ada_linear_backward")
+    return dx, dw, dbias
+
+
+def ada_glu(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, bias_gate=None, bias_up=None,
+            act: str = "silu", y=None, pre=None, workspace=None, stream=None):
+    """y = act(g) u with g = x w_gate^T + bias_gate and u = x w_up^T + bias_up, in one pass;
+    `pre`, if given, is a pair (g, u) of matrices to receive them for the backward pass."""
+    rows, d_out, d_in = _sizes(x, w_gate)
+    dt, code, lib = _dtype(x), _act(act), _lib.load()
+    px, ldx = _mat(x, rows, d_in, x, "x")
+    pg, ldg = _mat(w_gate, d_out, d_in, x, "w_gate")
+    pu, ldu = _mat(w_up, d_out, d_in, x, "w_up")
+    pbg = _vec(bias_gate, d_out, x, "bias_gate")
+    pbu = _vec(bias_up, d_out, x, "bias_up")
+    gate_pre, up_pre = pre if pre is not None else (None, None)
+    ppg, ldpg = _mat(gate_pre, rows, d_out, x, "gate_pre")
+    ppu, ldpu = _mat(up_pre, rows, d_out, x, "up_pre")
+    if y is not None:
+        py, ldy = _mat(y, rows, d_out, x, "y")
+    _current(x)
+    with _On(stream):
+        if y is None:
+            y = torch.empty((rows, d_out), dtype=x.dtype, device=x.device)
+            py, ldy = y.data_ptr(), d_out
+        ws, nbytes, _keep = _workspace(lib.ada_glu_workspace(rows, d_out, d_in, dt), workspace, x, "ada_glu_workspace")
+        args = AdaGluArgs(px, pg, pu, pbg, pbu, py, ppg, ppu, ldx, ldg, ldu, ldy, ldpg, ldpu, rows, d_out, d_in)
+        _check(lib.ada_glu(args, code, dt, ws, nbytes, _stream(stream)), "ada_glu")
+    return y
+
+
+def ada_glu_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, gate_pre, up_pre,
+                     act: str = "silu", dx=None, dw_gate=None, dw_up=None, dbias_gate=None, dbias_up=None,
+                     want_dx: bool = True, want_dw: bool = True, want_dbias: bool = False, workspace=None,
+                     stream=None):
+    """(dx, dw_gate, dw_up, dbias_gate, dbias_up) of ada_glu, given g and u as it saved them:
+    dg = dy u act'(g), du = dy act(g), dx = dg w_gate + du w_up, dw = d^T x, dbias the sums
+    over rows; None for what is neither passed nor wanted."""
+    rows, d_out, d_in = _sizes(x, w_gate)
+    dt, code, lib = _dtype(x), _act(act), _lib.load()
+    if gate_pre is None or up_pre is None:
+        raise ValueError("gate_pre and up_pre are needed for the slopes")
+    pdy, lddy = _mat(dy, rows, d_out, x, "dy")
+    px, ldx = _mat(x, rows, d_in, x, "x")
+    pg, ldg = _mat(w_gate, d_out, d_in, x, "w_gate")
+    pu, ldu = _mat(w_up, d_out, d_in, x, "w_up")
+    ppg, ldpg = _mat(gate_pre, rows, d_out, x, "gate_pre")
+    ppu, ldpu = _mat(up_pre, rows, d_out, x, "up_pre")
+    _mat(dx, rows, d_in, x, "dx")
+    _mat(dw_gate, d_out, d_in, x, "dw_gate")
+    _mat(dw_up, d_out, d_in, x, "dw_up")
+    _vec(dbias_gate, d_out, x, "dbias_gate")
+    _vec(dbias_up, d_out, x, "dbias_up")
+    _current(x)
+
+    def made(t, want, *shape):
+        return torch.empty(shape, dtype=x.dtype, device=x.device) if t is None and want else t
+
+    with _On(stream):
+        dx = made(dx, want_dx, rows, d_in)
+        dw_gate, dw_up = made(dw_gate, want_dw, d_out, d_in), made(dw_up, want_dw, d_out, d_in)
+        dbias_gate, dbias_up = made(dbias_gate, want_dbias, d_out), made(dbias_up, want_dbias, d_out)
+        pdx, lddx = _mat(dx, rows, d_in, x, "dx")
+        pdg, lddg = _mat(dw_gate, d_out, d_in, x, "dw_gate")
+        pdu, lddu = _mat(dw_up, d_out, d_in, x, "dw_up")
+        pbg = _vec(dbias_gate, d_out, x, "dbias_gate")
+        pbu = _vec(dbias_up, d_out, x, "dbias_up")
+        ws, nbytes, _keep = _workspace(lib.ada_glu_backward_workspace(rows, d_out, d_in, code, dt), workspace, x,
+                                       "ada_glu_backward_workspace")
+        args = AdaGluGradArgs(pdy, px, pg, pu, ppg, ppu, pdx, pdg, pdu, pbg, pbu, lddy, ldx, ldg, ldu, ldpg, ldpu,
+                              lddx, lddg, lddu, rows, d_out, d_in)
+        _check(lib.ada_glu_backward(args, code, dt, ws, nbytes, _stream(stream)), "ada_glu_backward")
+    return dx, dw_gate, dw_up, dbias_gate, dbias_up

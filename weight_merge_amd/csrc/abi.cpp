@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "launch.h"
+#include "linear.h"
 
 #ifndef ADA_LONG_TILE_GROUP
 #define ADA_LONG_TILE_GROUP 8
@@ -186,6 +187,72 @@ int prepare_lora_layer(const ada_lora_proj* projs, int32_t n_proj, int32_t E, in
   p.scale = scale;
   p.nb = 1;
   ws_bytes = ws * 4;
+  return ADA_OK;
+}
+
+// ---- argument checks of the linear and gated products --------------------------------
+constexpr int64_t kMaxLd = int64_t(1) << 36;
+
+// A matrix argument of `rows` x `cols` elements: its checks, and its place in memory for
+// the overlap rules.
+struct MatArg {
+  const void* p;
+  int64_t rows;
+  int64_t cols;
+  int64_t ld;
+  bool out;
+};
+
+int check_mats(const MatArg* m, int n, int esz) {
+  for (int i = 0; i < n; ++i)
+    if (!aligned16(m[i].p)) return ADA_EALIGN;
+  for (int i = 0; i < n; ++i)
+    if (m[i].p != nullptr && (m[i].ld < m[i].cols || m[i].ld > kMaxLd)) return ADA_ESHAPE;
+  for (int i = 0; i < n; ++i)
+    if (m[i].p != nullptr && (m[i].ld * esz) % 16 != 0) return ADA_EALIGN;
+  return ADA_OK;
+}
+
+bool overlaps(const MatArg& a, const MatArg& b, int esz) {
+  if (a.p == nullptr || b.p == nullptr || a.rows == 0 || b.rows == 0) return false;
+  const uint64_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+  const uint64_t a1 = a0 + uint64_t((a.rows - 1) * a.ld + a.cols) * esz;
+  const uint64_t b1 = b0 + uint64_t((b.rows - 1) * b.ld + b.cols) * esz;
+  if (a1 <= b0 || b1 <= a0) return false;
+  if (a.ld != b.ld) return true;
+  // equal strides: column ranges of one buffer's rows, apart unless they meet modulo the stride
+  const uint64_t pitch = uint64_t(a.ld) * esz, wa = uint64_t(a.cols) * esz, wb = uint64_t(b.cols) * esz;
+  const uint64_t off = b0 >= a0 ? (b0 - a0) % pitch : (pitch - (a0 - b0) % pitch) % pitch;
+  return !(off >= wa && off + wb <= pitch);
+}
+
+// Whether an output overlaps any other argument (m[same_a] and m[same_b] may be one matrix).
+bool outputs_overlap(const MatArg* m, int n, int esz, int same_a = -1, int same_b = -1) {
+  for (int i = 0; i < n; ++i)
+    for (int j = i + 1; j < n; ++j) {
+      if (!m[i].out && !m[j].out) continue;
+      if (i == same_a && j == same_b && m[i].p == m[j].p && m[i].ld == m[j].ld) continue;
+      if (overlaps(m[i], m[j], esz)) return true;
+    }
+  return false;
+}
+
+bool act_ok(int32_t act) { return act >= ADA_ACT_NONE && act <= ADA_ACT_GELU_TANH; }
+
+int check_linear_sizes(int64_t rows, int32_t d_out, int32_t d_in, int32_t dtype) {
+  if (!dtype_ok(dtype)) return ADA_EDTYPE;
+  if (rows < 0 || rows > kMaxDim || !dim_ok(d_out) || !dim_ok(d_in)) return ADA_ESHAPE;
+  return ADA_OK;
+}
+
+int check_workspace(const void* ws, int64_t have, int64_t need, const MatArg* m, int n, int esz) {
+  if (!aligned16(ws)) return ADA_EALIGN;
+  if (need == 0) return ADA_OK;
+  if (ws == nullptr) return ADA_EINVAL;
+  if (have < need) return ADA_ESHAPE;
+  const MatArg w{ws, 1, (need + esz - 1) / esz, (need + esz - 1) / esz, true};
+  for (int i = 0; i < n; ++i)
+    if (overlaps(w, m[i], esz)) return ADA_EINVAL;
   return ADA_OK;
 }
 
@@ -504,6 +571,183 @@ int ada_lora_batch(const ada_lora_proj* projs, int32_t n_proj, int32_t nb, int32
   p.nb = nb;
   const hipError_t e = ada::launch_lora_batch(p, static_cast<int>(dot_rows), static_cast<int>(out_rows), dtype,
                                               static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? ADA_OK : ADA_EHIP;
+}
+
+int64_t ada_linear_workspace(int64_t rows, int32_t d_out, int32_t d_in, int32_t dtype) {
+  if (int st = check_linear_sizes(rows, d_out, d_in, dtype); st != ADA_OK) return st;
+  return ada::linear_workspace(rows, d_out, d_in, 0, dtype);
+}
+
+int64_t ada_glu_workspace(int64_t rows, int32_t d_out, int32_t d_in, int32_t dtype) {
+  if (int st = check_linear_sizes(rows, d_out, d_in, dtype); st != ADA_OK) return st;
+  return ada::linear_workspace(rows, d_out, d_in, 1, dtype);
+}
+
+int64_t ada_linear_backward_workspace(int64_t rows, int32_t d_out, int32_t d_in, int32_t act, int32_t dtype) {
+  if (int st = check_linear_sizes(rows, d_out, d_in, dtype); st != ADA_OK) return st;
+  if (!act_ok(act)) return ADA_EINVAL;
+  return ada::linear_grad_workspace(rows, d_out, d_in, act, 0, dtype);
+}
+
+int64_t ada_glu_backward_workspace(int64_t rows, int32_t d_out, int32_t d_in, int32_t act, int32_t dtype) {
+  if (int st = check_linear_sizes(rows, d_out, d_in, dtype); st != ADA_OK) return st;
+  if (!act_ok(act)) return ADA_EINVAL;
+  return ada::linear_grad_workspace(rows, d_out, d_in, act, 1, dtype);
+}
+
+int ada_linear(const ada_linear_args* q, int32_t act, int32_t dtype, void* workspace, int64_t workspace_bytes,
+               void* stream) {
+  if (q == nullptr || q->w == nullptr || !act_ok(act)) return ADA_EINVAL;
+  if (int st = check_linear_sizes(q->rows, q->d_out, q->d_in, dtype); st != ADA_OK) return st;
+  if (q->rows > 0 && (q->x == nullptr || q->y == nullptr)) return ADA_EINVAL;
+  const int esz = dtype == ADA_BF16 ? 2 : 4;
+  const int64_t rows = q->rows, n = q->d_out, k = q->d_in;
+  const MatArg m[] = {{q->x, rows, k, q->ld_x, false},          {q->w, n, k, q->ld_w, false},
+                      {q->bias, 1, n, n, false},                {q->residual, rows, n, q->ld_res, false},
+                      {q->y, rows, n, q->ld_y, true},           {q->pre, rows, n, q->ld_pre, true}};
+  if (int st = check_mats(m, 6, esz); st != ADA_OK) return st;
+  if (outputs_overlap(m, 6, esz, 3, 4)) return ADA_EINVAL;
+  const int64_t need = ada::linear_workspace(rows, q->d_out, q->d_in, 0, dtype);
+  if (int st = check_workspace(workspace, workspace_bytes, need, m, 6, esz); st != ADA_OK) return st;
+  ada::LinearParams p{};
+  p.x = {q->x, q->ld_x};
+  p.w[0] = {q->w, q->ld_w};
+  p.bias[0] = q->bias;
+  p.res = {q->residual, q->ld_res};
+  p.y = {q->y, q->ld_y};
+  p.pre[0] = {q->pre, q->ld_pre};
+  p.rows = rows;
+  p.d_out = q->d_out;
+  p.d_in = q->d_in;
+  p.act = act;
+  const hipError_t e = ada::launch_linear(p, dtype, workspace, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? ADA_OK : ADA_EHIP;
+}
+
+int ada_glu(const ada_glu_args* q, int32_t act, int32_t dtype, void* workspace, int64_t workspace_bytes,
+            void* stream) {
+  if (q == nullptr || q->w_gate == nullptr || q->w_up == nullptr || !act_ok(act)) return ADA_EINVAL;
+  if (int st = check_linear_sizes(q->rows, q->d_out, q->d_in, dtype); st != ADA_OK) return st;
+  if (q->rows > 0 && (q->x == nullptr || q->y == nullptr)) return ADA_EINVAL;
+  const int esz = dtype == ADA_BF16 ? 2 : 4;
+  const int64_t rows = q->rows, n = q->d_out, k = q->d_in;
+  const MatArg m[] = {{q->x, rows, k, q->ld_x, false},
+                      {q->w_gate, n, k, q->ld_w_gate, false},
+                      {q->w_up, n, k, q->ld_w_up, false},
+                      {q->bias_gate, 1, n, n, false},
+                      {q->bias_up, 1, n, n, false},
+                      {q->y, rows, n, q->ld_y, true},
+                      {q->gate_pre, rows, n, q->ld_gate_pre, true},
+                      {q->up_pre, rows, n, q->ld_up_pre, true}};
+  if (int st = check_mats(m, 8, esz); st != ADA_OK) return st;
+  if (outputs_overlap(m, 8, esz)) return ADA_EINVAL;
+  const int64_t need = ada::linear_workspace(rows, q->d_out, q->d_in, 1, dtype);
+  if (int st = check_workspace(workspace, workspace_bytes, need, m, 8, esz); st != ADA_OK) return st;
+  ada::LinearParams p{};
+  p.x = {q->x, q->ld_x};
+  p.w[0] = {q->w_gate, q->ld_w_gate};
+  p.w[1] = {q->w_up, q->ld_w_up};
+  p.bias[0] = q->bias_gate;
+  p.bias[1] = q->bias_up;
+  p.y = {q->y, q->ld_y};
+  p.pre[0] = {q->gate_pre, q->ld_gate_pre};
+  p.pre[1] = {q->up_pre, q->ld_up_pre};
+  p.rows = rows;
+  p.d_out = q->d_out;
+  p.d_in = q->d_in;
+  p.act = act;
+  p.gated = 1;
+  const hipError_t e = ada::launch_linear(p, dtype, workspace, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? ADA_OK : ADA_EHIP;
+}
+
+int ada_linear_backward(const ada_linear_grad_args* q, int32_t act, int32_t dtype, void* workspace,
+                        int64_t workspace_bytes, void* stream) {
+  if (q == nullptr || !act_ok(act)) return ADA_EINVAL;
+  if (int st = check_linear_sizes(q->rows, q->d_out, q->d_in, dtype); st != ADA_OK) return st;
+  const int64_t rows = q->rows, n = q->d_out, k = q->d_in;
+  if (q->dw == nullptr && q->dbias == nullptr && q->dx == nullptr && rows > 0) return ADA_EINVAL;
+  // what is not read is not looked at either: pre without an activation, x without dw, w without dx
+  const void* pre = act == ADA_ACT_NONE ? nullptr : q->pre;
+  const void* x = q->dw != nullptr ? q->x : nullptr;
+  const void* w = q->dx != nullptr ? q->w : nullptr;
+  if (rows > 0 && (q->dy == nullptr || (act != ADA_ACT_NONE && pre == nullptr) || (q->dw != nullptr && x == nullptr) ||
+                   (q->dx != nullptr && w == nullptr)))
+    return ADA_EINVAL;
+  const int esz = dtype == ADA_BF16 ? 2 : 4;
+  const MatArg m[] = {{q->dy, rows, n, q->ld_dy, false}, {x, rows, k, q->ld_x, false},
+                      {w, n, k, q->ld_w, false},         {pre, rows, n, q->ld_pre, false},
+                      {q->dx, rows, k, q->ld_dx, true},  {q->dw, n, k, q->ld_dw, true},
+                      {q->dbias, 1, n, n, true}};
+  if (int st = check_mats(m, 7, esz); st != ADA_OK) return st;
+  if (outputs_overlap(m, 7, esz)) return ADA_EINVAL;
+  const int64_t need = ada::linear_grad_workspace(rows, q->d_out, q->d_in, act, 0, dtype);
+  if (int st = check_workspace(workspace, workspace_bytes, need, m, 7, esz); st != ADA_OK) return st;
+  ada::LinearGradParams p{};
+  p.dy = {q->dy, q->ld_dy};
+  p.x = {x, q->ld_x};
+  p.w[0] = {w, q->ld_w};
+  p.pre[0] = {pre, q->ld_pre};
+  p.dx = {q->dx, q->ld_dx};
+  p.dw[0] = {q->dw, q->ld_dw};
+  p.dbias[0] = q->dbias;
+  p.rows = rows;
+  p.d_out = q->d_out;
+  p.d_in = q->d_in;
+  p.act = act;
+  const hipError_t e = ada::launch_linear_grad(p, dtype, workspace, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? ADA_OK : ADA_EHIP;
+}
+
+int ada_glu_backward(const ada_glu_grad_args* q, int32_t act, int32_t dtype, void* workspace, int64_t workspace_bytes,
+                     void* stream) {
+  if (q == nullptr || !act_ok(act)) return ADA_EINVAL;
+  if (int st = check_linear_sizes(q->rows, q->d_out, q->d_in, dtype); st != ADA_OK) return st;
+  const int64_t rows = q->rows, n = q->d_out, k = q->d_in;
+  const bool want_dw = q->dw_gate != nullptr || q->dw_up != nullptr;
+  if (!want_dw && q->dbias_gate == nullptr && q->dbias_up == nullptr && q->dx == nullptr && rows > 0)
+    return ADA_EINVAL;
+  const void* x = want_dw ? q->x : nullptr;
+  const void* wg = q->dx != nullptr ? q->w_gate : nullptr;
+  const void* wu = q->dx != nullptr ? q->w_up : nullptr;
+  if (rows > 0 && (q->dy == nullptr || q->gate_pre == nullptr || q->up_pre == nullptr || (want_dw && x == nullptr) ||
+                   (q->dx != nullptr && (wg == nullptr || wu == nullptr))))
+    return ADA_EINVAL;
+  const int esz = dtype == ADA_BF16 ? 2 : 4;
+  const MatArg m[] = {{q->dy, rows, n, q->ld_dy, false},
+                      {x, rows, k, q->ld_x, false},
+                      {wg, n, k, q->ld_w_gate, false},
+                      {wu, n, k, q->ld_w_up, false},
+                      {q->gate_pre, rows, n, q->ld_gate_pre, false},
+                      {q->up_pre, rows, n, q->ld_up_pre, false},
+                      {q->dx, rows, k, q->ld_dx, true},
+                      {q->dw_gate, n, k, q->ld_dw_gate, true},
+                      {q->dw_up, n, k, q->ld_dw_up, true},
+                      {q->dbias_gate, 1, n, n, true},
+                      {q->dbias_up, 1, n, n, true}};
+  if (int st = check_mats(m, 11, esz); st != ADA_OK) return st;
+  if (outputs_overlap(m, 11, esz)) return ADA_EINVAL;
+  const int64_t need = ada::linear_grad_workspace(rows, q->d_out, q->d_in, act, 1, dtype);
+  if (int st = check_workspace(workspace, workspace_bytes, need, m, 11, esz); st != ADA_OK) return st;
+  ada::LinearGradParams p{};
+  p.dy = {q->dy, q->ld_dy};
+  p.x = {x, q->ld_x};
+  p.w[0] = {wg, q->ld_w_gate};
+  p.w[1] = {wu, q->ld_w_up};
+  p.pre[0] = {q->gate_pre, q->ld_gate_pre};
+  p.pre[1] = {q->up_pre, q->ld_up_pre};
+  p.dx = {q->dx, q->ld_dx};
+  p.dw[0] = {q->dw_gate, q->ld_dw_gate};
+  p.dw[1] = {q->dw_up, q->ld_dw_up};
+  p.dbias[0] = q->dbias_gate;
+  p.dbias[1] = q->dbias_up;
+  p.rows = rows;
+  p.d_out = q->d_out;
+  p.d_in = q->d_in;
+  p.act = act;
+  p.gated = 1;
+  const hipError_t e = ada::launch_linear_grad(p, dtype, workspace, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? ADA_OK : ADA_EHIP;
 }
 
