@@ -278,7 +278,7 @@ typedef enum {
  *   - Matrices are row-major with a row stride ld (elements, at least the row's length, at
  *     most 2^36): row i of a matrix of c columns is elements [i ld, i ld + c).  Every
  *     pointer and every row stride is 16-byte aligned.
- *   - rows: 0 <= rows <= 2^22, odd ones included.  With rows = 0 the matrices of `rows`
+ *   - No matrix has more than 2^35 elements.  rows: 0 <= rows <= 2^22, odd ones included.  With rows = 0 the matrices of `rows`
  *     rows may be NULL; the forward calls then write nothing, and the gradients summed
  *     over rows are zeros.
  *   - An output may not overlap an input or another output, except that y may be the

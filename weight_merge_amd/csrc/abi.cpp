@@ -192,6 +192,7 @@ int prepare_lora_layer(const ada_lora_proj* projs, int32_t n_proj, int32_t E, in
 
 // ---- argument checks of the linear and gated products --------------------------------
 constexpr int64_t kMaxLd = int64_t(1) << 36;
+constexpr int64_t kMaxMat = int64_t(1) << 35;  // elements of x, y or a weight matrix
 
 // A matrix argument of `rows` x `cols` elements: its checks, and its place in memory for
 // the overlap rules.
@@ -242,6 +243,8 @@ bool act_ok(int32_t act) { return act >= ADA_ACT_NONE && act <= ADA_ACT_GELU_TAN
 int check_linear_sizes(int64_t rows, int32_t d_out, int32_t d_in, int32_t dtype) {
   if (!dtype_ok(dtype)) return ADA_EDTYPE;
   if (rows < 0 || rows > kMaxDim || !dim_ok(d_out) || !dim_ok(d_in)) return ADA_ESHAPE;
+  // grids of 64 x 64 tiles of any of the matrices stay under 2^32 threads
+  if (rows * d_out > kMaxMat || rows * d_in > kMaxMat || int64_t(d_out) * d_in > kMaxMat) return ADA_ESHAPE;
   return ADA_OK;
 }
 
