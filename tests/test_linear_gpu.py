@@ -372,3 +372,25 @@ def test_large_values(dtype):
         rz = OL.linear_backward(H.f64(dy), H.f64(x), H.f64(w), H.f64(pre), act)[3]
         b = H.grad_bounds([rz], [H.slope_error(H.f64(dy), H.f64(pre), act)], H.f64(x), [H.f64(w)], dtype)[2]
         H.assert_within(db, rz.sum(axis=0), b, act)
+
+
+# sizes of the largest tile (at least 192 tiles of 256 x 256), ragged in every dimension
+LARGE = [(3850, 3304, 200), (2047, 6664, 1096)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ("fp32", "bf16"))
+@pytest.mark.parametrize("shape", LARGE, ids=lambda s: "x".join(map(str, s)))
+def test_large_shapes(shape, dtype):
+    rows, d_out, d_in = shape
+    check_linear(rows, d_out, d_in, dtype, "silu", pad=8, seed=21)
+    check_glu(rows, d_out // 2 // 8 * 8, d_in, dtype, "silu", seed=22)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ("fp32", "bf16"))
+@pytest.mark.parametrize("shape", [(3850, 200, 3304), (200, 3848, 3304)], ids=lambda s: "x".join(map(str, s)))
+def test_large_gradients(shape, dtype):
+    """Many tiles of dx (depth d_out) in one shape, of dW (depth rows) in the other."""
+    check_linear_backward(*shape, dtype, "silu", seed=23)
+    check_glu_backward(*shape, dtype, "silu", seed=24)

@@ -7,12 +7,12 @@
 //
 // Every product is D(i, j) = sum_k P(i, k) Q(j, k) on the matrix instructions with fp32
 // sums and both operands read along k: x and W of the forward pass as they are, W of dx and
-// dz and x of dW from transposed copies in the workspace.  Matrix instruction layout (16 x
-// 16 tile): lane l = 16 q + c supplies Q(c, k) as the row operand and P(c, k) as the column
-// operand for its k slice, and receives D(i = c, j = 4 q .. 4 q + 3), four consecutive
-// columns of an output row.  A 16-byte vector per lane feeds one 16x16x32 instruction in
-// bf16 and four 16x16x4 ones in fp32 (the instruction's k order is free as long as both
-// operands share it).
+// dz and x of dW from transposed copies in the workspace.  Matrix instruction layout (32 x
+// 32 tile): lane l = 32 q + c supplies Q(c, k) as the row operand and P(c, k) as the column
+// operand for its k slice, and receives D(i = c, j = 8 g + 4 q + e) in register 4 g + e:
+// groups of four consecutive columns of an output row.  A 16-byte vector per lane feeds one
+// 32x32x16 instruction in bf16 and four 32x32x2 ones in fp32 (the instruction's k order is
+// free as long as both operands share it).
 #include "linear.h"
 
 #include "adafuse.h"
@@ -21,6 +21,7 @@ namespace ada {
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
@@ -41,17 +42,31 @@ __device__ __forceinline__ uint16_t from_f32<uint16_t>(float v) {  // to nearest
   return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
 }
 
+// Eight consecutive elements (16-byte aligned) as floats, and back.
 template <typename T>
-__device__ __forceinline__ void load4(const T* p, float* v) {
+struct alignas(16) Vec16 {
+  T e[16 / sizeof(T)];
+};
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+  constexpr int VEC = 16 / sizeof(T);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = to_f32<T>(p[i]);
+  for (int i = 0; i < 8; i += VEC) {
+    const Vec16<T> d = *reinterpret_cast<const Vec16<T>*>(p + i);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[i + e] = to_f32<T>(d.e[e]);
+  }
 }
 template <typename T>
-__device__ __forceinline__ void store4(T* p, const float* v) {
-  struct alignas(4 * sizeof(T)) Quad { T e[4]; } q;
+__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
+  constexpr int VEC = 16 / sizeof(T);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) q.e[i] = from_f32<T>(v[i]);
-  *reinterpret_cast<Quad*>(p) = q;
+  for (int i = 0; i < 8; i += VEC) {
+    Vec16<T> d;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) d.e[e] = from_f32<T>(v[i + e]);
+    *reinterpret_cast<Vec16<T>*>(p + i) = d;
+  }
 }
 
 // ---- activations: value and slope in fp32 --------------------------------------------
@@ -68,6 +83,22 @@ __device__ __forceinline__ float act_value(float z, int act) {
     case ADA_ACT_GELU_TANH: return 0.5f * z * (1.f + tanhf(kSqrt2OverPi * (z + kCubic * z * z * z)));
     default: return z;
   }
+}
+
+// One choice of the activation for eight values.
+__device__ __forceinline__ void act_values(float (&z)[8], int act) {
+#define ADA_EACH(a)                                         \
+  case a:                                                   \
+    _Pragma("unroll") for (int e = 0; e < 8; ++e) z[e] = act_value(z[e], a); \
+    break;
+  switch (act) {
+    ADA_EACH(ADA_ACT_RELU)
+    ADA_EACH(ADA_ACT_SILU)
+    ADA_EACH(ADA_ACT_GELU)
+    ADA_EACH(ADA_ACT_GELU_TANH)
+    default: break;
+  }
+#undef ADA_EACH
 }
 
 __device__ __forceinline__ float act_slope(float z, int act) {
@@ -110,38 +141,45 @@ struct GemmParams {
   int32_t tiles_n;
 };
 
-// y, pre of four consecutive columns n of row m, from the sums without the bias.
+// y, pre of eight consecutive columns n of row m, from the sums without the bias.
 template <typename T, bool GATED>
-__device__ __forceinline__ void finish4(const GemmParams& a, int64_t m, int64_t n, const f32x4 (&acc)[GATED ? 2 : 1]) {
-  constexpr int NQ = GATED ? 2 : 1;
-  float z[NQ][4], o[4];
+__device__ __forceinline__ void finish8(const GemmParams& a, int64_t m, int64_t n, float (&z)[GATED ? 2 : 1][8]) {
 #pragma unroll
-  for (int h = 0; h < NQ; ++h) {
-    float b[4] = {0.f, 0.f, 0.f, 0.f};
-    if (a.bias[h] != nullptr) load4(static_cast<const T*>(a.bias[h]) + n, b);
+  for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+    if (a.bias[h] != nullptr) {
+      float b[8];
+      load8(static_cast<const T*>(a.bias[h]) + n, b);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) z[h][e] = acc[h][e] + b[e];
-    if (a.pre[h].p != nullptr) store4(static_cast<T*>(a.pre[h].p) + m * a.pre[h].ld + n, z[h]);
+      for (int e = 0; e < 8; ++e) z[h][e] += b[e];
+    }
+    if (a.pre[h].p != nullptr) store8(static_cast<T*>(a.pre[h].p) + m * a.pre[h].ld + n, z[h]);
   }
+  act_values(z[0], a.act);
+  if constexpr (GATED) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    o[e] = act_value(z[0][e], a.act);
-    if constexpr (GATED) o[e] *= z[1][e];
+    for (int e = 0; e < 8; ++e) z[0][e] *= z[1][e];
   }
   if (a.res.p != nullptr) {
-    float r[4];
-    load4(static_cast<const T*>(a.res.p) + m * a.res.ld + n, r);
+    float r[8];
+    load8(static_cast<const T*>(a.res.p) + m * a.res.ld + n, r);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] += r[e];
+    for (int e = 0; e < 8; ++e) z[0][e] += r[e];
   }
   const int second = m >= a.row_split;
-  store4(static_cast<T*>(a.y[second].p) + (m - (second ? a.row_split : 0)) * a.y[second].ld + n, o);
+  store8(static_cast<T*>(a.y[second].p) + (m - (second ? a.row_split : 0)) * a.y[second].ld + n, z[0]);
 }
 
 // Sixteen bytes per lane from global memory to LDS, lane l's at lds + 16 l (lds is the same
 // in every lane of the wave).
 __device__ __forceinline__ void copy_to_lds(const unsigned char* g, unsigned char* lds) {
   __builtin_amdgcn_global_load_lds((const ADA_GLOBAL void*)g, (ADA_LDS void*)lds, 16, 0, 0);
+}
+
+// Order the LDS accesses of one wave: what its lanes wrote before is what they read after.
+__device__ __forceinline__ void lds_wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // Wait until at most N of the wave's copies to LDS are in flight and all its LDS reads and
@@ -152,44 +190,50 @@ __device__ __forceinline__ void copies_then_barrier() {
 }
 
 template <typename T>
-__device__ __forceinline__ f32x4 mfma16(u32x4 q, u32x4 p, f32x4 acc) {
+__device__ __forceinline__ f32x16 mfma32(u32x4 q, u32x4 p, f32x16 acc) {
   if constexpr (sizeof(T) == 2) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, q), __builtin_bit_cast(bf16x8, p), acc,
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, q), __builtin_bit_cast(bf16x8, p), acc,
                                                    0, 0, 0);
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(q[j]), __uint_as_float(p[j]), acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(q[j]), __uint_as_float(p[j]), acc, 0, 0, 0);
     return acc;
   }
 }
 
 // A tile of BM x BN outputs (gated: BN counts the columns of both products, 16 of the gate's
 // next to 16 of the up projection's, so a wave holds both for its columns) by WM x WN waves.
-// A step stages 128 bytes of k of every operand row (BM + BN rows) in LDS by direct copies,
-// S buffers deep; vector v of row r lies at r * 128 + 16 (v ^ (r >> 1 & 7)), which spreads
-// the 16 rows of a fragment read over all banks.  The depth's last part of a step (depth is
-// a multiple of 16 bytes) goes through registers, zeros behind its end.  Rows past an
-// operand's end repeat its last row and are not stored.
-template <typename T, int BM_, int BN_, int WM_, int WN_, int S_, int WAVES_PER_SIMD_>
+// A step is 128 bytes of k.  One operand's rows of one step are a unit; units go to LDS by
+// direct copies into a ring of U slots: 2 t holds P of step t, 2 t + 1 holds Q.  Vector v of a
+// staged row r lies at r * 128 + 16 (v ^ (r >> 1 & 7)), which spreads the rows of a fragment
+// read over all banks.  The depth's last part of a step (depth is a multiple of 16 bytes) goes
+// through registers, zeros behind its end.  Rows past an operand's end repeat its last row and
+// are not stored.
+template <int BM_, int BN_, int U_, int WAVES_PER_SIMD_>
 struct TileConfig {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_, waves = WM_ * WN_;
+  static constexpr int BM = BM_, BN = BN_, WM = 2, WN = 2, U = U_, waves = WM * WN;
   static constexpr int threads = 64 * waves, per_simd = WAVES_PER_SIMD_;
-  static constexpr int rows = BM + BN;           // staged rows per step
-  static constexpr int copies = rows / 8 / waves;  // direct copies per wave and step
-  static constexpr int lds = S * rows * 128;
-  static_assert(rows % (8 * waves) == 0 && BM % 8 == 0, "a copy holds rows of one operand");
+  static constexpr int copies_p = BM / 8 / waves, copies_q = BN / 8 / waves;  // direct copies per wave and unit
+  static constexpr int win_pitch = BN / WN + 4;       // floats of a row of a wave's epilogue window
+  static constexpr int window = 32 * win_pitch * 4;   // its bytes
+  static constexpr int ring = BM == BN ? U * BM * 128 : U / 2 * (BM + BN) * 128;
+  static constexpr int lds = ring > waves * window ? ring : waves * window;
+  // where slot s lies (an even ring keeps P in even slots)
+  __device__ static int slot(int s) { return BM == BN ? s * BM * 128 : (s >> 1) * (BM + BN) * 128 + (s & 1) * BM * 128; }
+  // copies of n units from a P unit on
+  static constexpr int copies(int n) { return (n + 1) / 2 * copies_p + n / 2 * copies_q; }
+  static_assert((BM == BN || U % 2 == 0) && U >= 5 && lds <= 160 * 1024 && copies(U - 3) < 64, "ring");
 };
 
 template <typename T, typename C, bool GATED, bool PARTIAL>
 __global__ void __launch_bounds__(C::threads, C::per_simd) gemm_kernel(GemmParams a) {
   constexpr int NQ = GATED ? 2 : 1;
-  constexpr int FM = C::BM / C::WM / 16, FN = C::BN / C::WN / 16;
+  constexpr int FM = C::BM / C::WM / 32, FN = C::BN / C::WN / 32;
   constexpr int CC = C::BN / NQ;  // output columns of a tile
-  static_assert(!GATED || FN % 2 == 0, "a wave holds both products of its columns");
   __shared__ __attribute__((aligned(16))) unsigned char lds[C::lds];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c = lane & 15, q = lane >> 4;
+  const int c = lane & 31, q = lane >> 5;
 
   // consecutive workgroups go to the 8 XCDs in turn: give each XCD a run of tiles, walked
   // down groups of 8 row bands so that its L2 serves a compact block of the output
@@ -210,92 +254,158 @@ __global__ void __launch_bounds__(C::threads, C::per_simd) gemm_kernel(GemmParam
   const int tail = step0 + steps == all ? static_cast<int>(bytes & 127) : 0;  // bytes of the last step if short
   const int full = steps - (tail != 0);
 
-  // where this lane reads: copy j of the wave fills staged rows 8 (wave copies + j) + lane / 8
-  const unsigned char* src[C::copies];
+  // With one row band no W is shared between workgroups: each starts elsewhere in k, or all of
+  // them would read the same few memory channels at a time.
+  const int turn = a.tiles_m == 1 && full > 0 ? static_cast<int>(blockIdx.x) * 5 % full : 0;
+
+  // where this lane reads: copy j of the wave fills rows 8 (wave copies + j) + lane / 8 of a unit
+  constexpr int kCopies[2] = {C::copies_p, C::copies_q};
+  constexpr int kMost = C::copies_p > C::copies_q ? C::copies_p : C::copies_q;
+  const unsigned char* src[2][kMost];
 #pragma unroll
-  for (int j = 0; j < C::copies; ++j) {
-    const int r = 8 * (wave * C::copies + j) + (lane >> 3);
-    const int v = (lane & 7) ^ ((r >> 1) & 7);
-    const MatIn* m;
-    int64_t i, n;
-    if (r < C::BM) {
-      m = &a.p;
-      i = row0 + r;
-      n = a.rows;
-    } else {
-      const int rq = r - C::BM;
-      m = &a.q[GATED ? (rq >> 4) & 1 : 0];
-      i = col0 + (GATED ? (rq >> 5) * 16 + (rq & 15) : rq);
-      n = a.cols;
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < kCopies[h]; ++j) {
+      const int r = 8 * (wave * kCopies[h] + j) + (lane >> 3);
+      const MatIn& m = h == 0 ? a.p : a.q[GATED ? (r >> 4) & 1 : 0];
+      const int64_t at = h == 0 ? row0 + r : col0 + (GATED ? (r >> 5) * 16 + (r & 15) : r);
+      const int64_t n = h == 0 ? a.rows : a.cols;
+      src[h][j] = static_cast<const unsigned char*>(m.p) + (at < n ? at : n - 1) * m.ld * int64_t(sizeof(T)) +
+                  int64_t(step0 + turn) * 128 + ((lane & 7) ^ ((r >> 1) & 7)) * 16;
     }
-    if (i >= n) i = n - 1;
-    src[j] = static_cast<const unsigned char*>(m->p) + i * m->ld * int64_t(sizeof(T)) + int64_t(step0) * 128 + v * 16;
-  }
-  auto stage = [&](int t) {
-    const int at = (t % C::S) * C::rows * 128 + wave * C::copies * 1024;
-    if (t < full) {
+  auto advance = [&](int t) { return t == full - 1 - turn ? 128 - full * 128 : 128; };  // bytes from step t to t + 1
+  auto copy_unit = [&](int t, int slot, int h) {
+    unsigned char* at = lds + C::slot(slot) + wave * kCopies[h] * 1024;
 #pragma unroll
-      for (int j = 0; j < C::copies; ++j) {
-        copy_to_lds(src[j], lds + at + j * 1024);
-        src[j] += 128;
-      }
-    } else {
+    for (int j = 0; j < kCopies[h]; ++j) {
+      copy_to_lds(src[h][j], at + j * 1024);
+      src[h][j] += advance(t);
+    }
+  };
+  auto copy_unit_or_tail = [&](int u, int slot, int h) {
+    if ((u >> 1) < full) {
+      copy_unit(u >> 1, slot, h);
+    } else if ((u >> 1) < steps) {
+      unsigned char* at = lds + C::slot(slot) + wave * kCopies[h] * 1024;
 #pragma unroll
-      for (int j = 0; j < C::copies; ++j) {
-        const int r = 8 * (wave * C::copies + j) + (lane >> 3);
-        const int v = (lane & 7) ^ ((r >> 1) & 7);
+      for (int j = 0; j < kCopies[h]; ++j) {
+        const int r = 8 * (wave * kCopies[h] + j) + (lane >> 3);
         u32x4 d = {0, 0, 0, 0};
-        if (v * 16 < tail) d = *reinterpret_cast<const u32x4*>(src[j]);
-        *reinterpret_cast<u32x4*>(lds + at + j * 1024 + lane * 16) = d;
+        if (((lane & 7) ^ ((r >> 1) & 7)) * 16 < tail) d = *reinterpret_cast<const u32x4*>(src[h][j] + (full - turn) * 128);
+        *reinterpret_cast<u32x4*>(at + j * 1024 + lane * 16) = d;
       }
     }
   };
 
-  f32x4 acc[FM][FN] = {};
+  f32x16 acc[FM][FN] = {};
   const int wm = wave / C::WN, wn = wave % C::WN;
-  const int rd = 16 * (q ^ (c >> 1));  // vectors 4 .. 7 of a row lie at rd ^ 64
-  const int rp = (wm * FM * 16 + c) * 128, rq = (C::BM + wn * FN * 16 + c) * 128;
+  const int rd = 16 * (q ^ ((c >> 1) & 7));  // vector 2 s + q of the row lies at rd ^ 32 s
+  const int rp = (wm * FM * 32 + c) * 128, rq = (wn * FN * 32 + c) * 128;
+  // A step has two halves; the fragments of one are read while the other is multiplied.  One
+  // barrier a step, between them: behind it every wave has read step t's units, and step t + 1's
+  // are complete for every wave.  Unit 2 t + U takes unit 2 t's slot from there on, unit
+  // 2 t + U + 1 the next one in the first half of step t + 1: the copies spread evenly over
+  // the multiplications, and the last of a step's own has half a step to arrive.
+  u32x4 p0[2][FM], q0[2][FN], p1[2][FM], q1[2][FN];
+  auto read = [&](int slot_p, int slot_q, int half, u32x4 (&pv)[2][FM], u32x4 (&qv)[2][FN]) {
 #pragma unroll
-  for (int t = 0; t < C::S - 1; ++t)
-    if (t < steps) stage(t);
-  for (int t = 0; t < steps; ++t) {
-    if (t + C::S - 2 < full)
-      copies_then_barrier<(C::S - 2) * C::copies>();
-    else
-      copies_then_barrier<0>();
-    if (t + C::S - 1 < steps) stage(t + C::S - 1);
-    const unsigned char* buf = lds + (t % C::S) * C::rows * 128;
+    for (int s = 0; s < 2; ++s) {
+      const int v = rd ^ (half * 64 + s * 32);
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      u32x4 pv[FM], qv[FN];
-#pragma unroll
-      for (int j = 0; j < FN; ++j) qv[j] = *reinterpret_cast<const u32x4*>(buf + rq + (rd ^ (kk * 64)) + j * 2048);
-#pragma unroll
-      for (int i = 0; i < FM; ++i) pv[i] = *reinterpret_cast<const u32x4*>(buf + rp + (rd ^ (kk * 64)) + i * 2048);
+      for (int j = 0; j < FN; ++j)
+        qv[s][j] = *reinterpret_cast<const u32x4*>(lds + C::slot(slot_q) + rq + v + j * 4096);
 #pragma unroll
       for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = mfma16<T>(qv[j], pv[i], acc[i][j]);
+        pv[s][i] = *reinterpret_cast<const u32x4*>(lds + C::slot(slot_p) + rp + v + i * 4096);
     }
+  };
+  // One half multiplied, with the other's fragment reads (over its first three quarters) and one
+  // unit's copies spread evenly between the multiplications, in exactly this order.
+  constexpr int kMults = 2 * FM * FN, kReads = 2 * (FM + FN), kEarly = kMults * 3 / 4 > 0 ? kMults * 3 / 4 : 1;
+  auto half_step = [&](const u32x4 (&pa)[2][FM], const u32x4 (&qa)[2][FN], int slot_p, int slot_q, int half,
+                       u32x4 (&pb)[2][FM], u32x4 (&qb)[2][FN], int step, int slot_copy, int h, bool copies) {
+    unsigned char* at = lds + C::slot(slot_copy) + wave * kCopies[h] * 1024;
+    const int by = advance(step);
+#pragma unroll
+    for (int m = 0; m < kMults; ++m) {
+      const int s = m / (FM * FN), i = m / FN % FM, j = m % FN;
+      acc[i][j] = mfma32<T>(qa[s][j], pa[s][i], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int r = m < kEarly ? kReads * m / kEarly : kReads; r < (m < kEarly ? kReads * (m + 1) / kEarly : kReads); ++r) {
+        const int rs = r / (FM + FN), x = r % (FM + FN), v = rd ^ (half * 64 + rs * 32);
+        if (x < FN)
+          qb[rs][x] = *reinterpret_cast<const u32x4*>(lds + C::slot(slot_q) + rq + v + x * 4096);
+        else
+          pb[rs][x - FN] = *reinterpret_cast<const u32x4*>(lds + C::slot(slot_p) + rp + v + (x - FN) * 4096);
+      }
+      if (copies) {
+#pragma unroll
+        for (int k = kCopies[h] * m / kMults; k < kCopies[h] * (m + 1) / kMults; ++k) {
+          copy_to_lds(src[h][k], at + k * 1024);
+          src[h][k] += by;
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto after = [](int slot, int by) { return slot + by >= C::U ? slot + by - C::U : slot + by; };
+#pragma unroll
+  for (int u = 0; u < C::U - 1; ++u) copy_unit_or_tail(u, u, u & 1);
+  if ((C::U - 2) / 2 < full)
+    copies_then_barrier<C::copies(C::U - 3)>();
+  else
+    copies_then_barrier<0>();
+  read(0, 1, 0, p0, q0);
+  int t = 0, slot = 0;  // slot of unit 2 t
+  for (; (2 * t + C::U) / 2 < full; ++t) {
+    half_step(p0, q0, slot, after(slot, 1), 1, p1, q1, (2 * t + C::U - 1) / 2, after(slot, C::U - 1),
+              (C::U - 1) & 1, true);
+    copies_then_barrier<C::copies(C::U - 4)>();
+    const int next = after(slot, 2);
+    half_step(p1, q1, next, after(next, 1), 0, p0, q0, (2 * t + C::U) / 2, slot, C::U & 1, true);
+    slot = next;
+  }
+  for (; t < steps; ++t) {
+    copy_unit_or_tail(2 * t + C::U - 1, after(slot, C::U - 1), (C::U - 1) & 1);
+    half_step(p0, q0, slot, after(slot, 1), 1, p1, q1, 0, 0, 0, false);
+    copies_then_barrier<0>();
+    copy_unit_or_tail(2 * t + C::U, slot, C::U & 1);
+    slot = after(slot, 2);
+    half_step(p1, q1, slot, after(slot, 1), 0, p0, q0, 0, 0, 0, false);
   }
 
+  // Epilogue: each wave passes its sums, 32 rows at a time, through an LDS window of its own,
+  // so that a lane has eight consecutive columns and a row's lanes write whole lines.
+  __syncthreads();
+  float* win = reinterpret_cast<float*>(lds + wave * C::window);
+  constexpr int CW = FN * 32 / NQ, LANES = CW / 8;  // output columns of the wave, lanes per row
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
-    const int64_t m = row0 + (wm * FM + i) * 16 + c;
-    if (m >= a.rows) continue;
+    lds_wave_sync();
 #pragma unroll
-    for (int j = 0; j < FN; j += NQ) {
-      const int64_t n = col0 + (wn * FN + j) / NQ * 16 + 4 * q;
-      if (n >= a.cols) continue;
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<f32x4*>(win + c * C::win_pitch + 32 * j + 8 * g + 4 * q) =
+            f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+    lds_wave_sync();
+#pragma unroll 1
+    for (int v = lane; v < 32 * LANES; v += 64) {
+      const int r = v / LANES, nc = (v % LANES) * 8;
+      const int64_t m = row0 + (wm * FM + i) * 32 + r, n = col0 + wn * CW + nc;
+      if (m >= a.rows || n >= a.cols) continue;
+      float z[NQ][8];
+#pragma unroll
+      for (int h = 0; h < NQ; ++h) {
+        const float* from = win + r * C::win_pitch + (GATED ? (nc >> 4) * 32 + h * 16 + (nc & 15) : nc);
+        load8(from, z[h]);
+      }
       if constexpr (PARTIAL) {
 #pragma unroll
-        for (int h = 0; h < NQ; ++h)
-          *reinterpret_cast<f32x4*>(a.part + ((int64_t(split) * NQ + h) * a.rows + m) * a.cols + n) = acc[i][j + h];
+        for (int h = 0; h < NQ; ++h) store8(a.part + ((int64_t(split) * NQ + h) * a.rows + m) * a.cols + n, z[h]);
       } else {
-        f32x4 z[NQ];
-#pragma unroll
-        for (int h = 0; h < NQ; ++h) z[h] = acc[i][j + h];
-        finish4<T, GATED>(a, m, n, z);
+        finish8<T, GATED>(a, m, n, z);
       }
     }
   }
@@ -305,36 +415,396 @@ __global__ void __launch_bounds__(C::threads, C::per_simd) gemm_kernel(GemmParam
 template <typename T, bool GATED>
 __global__ void __launch_bounds__(256) join_kernel(GemmParams a) {
   constexpr int NQ = GATED ? 2 : 1;
-  const int64_t quads = a.rows * (a.cols / 4);
+  const int64_t groups = a.rows * (a.cols / 8);
   const int64_t v = blockIdx.x * 256ll + threadIdx.x;
-  if (v >= quads) return;
-  const int64_t m = v / (a.cols / 4);
-  const int64_t n = (v - m * (a.cols / 4)) * 4;
-  f32x4 z[NQ] = {};
-  for (int s = 0; s < a.splits; ++s)
+  if (v >= groups) return;
+  const int64_t m = v / (a.cols / 8);
+  const int64_t n = (v - m * (a.cols / 8)) * 8;
+  float z[NQ][8] = {};
+  constexpr int kAhead = 4;  // parts whose loads are in flight together
+  for (int s0 = 0; s0 < a.splits; s0 += kAhead) {
+    float t[kAhead][NQ][8];
 #pragma unroll
-    for (int h = 0; h < NQ; ++h)
-      z[h] += *reinterpret_cast<const f32x4*>(a.part + ((int64_t(s) * NQ + h) * a.rows + m) * a.cols + n);
-  finish4<T, GATED>(a, m, n, z);
+    for (int s = 0; s < kAhead; ++s)
+#pragma unroll
+      for (int h = 0; h < NQ; ++h) {
+        const int from = s0 + s < a.splits ? s0 + s : s0;
+        load8(a.part + ((int64_t(from) * NQ + h) * a.rows + m) * a.cols + n, t[s][h]);
+      }
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s)
+#pragma unroll
+      for (int h = 0; h < NQ; ++h)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (s0 + s < a.splits) z[h][e] += t[s][h][e];
+  }
+  finish8<T, GATED>(a, m, n, z);
 }
 
+// ---- few rows ------------------------------------------------------------------------
+// Up to 64 rows: bound by reading W once.  A workgroup takes 16 output columns (gated: of both
+// products) and its NW waves share the contraction in windows of 256 bytes of k, dealt out in
+// turn.  A wave streams the 16 W rows of its windows through an LDS ring of its own, S windows
+// deep, by direct copies (4 rows x 256 bytes each), so no barrier is met before the end; x comes
+// from the caches straight into the operand registers, as many windows ahead.  Vector v of row r
+// lies at r * 256 + 16 (v ^ r): the 16 rows of a fragment read fall on all banks.  The waves'
+// sums meet in LDS in a fixed order.  16 x 16 instructions: lane l = 16 q + c supplies W(c, k)
+// and x(c, k) of vector 4 s + q, and receives columns 4 q .. 4 q + 3 of row c.
 template <typename T>
-struct Tiles {
-  using Big = TileConfig<T, 256, 256, 2, 4, 2, 2>;
-  using Mid = TileConfig<T, 128, 128, 2, 2, 2, 2>;
-  using Small = TileConfig<T, 64, 64, 2, 2, 3, 2>;
+__device__ __forceinline__ f32x4 mfma16(u32x4 q, u32x4 p, f32x4 acc) {
+  if constexpr (sizeof(T) == 2) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, q), __builtin_bit_cast(bf16x8, p), acc,
+                                                   0, 0, 0);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(q[j]), __uint_as_float(p[j]), acc, 0, 0, 0);
+    return acc;
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+template <bool GATED, int TB, int NW, int S>
+struct FewRows {
+  static constexpr int NQ = GATED ? 2 : 1;
+  static constexpr int ring = S * NQ * 4096;  // bytes of a wave's ring
+  static constexpr int pitch = 20;            // floats of a row of 16 sums
+  static constexpr int sums = NQ * TB * 16 * pitch * 4;
+  static constexpr int lds = NW * (ring > sums ? ring : sums);
 };
+
+template <typename T, bool GATED, int TB, int NW, int S>
+__device__ __forceinline__ void few_rows_product(const GemmParams& a, unsigned char* lds) {
+  using F = FewRows<GATED, TB, NW, S>;
+  constexpr int NQ = F::NQ, kRing = F::ring, kPitch = F::pitch;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, q = lane >> 4;
+  const int64_t col0 = int64_t(blockIdx.x) * 16;
+  const int64_t bytes = a.depth * sizeof(T);
+  const int whole = static_cast<int>(bytes >> 8), windows = static_cast<int>((bytes + 255) >> 8);
+  const int tail = static_cast<int>(bytes & 255);  // bytes of the last window if short
+  const int n = wave < windows ? (windows - wave + NW - 1) / NW : 0;  // this wave's: wave, wave + NW, ...
+  const int full = n - (tail != 0 && n > 0 && wave + (n - 1) * NW == windows - 1);
+  // each workgroup starts elsewhere in k
+  const int turn = whole > 0 ? static_cast<int>(blockIdx.x) * NW % whole : 0;
+  auto window = [&](int i) {  // byte offset of this wave's window i
+    const int p = wave + i * NW, r = p + turn;
+    return 256 * (p >= whole ? p : r >= whole ? r - whole : r);
+  };
+
+  // W by buffer copies: the columns' first row as base, 32-bit offsets to the others
+  const int64_t last = a.cols - 1 - col0 < 15 ? a.cols - 1 - col0 : 15;
+  __amdgpu_buffer_rsrc_t w[NQ];
+  int off[NQ][4];
+#pragma unroll
+  for (int h = 0; h < NQ; ++h) {
+    const int64_t ld = a.q[h].ld * int64_t(sizeof(T));
+    w[h] = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<unsigned char*>(static_cast<const unsigned char*>(a.q[h].p) + col0 * ld), 0,
+        static_cast<int>(last * ld + bytes), 0x00020000);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = 4 * j + (lane >> 4);
+      off[h][j] = static_cast<int>((r < last ? r : last) * ld) + ((lane & 15) ^ r) * 16;
+    }
+  }
+  const unsigned char* xs[TB];
+#pragma unroll
+  for (int b = 0; b < TB; ++b) {
+    const int64_t m = 16 * b + c < a.rows ? 16 * b + c : a.rows - 1;
+    xs[b] = static_cast<const unsigned char*>(a.p.p) + m * a.p.ld * int64_t(sizeof(T)) + q * 16;
+  }
+  unsigned char* ring = lds + wave * kRing;
+  auto copy = [&](int i) {  // window i of this wave
+    unsigned char* at = ring + (i % S) * NQ * 4096;
+#pragma unroll
+    for (int h = 0; h < NQ; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(w[h], (ADA_LDS void*)(at + h * 4096 + j * 1024), 16, off[h][j],
+                                                 window(i), 0, 2);  // streamed once
+      }
+  };
+  auto copy_or_tail = [&](int i) {
+    if (i < full) {
+      copy(i);
+    } else if (i < n) {
+      unsigned char* at = ring + (i % S) * NQ * 4096;
+#pragma unroll
+      for (int h = 0; h < NQ; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          u32x4 d = {0, 0, 0, 0};
+          if (((lane & 15) ^ (4 * j + (lane >> 4))) * 16 < tail)
+            d = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(w[h], off[h][j], window(i), 0));
+          *reinterpret_cast<u32x4*>(at + h * 4096 + j * 1024 + lane * 16) = d;
+        }
+    }
+  };
+  u32x4 x[S][TB][4];
+  auto load_x = [&](int i, u32x4 (&to)[TB][4]) {
+#pragma unroll
+    for (int b = 0; b < TB; ++b)
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        to[b][s] = *reinterpret_cast<const u32x4*>(xs[b] + window(i) + s * 64);
+  };
+  auto load_x_or_tail = [&](int i, u32x4 (&to)[TB][4]) {
+    if (i < full) {
+      load_x(i, to);
+    } else {
+#pragma unroll
+      for (int b = 0; b < TB; ++b)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          u32x4 d = {0, 0, 0, 0};
+          if (i < n && (4 * s + q) * 16 < tail)
+            d = *reinterpret_cast<const u32x4*>(xs[b] + window(i) + s * 64);
+          to[b][s] = d;
+        }
+    }
+  };
+  f32x4 acc[NQ][TB] = {};
+  auto multiply = [&](int i, const u32x4 (&x)[TB][4]) {
+    const unsigned char* at = ring + (i % S) * NQ * 4096 + c * 256;
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int h = 0; h < NQ; ++h) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(at + h * 4096 + (((4 * s + q) ^ c) * 16));
+#pragma unroll
+        for (int b = 0; b < TB; ++b) acc[h][b] = mfma16<T>(w, x[b][s], acc[h][b]);
+      }
+    // the window's reads are done before its slot is copied to again
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  };
+  // Behind window i's data up to S - 1 windows are in flight when it is waited for.
+  constexpr int kWindow = 4 * (NQ + TB);
+  static_assert(S >= 2 && (S - 1) * kWindow < 64, "vmcnt");
+  int i = 0;
+  if (full >= 2 * S - 1) {
+#pragma unroll
+    for (int j = 0; j < S - 1; ++j) {
+      load_x(j, x[j]);
+      copy(j);
+    }
+    do {
+#pragma unroll
+      for (int u = 0; u < S; ++u) {
+        load_x(i + u + S - 1, x[(u + S - 1) % S]);
+        copy(i + u + S - 1);
+        wait_copies<(S - 1) * kWindow>();
+        multiply(i + u, x[u]);
+      }
+      i += S;
+    } while (i + 2 * S - 2 < full);
+  } else {
+#pragma unroll
+    for (int j = 0; j < S - 1; ++j) {
+      load_x_or_tail(j, x[j]);
+      copy_or_tail(j);
+    }
+  }
+  for (; i < n; i += S) {
+#pragma unroll
+    for (int u = 0; u < S; ++u) {
+      if (i + u >= n) break;
+      load_x_or_tail(i + u + S - 1, x[(u + S - 1) % S]);
+      copy_or_tail(i + u + S - 1);
+      const int behind = full - 1 - (i + u);  // whole windows in flight behind this one
+      if (behind >= S - 1)
+        wait_copies<(S - 1) * kWindow>();
+      else if (S > 2 && behind == S - 2)
+        wait_copies<(S - 2) * kWindow>();
+      else if (S > 3 && behind == S - 3)
+        wait_copies<(S > 3 ? S - 3 : 0) * kWindow>();
+      else
+        wait_copies<0>();
+      lds_wave_sync();  // a tail window went through registers
+      multiply(i + u, x[u]);
+    }
+  }
+
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(lds);
+  constexpr int kWave = NQ * TB * 16 * kPitch;
+#pragma unroll
+  for (int h = 0; h < NQ; ++h)
+#pragma unroll
+    for (int b = 0; b < TB; ++b)
+      *reinterpret_cast<f32x4*>(sums + wave * kWave + ((h * TB + b) * 16 + c) * kPitch + 4 * q) = acc[h][b];
+  __syncthreads();
+  for (int v = threadIdx.x; v < 2 * a.rows; v += 64 * NW) {
+    const int m = v >> 1, nc = (v & 1) * 8;
+    if (col0 + nc >= a.cols) continue;
+    float z[NQ][8] = {};
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+#pragma unroll
+      for (int h = 0; h < NQ; ++h) {
+        float t[8];
+        load8(sums + w * kWave + (h * TB * 16 + m) * kPitch + nc, t);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[h][e] += t[e];
+      }
+    finish8<T, GATED>(a, m, col0 + nc, z);
+  }
+}
+
+template <typename T, bool GATED, int TB, int NW, int S>
+__global__ void __launch_bounds__(64 * NW, 2) few_rows_kernel(GemmParams a) {
+  __shared__ __attribute__((aligned(16))) unsigned char lds[FewRows<GATED, TB, NW, S>::lds];
+  few_rows_product<T, GATED, TB, NW, S>(a, lds);
+}
+
+// ---- one to four rows ----------------------------------------------------------------
+// Bound by reading W once: one wave per W row (gated: per pair), lanes along it with 16-byte
+// loads, U vectors of each row in flight before any is used, x from the caches.  Eight waves
+// hold eight consecutive columns, which the epilogue takes together.  Past the row's end a
+// lane re-reads its first vector and multiplies it by a zero x.
+template <typename T>
+__device__ __forceinline__ float dot16(u32x4 w, u32x4 x, float acc) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      acc = fmaf(__uint_as_float(w[i] << 16), __uint_as_float(x[i] << 16), acc);
+      acc = fmaf(__uint_as_float(w[i] & 0xffff0000u), __uint_as_float(x[i] & 0xffff0000u), acc);
+    } else {
+      acc = fmaf(__uint_as_float(w[i]), __uint_as_float(x[i]), acc);
+    }
+  }
+  return acc;
+}
+
+constexpr int kDotRows = 1;
+
+template <typename T, bool GATED, int R>
+__global__ void __launch_bounds__(512) dot_kernel(GemmParams a) {
+  constexpr int NQ = GATED ? 2 : 1, VEC = 16 / sizeof(T);
+  constexpr int U = GATED || R > 2 ? 4 : 8;
+  __shared__ float sums[NQ][R][8];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n = int64_t(blockIdx.x) * 8 + wave;
+  const int nvec = static_cast<int>(a.depth / VEC);
+  const u32x4* w[NQ];
+  const u32x4* x[R];
+#pragma unroll
+  for (int h = 0; h < NQ; ++h)
+    w[h] = reinterpret_cast<const u32x4*>(static_cast<const T*>(a.q[h].p) + n * a.q[h].ld);
+#pragma unroll
+  for (int r = 0; r < R; ++r) x[r] = reinterpret_cast<const u32x4*>(static_cast<const T*>(a.p.p) + r * a.p.ld);
+  float acc[NQ][R] = {};
+  for (int v0 = 0; v0 < nvec; v0 += 64 * U) {
+    u32x4 wv[NQ][U], xv[R][U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int v = v0 + 64 * u + lane, at = v < nvec ? v : 0;
+#pragma unroll
+      for (int h = 0; h < NQ; ++h) wv[h][u] = __builtin_nontemporal_load(w[h] + at);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int v = v0 + 64 * u + lane, at = v < nvec ? v : 0;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const u32x4 d = x[r][at];
+        xv[r][u] = v < nvec ? d : u32x4{0, 0, 0, 0};
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < NQ; ++h)
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[h][r] = dot16<T>(wv[h][u], xv[r][u], acc[h][r]);
+  }
+#pragma unroll
+  for (int h = 0; h < NQ; ++h)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float v = acc[h][r];
+#pragma unroll
+      for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
+      if (lane == 0) sums[h][r][wave] = v;
+    }
+  __syncthreads();
+  if (threadIdx.x < R) {
+    float z[NQ][8];
+#pragma unroll
+    for (int h = 0; h < NQ; ++h)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[h][e] = sums[h][threadIdx.x][e];
+    finish8<T, GATED>(a, threadIdx.x, int64_t(blockIdx.x) * 8, z);
+  }
+}
+
+template <typename T, bool GATED>
+hipError_t launch_dot(const GemmParams& a, hipStream_t s) {
+  const unsigned grid = a.cols / 8;
+  switch (a.rows) {
+    case 1: dot_kernel<T, GATED, 1><<<grid, 512, 0, s>>>(a); break;
+    case 2: dot_kernel<T, GATED, 2><<<grid, 512, 0, s>>>(a); break;
+    case 3: dot_kernel<T, GATED, 3><<<grid, 512, 0, s>>>(a); break;
+    default: dot_kernel<T, GATED, 4><<<grid, 512, 0, s>>>(a); break;
+  }
+  return hipGetLastError();
+}
+
+#ifndef FEWROWS
+#define FEWROWS 16
+#endif
+constexpr int kFewRows = FEWROWS;
+
+// Whether a product takes the few-rows kernel: up to 64 rows, and 16 rows of each W within
+// the 32-bit offsets of its buffer copies.
+bool few_rows(const GemmParams& a, int gated, int esz) {
+  if (a.rows > kFewRows || a.row_split < a.rows) return false;
+  for (int h = 0; h < (gated ? 2 : 1); ++h)
+    if ((15 * a.q[h].ld + a.depth) * esz >= (int64_t(1) << 31)) return false;
+  return true;
+}
+
+template <typename T, bool GATED, int TB>
+hipError_t launch_few_rows_tb(const GemmParams& a, hipStream_t s) {
+  const unsigned grid = (a.cols + 15) / 16;
+#ifndef NWAVES
+#define NWAVES 8
+#define NSTAGES 2
+#endif
+  few_rows_kernel<T, GATED, TB, NWAVES, NSTAGES><<<grid, 64 * NWAVES, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <typename T, bool GATED>
+hipError_t launch_few_rows(const GemmParams& a, hipStream_t s) {
+  switch ((a.rows + 15) / 16) {
+    case 1: return launch_few_rows_tb<T, GATED, 1>(a, s);
+    case 2: return launch_few_rows_tb<T, GATED, 2>(a, s);
+    case 3: return launch_few_rows_tb<T, GATED, 3>(a, s);
+    default: return launch_few_rows_tb<T, GATED, 4>(a, s);
+  }
+}
+
+using BigTile = TileConfig<256, 256, 5, 1>;
+using MidTile = TileConfig<128, 128, 5, 2>;
+using SmallTile = TileConfig<64, 64, 6, 3>;
 
 template <typename T, typename C, bool GATED>
 hipError_t launch_tiles(GemmParams a, hipStream_t s) {
+  constexpr int cc = C::BN / (GATED ? 2 : 1);
   a.tiles_m = static_cast<int32_t>((a.rows + C::BM - 1) / C::BM);
-  a.tiles_n = (a.cols + C::BN / (GATED ? 2 : 1) - 1) / (C::BN / (GATED ? 2 : 1));
+  a.tiles_n = (a.cols + cc - 1) / cc;
   const unsigned grid = static_cast<unsigned>(a.tiles_m) * a.tiles_n * a.splits;
   if (a.splits > 1) {
     gemm_kernel<T, C, GATED, true><<<grid, C::threads, 0, s>>>(a);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    const int64_t quads = a.rows * (a.cols / 4);
-    join_kernel<T, GATED><<<static_cast<unsigned>((quads + 255) / 256), 256, 0, s>>>(a);
+    const int64_t groups = a.rows * (a.cols / 8);
+    join_kernel<T, GATED><<<static_cast<unsigned>((groups + 255) / 256), 256, 0, s>>>(a);
   } else {
     gemm_kernel<T, C, GATED, false><<<grid, C::threads, 0, s>>>(a);
   }
@@ -367,22 +837,19 @@ int64_t plan_bytes(const Plan& p, int64_t rows, int64_t cols, int gated) {
 
 template <typename T, bool GATED>
 hipError_t launch_gemm(GemmParams a, float* part, hipStream_t s) {
+  if (a.rows <= kDotRows && a.row_split >= a.rows) return launch_dot<T, GATED>(a, s);
+  if (few_rows(a, GATED, sizeof(T))) return launch_few_rows<T, GATED>(a, s);
   const Plan p = plan_gemm(a.rows, a.cols, a.depth, GATED, sizeof(T));
   a.splits = p.splits;
   a.part = part;
-  if (p.tile == 0) return launch_tiles<T, typename Tiles<T>::Big, GATED>(a, s);
-  if (p.tile == 1) return launch_tiles<T, typename Tiles<T>::Mid, GATED>(a, s);
-  return launch_tiles<T, typename Tiles<T>::Small, GATED>(a, s);
+  if (p.tile == 0) return launch_tiles<T, BigTile, GATED>(a, s);
+  if (p.tile == 1) return launch_tiles<T, MidTile, GATED>(a, s);
+  return launch_tiles<T, SmallTile, GATED>(a, s);
 }
 
 // ---- slopes and transposed copies ----------------------------------------------------
 // 64 x 64 tiles; a transposed copy goes through LDS so that both sides move 16-byte vectors.
 constexpr int kSide = 64;
-
-template <typename T>
-struct alignas(16) Vec16 {
-  T e[16 / sizeof(T)];
-};
 
 // Store the tile t[row][col] as out[col][row]: columns n0 .. (< cols), rows m0 .. (< m_end).
 template <typename T>
