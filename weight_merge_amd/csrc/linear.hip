@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(C::threads, C::per_simd) gemm_kernel(GemmParam
 
   // With one row band no W is shared between workgroups: each starts elsewhere in k, or all of
   // them would read the same few memory channels at a time.
-  const int turn = a.tiles_m == 1 && full > 0 ? static_cast<int>(blockIdx.x) * 5 % full : 0;
+  const int turn = a.tiles_m == 1 && full > 0 ? static_cast<int>(blockIdx.x % 4096 * 61 % full) : 0;
 
   // where this lane reads: copy j of the wave fills rows 8 (wave copies + j) + lane / 8 of a unit
   constexpr int kCopies[2] = {C::copies_p, C::copies_q};
@@ -443,14 +443,13 @@ __global__ void __launch_bounds__(256) join_kernel(GemmParams a) {
 }
 
 // ---- few rows ------------------------------------------------------------------------
-// Up to 64 rows: bound by reading W once.  A workgroup takes 16 output columns (gated: of both
+// Two to 16 rows: bound by reading W once.  A workgroup takes 16 output columns (gated: of both
 // products) and its NW waves share the contraction in windows of 256 bytes of k, dealt out in
-// turn.  A wave streams the 16 W rows of its windows through an LDS ring of its own, S windows
-// deep, by direct copies (4 rows x 256 bytes each), so no barrier is met before the end; x comes
-// from the caches straight into the operand registers, as many windows ahead.  Vector v of row r
-// lies at r * 256 + 16 (v ^ r): the 16 rows of a fragment read fall on all banks.  The waves'
-// sums meet in LDS in a fixed order.  16 x 16 instructions: lane l = 16 q + c supplies W(c, k)
-// and x(c, k) of vector 4 s + q, and receives columns 4 q .. 4 q + 3 of row c.
+// turn.  A wave streams its windows of W and of x through an LDS ring of its own, S windows
+// deep, by direct copies (4 rows x 256 bytes each), so no barrier is met before the end.
+// Vector v of row r lies at r * 256 + 16 (v ^ r): the 16 rows of a fragment read fall on all
+// banks.  The waves' sums meet in LDS in a fixed order.  16 x 16 instructions: lane l = 16 q + c
+// supplies W(c, k) and x(c, k) of vector 4 s + q, and receives columns 4 q .. 4 q + 3 of row c.
 template <typename T>
 __device__ __forceinline__ f32x4 mfma16(u32x4 q, u32x4 p, f32x4 acc) {
   if constexpr (sizeof(T) == 2) {
@@ -469,19 +468,20 @@ __device__ __forceinline__ void wait_copies() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-template <bool GATED, int TB, int NW, int S>
+template <bool GATED, int NW, int S>
 struct FewRows {
   static constexpr int NQ = GATED ? 2 : 1;
-  static constexpr int ring = S * NQ * 4096;  // bytes of a wave's ring
-  static constexpr int pitch = 20;            // floats of a row of 16 sums
-  static constexpr int sums = NQ * TB * 16 * pitch * 4;
-  static constexpr int lds = NW * (ring > sums ? ring : sums);
+  static constexpr int window = (NQ + 1) * 4096;  // bytes of a window: 16 rows of each W, then of x
+  static constexpr int pitch = 20;                // floats of a row of 16 sums
+  static constexpr int sums = NQ * 16 * pitch * 4;
+  static constexpr int lds = NW * S * window;
+  static_assert(S >= 2 && S * window >= sums && lds <= 160 * 1024 && 4 * (S - 1) * (NQ + 1) < 64, "ring");
 };
 
-template <typename T, bool GATED, int TB, int NW, int S>
+template <typename T, bool GATED, int NW, int S>
 __device__ __forceinline__ void few_rows_product(const GemmParams& a, unsigned char* lds) {
-  using F = FewRows<GATED, TB, NW, S>;
-  constexpr int NQ = F::NQ, kRing = F::ring, kPitch = F::pitch;
+  using F = FewRows<GATED, NW, S>;
+  constexpr int NQ = F::NQ, NO = NQ + 1;  // operands: the weights, then x
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, q = lane >> 4;
   const int64_t col0 = int64_t(blockIdx.x) * 16;
@@ -490,22 +490,25 @@ __device__ __forceinline__ void few_rows_product(const GemmParams& a, unsigned c
   const int tail = static_cast<int>(bytes & 255);  // bytes of the last window if short
   const int n = wave < windows ? (windows - wave + NW - 1) / NW : 0;  // this wave's: wave, wave + NW, ...
   const int full = n - (tail != 0 && n > 0 && wave + (n - 1) * NW == windows - 1);
-  // each workgroup starts elsewhere in k
-  const int turn = whole > 0 ? static_cast<int>(blockIdx.x) * NW % whole : 0;
+  // Each workgroup starts elsewhere in k: side by side, their 16 rows a stride apart, they would
+  // read the same few memory channels at a time (11008-long rows: 20.3 us, turned 16.6 us).
+  const int turn = whole > 0 ? static_cast<int>(blockIdx.x % 4096 * 61 % whole) : 0;
   auto window = [&](int i) {  // byte offset of this wave's window i
     const int p = wave + i * NW, r = p + turn;
     return 256 * (p >= whole ? p : r >= whole ? r - whole : r);
   };
 
-  // W by buffer copies: the columns' first row as base, 32-bit offsets to the others
-  const int64_t last = a.cols - 1 - col0 < 15 ? a.cols - 1 - col0 : 15;
-  __amdgpu_buffer_rsrc_t w[NQ];
-  int off[NQ][4];
+  // buffer copies: an operand's first row as base, 32-bit offsets to its others (rows past its
+  // end repeat the last)
+  __amdgpu_buffer_rsrc_t m[NO];
+  int off[NO][4];
 #pragma unroll
-  for (int h = 0; h < NQ; ++h) {
-    const int64_t ld = a.q[h].ld * int64_t(sizeof(T));
-    w[h] = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<unsigned char*>(static_cast<const unsigned char*>(a.q[h].p) + col0 * ld), 0,
+  for (int h = 0; h < NO; ++h) {
+    const MatIn& o = h < NQ ? a.q[h] : a.p;
+    const int64_t ld = o.ld * int64_t(sizeof(T)), first = h < NQ ? col0 : 0, rows = h < NQ ? a.cols : a.rows;
+    const int64_t last = rows - 1 - first < 15 ? rows - 1 - first : 15;
+    m[h] = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<unsigned char*>(static_cast<const unsigned char*>(o.p) + first * ld), 0,
         static_cast<int>(last * ld + bytes), 0x00020000);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -513,134 +516,63 @@ __device__ __forceinline__ void few_rows_product(const GemmParams& a, unsigned c
       off[h][j] = static_cast<int>((r < last ? r : last) * ld) + ((lane & 15) ^ r) * 16;
     }
   }
-  const unsigned char* xs[TB];
-#pragma unroll
-  for (int b = 0; b < TB; ++b) {
-    const int64_t m = 16 * b + c < a.rows ? 16 * b + c : a.rows - 1;
-    xs[b] = static_cast<const unsigned char*>(a.p.p) + m * a.p.ld * int64_t(sizeof(T)) + q * 16;
-  }
-  unsigned char* ring = lds + wave * kRing;
-  auto copy = [&](int i) {  // window i of this wave
-    unsigned char* at = ring + (i % S) * NQ * 4096;
-#pragma unroll
-    for (int h = 0; h < NQ; ++h)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(w[h], (ADA_LDS void*)(at + h * 4096 + j * 1024), 16, off[h][j],
-                                                 window(i), 0, 2);  // streamed once
-      }
-  };
-  auto copy_or_tail = [&](int i) {
+  unsigned char* ring = lds + wave * S * F::window;
+  auto copy_or_tail = [&](int i) {  // window i of this wave; W is streamed past the caches
+    unsigned char* at = ring + (i % S) * F::window;
     if (i < full) {
-      copy(i);
-    } else if (i < n) {
-      unsigned char* at = ring + (i % S) * NQ * 4096;
 #pragma unroll
-      for (int h = 0; h < NQ; ++h)
+      for (int h = 0; h < NO; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          ADA_LDS void* to = (ADA_LDS void*)(at + h * 4096 + j * 1024);
+          if (h < NQ)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(m[h], to, 16, off[h][j], window(i), 0, 2);
+          else
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(m[h], to, 16, off[h][j], window(i), 0, 0);
+        }
+    } else if (i < n) {
+#pragma unroll
+      for (int h = 0; h < NO; ++h)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           u32x4 d = {0, 0, 0, 0};
           if (((lane & 15) ^ (4 * j + (lane >> 4))) * 16 < tail)
-            d = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(w[h], off[h][j], window(i), 0));
+            d = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(m[h], off[h][j], window(i), 0));
           *reinterpret_cast<u32x4*>(at + h * 4096 + j * 1024 + lane * 16) = d;
         }
     }
   };
-  u32x4 x[S][TB][4];
-  auto load_x = [&](int i, u32x4 (&to)[TB][4]) {
+  f32x4 acc[NQ] = {};
 #pragma unroll
-    for (int b = 0; b < TB; ++b)
+  for (int i = 0; i < S - 1; ++i) copy_or_tail(i);
+  for (int i = 0; i < n; ++i) {
+    copy_or_tail(i + S - 1);
+    if (i + S - 1 < full)  // all but the S - 1 windows behind this one have arrived
+      wait_copies<4 * (S - 1) * NO>();
+    else
+      wait_copies<0>();
+    lds_wave_sync();  // a tail window went through registers
+    const unsigned char* at = ring + (i % S) * F::window + c * 256;
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-        to[b][s] = *reinterpret_cast<const u32x4*>(xs[b] + window(i) + s * 64);
-  };
-  auto load_x_or_tail = [&](int i, u32x4 (&to)[TB][4]) {
-    if (i < full) {
-      load_x(i, to);
-    } else {
+    for (int s = 0; s < 4; ++s) {
+      const int v = ((4 * s + q) ^ c) * 16;
+      const u32x4 x = *reinterpret_cast<const u32x4*>(at + NQ * 4096 + v);
 #pragma unroll
-      for (int b = 0; b < TB; ++b)
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          u32x4 d = {0, 0, 0, 0};
-          if (i < n && (4 * s + q) * 16 < tail)
-            d = *reinterpret_cast<const u32x4*>(xs[b] + window(i) + s * 64);
-          to[b][s] = d;
-        }
+      for (int h = 0; h < NQ; ++h) acc[h] = mfma16<T>(*reinterpret_cast<const u32x4*>(at + h * 4096 + v), x, acc[h]);
     }
-  };
-  f32x4 acc[NQ][TB] = {};
-  auto multiply = [&](int i, const u32x4 (&x)[TB][4]) {
-    const unsigned char* at = ring + (i % S) * NQ * 4096 + c * 256;
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int h = 0; h < NQ; ++h) {
-        const u32x4 w = *reinterpret_cast<const u32x4*>(at + h * 4096 + (((4 * s + q) ^ c) * 16));
-#pragma unroll
-        for (int b = 0; b < TB; ++b) acc[h][b] = mfma16<T>(w, x[b][s], acc[h][b]);
-      }
     // the window's reads are done before its slot is copied to again
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  };
-  // Behind window i's data up to S - 1 windows are in flight when it is waited for.
-  constexpr int kWindow = 4 * (NQ + TB);
-  static_assert(S >= 2 && (S - 1) * kWindow < 64, "vmcnt");
-  int i = 0;
-  if (full >= 2 * S - 1) {
-#pragma unroll
-    for (int j = 0; j < S - 1; ++j) {
-      load_x(j, x[j]);
-      copy(j);
-    }
-    do {
-#pragma unroll
-      for (int u = 0; u < S; ++u) {
-        load_x(i + u + S - 1, x[(u + S - 1) % S]);
-        copy(i + u + S - 1);
-        wait_copies<(S - 1) * kWindow>();
-        multiply(i + u, x[u]);
-      }
-      i += S;
-    } while (i + 2 * S - 2 < full);
-  } else {
-#pragma unroll
-    for (int j = 0; j < S - 1; ++j) {
-      load_x_or_tail(j, x[j]);
-      copy_or_tail(j);
-    }
-  }
-  for (; i < n; i += S) {
-#pragma unroll
-    for (int u = 0; u < S; ++u) {
-      if (i + u >= n) break;
-      load_x_or_tail(i + u + S - 1, x[(u + S - 1) % S]);
-      copy_or_tail(i + u + S - 1);
-      const int behind = full - 1 - (i + u);  // whole windows in flight behind this one
-      if (behind >= S - 1)
-        wait_copies<(S - 1) * kWindow>();
-      else if (S > 2 && behind == S - 2)
-        wait_copies<(S - 2) * kWindow>();
-      else if (S > 3 && behind == S - 3)
-        wait_copies<(S > 3 ? S - 3 : 0) * kWindow>();
-      else
-        wait_copies<0>();
-      lds_wave_sync();  // a tail window went through registers
-      multiply(i + u, x[u]);
-    }
   }
 
   __syncthreads();
   float* sums = reinterpret_cast<float*>(lds);
-  constexpr int kWave = NQ * TB * 16 * kPitch;
+  constexpr int kWave = F::sums / 4;
 #pragma unroll
   for (int h = 0; h < NQ; ++h)
-#pragma unroll
-    for (int b = 0; b < TB; ++b)
-      *reinterpret_cast<f32x4*>(sums + wave * kWave + ((h * TB + b) * 16 + c) * kPitch + 4 * q) = acc[h][b];
+    *reinterpret_cast<f32x4*>(sums + wave * kWave + (h * 16 + c) * F::pitch + 4 * q) = acc[h];
   __syncthreads();
   for (int v = threadIdx.x; v < 2 * a.rows; v += 64 * NW) {
-    const int m = v >> 1, nc = (v & 1) * 8;
+    const int r = v >> 1, nc = (v & 1) * 8;
     if (col0 + nc >= a.cols) continue;
     float z[NQ][8] = {};
 #pragma unroll
@@ -648,21 +580,40 @@ __device__ __forceinline__ void few_rows_product(const GemmParams& a, unsigned c
 #pragma unroll
       for (int h = 0; h < NQ; ++h) {
         float t[8];
-        load8(sums + w * kWave + (h * TB * 16 + m) * kPitch + nc, t);
+        load8(sums + w * kWave + (h * 16 + r) * F::pitch + nc, t);
 #pragma unroll
         for (int e = 0; e < 8; ++e) z[h][e] += t[e];
       }
-    finish8<T, GATED>(a, m, col0 + nc, z);
+    finish8<T, GATED>(a, r, col0 + nc, z);
   }
 }
 
-template <typename T, bool GATED, int TB, int NW, int S>
-__global__ void __launch_bounds__(64 * NW, 2) few_rows_kernel(GemmParams a) {
-  __shared__ __attribute__((aligned(16))) unsigned char lds[FewRows<GATED, TB, NW, S>::lds];
-  few_rows_product<T, GATED, TB, NW, S>(a, lds);
+template <typename T, bool GATED, int NW, int S>
+__global__ void __launch_bounds__(64 * NW) few_rows_kernel(GemmParams a) {
+  __shared__ __attribute__((aligned(16))) unsigned char lds[FewRows<GATED, NW, S>::lds];
+  few_rows_product<T, GATED, NW, S>(a, lds);
 }
 
-// ---- one to four rows ----------------------------------------------------------------
+constexpr int kFewRows = 16;
+
+// Whether a product takes the few-rows kernel: up to 16 rows, within the 32-bit offsets of its
+// buffer copies.
+bool few_rows(const GemmParams& a, int gated, int esz) {
+  if (a.rows > kFewRows || a.row_split < a.rows) return false;
+  for (int h = 0; h < (gated ? 3 : 2); ++h)
+    if ((15 * (h == 0 ? a.p : a.q[h - 1]).ld + a.depth) * esz >= (int64_t(1) << 31)) return false;
+  return true;
+}
+
+template <typename T, bool GATED>
+hipError_t launch_few_rows(const GemmParams& a, hipStream_t s) {
+  const unsigned grid = (a.cols + 15) / 16;
+  constexpr int waves = GATED ? 4 : 8;
+  few_rows_kernel<T, GATED, waves, 2><<<grid, 64 * waves, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+// ---- one row -------------------------------------------------------------------------
 // Bound by reading W once: one wave per W row (gated: per pair), lanes along it with 16-byte
 // loads, U vectors of each row in flight before any is used, x from the caches.  Eight waves
 // hold eight consecutive columns, which the epilogue takes together.  Past the row's end a
@@ -681,118 +632,75 @@ __device__ __forceinline__ float dot16(u32x4 w, u32x4 x, float acc) {
   return acc;
 }
 
-constexpr int kDotRows = 1;
-
-template <typename T, bool GATED, int R>
-__global__ void __launch_bounds__(512) dot_kernel(GemmParams a) {
-  constexpr int NQ = GATED ? 2 : 1, VEC = 16 / sizeof(T);
-  constexpr int U = GATED || R > 2 ? 4 : 8;
-  __shared__ float sums[NQ][R][8];
+template <typename T, bool GATED>
+__global__ void __launch_bounds__(512) one_row_kernel(GemmParams a) {
+  constexpr int NQ = GATED ? 2 : 1, VEC = 16 / sizeof(T), U = GATED ? 4 : 8;
+  __shared__ float sums[NQ][8];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t n = int64_t(blockIdx.x) * 8 + wave;
   const int nvec = static_cast<int>(a.depth / VEC);
+  const u32x4* x = static_cast<const u32x4*>(a.p.p);
   const u32x4* w[NQ];
-  const u32x4* x[R];
 #pragma unroll
   for (int h = 0; h < NQ; ++h)
     w[h] = reinterpret_cast<const u32x4*>(static_cast<const T*>(a.q[h].p) + n * a.q[h].ld);
-#pragma unroll
-  for (int r = 0; r < R; ++r) x[r] = reinterpret_cast<const u32x4*>(static_cast<const T*>(a.p.p) + r * a.p.ld);
-  float acc[NQ][R] = {};
+  float acc[NQ] = {};
   for (int v0 = 0; v0 < nvec; v0 += 64 * U) {
-    u32x4 wv[NQ][U], xv[R][U];
+    u32x4 wv[NQ][U], xv[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int v = v0 + 64 * u + lane, at = v < nvec ? v : 0;
 #pragma unroll
       for (int h = 0; h < NQ; ++h) wv[h][u] = __builtin_nontemporal_load(w[h] + at);
+      xv[u] = x[at];
     }
+    __builtin_amdgcn_sched_barrier(0);  // every load before the first use
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int v = v0 + 64 * u + lane, at = v < nvec ? v : 0;
+      const u32x4 d = v0 + 64 * u + lane < nvec ? xv[u] : u32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const u32x4 d = x[r][at];
-        xv[r][u] = v < nvec ? d : u32x4{0, 0, 0, 0};
-      }
+      for (int h = 0; h < NQ; ++h) acc[h] = dot16<T>(wv[h][u], d, acc[h]);
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int h = 0; h < NQ; ++h)
-#pragma unroll
-        for (int r = 0; r < R; ++r) acc[h][r] = dot16<T>(wv[h][u], xv[r][u], acc[h][r]);
   }
 #pragma unroll
-  for (int h = 0; h < NQ; ++h)
+  for (int h = 0; h < NQ; ++h) {
+    float v = acc[h];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float v = acc[h][r];
-#pragma unroll
-      for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
-      if (lane == 0) sums[h][r][wave] = v;
-    }
+    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
+    if (lane == 0) sums[h][wave] = v;
+  }
   __syncthreads();
-  if (threadIdx.x < R) {
+  if (threadIdx.x == 0) {
     float z[NQ][8];
 #pragma unroll
     for (int h = 0; h < NQ; ++h)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) z[h][e] = sums[h][threadIdx.x][e];
-    finish8<T, GATED>(a, threadIdx.x, int64_t(blockIdx.x) * 8, z);
+      for (int e = 0; e < 8; ++e) z[h][e] = sums[h][e];
+    finish8<T, GATED>(a, 0, int64_t(blockIdx.x) * 8, z);
   }
 }
 
 template <typename T, bool GATED>
-hipError_t launch_dot(const GemmParams& a, hipStream_t s) {
-  const unsigned grid = a.cols / 8;
-  switch (a.rows) {
-    case 1: dot_kernel<T, GATED, 1><<<grid, 512, 0, s>>>(a); break;
-    case 2: dot_kernel<T, GATED, 2><<<grid, 512, 0, s>>>(a); break;
-    case 3: dot_kernel<T, GATED, 3><<<grid, 512, 0, s>>>(a); break;
-    default: dot_kernel<T, GATED, 4><<<grid, 512, 0, s>>>(a); break;
-  }
+hipError_t launch_one_row(const GemmParams& a, hipStream_t s) {
+  one_row_kernel<T, GATED><<<a.cols / 8, 512, 0, s>>>(a);
   return hipGetLastError();
 }
 
-#ifndef FEWROWS
-#define FEWROWS 16
-#endif
-constexpr int kFewRows = FEWROWS;
-
-// Whether a product takes the few-rows kernel: up to 64 rows, and 16 rows of each W within
-// the 32-bit offsets of its buffer copies.
-bool few_rows(const GemmParams& a, int gated, int esz) {
-  if (a.rows > kFewRows || a.row_split < a.rows) return false;
-  for (int h = 0; h < (gated ? 2 : 1); ++h)
-    if ((15 * a.q[h].ld + a.depth) * esz >= (int64_t(1) << 31)) return false;
-  return true;
-}
-
-template <typename T, bool GATED, int TB>
-hipError_t launch_few_rows_tb(const GemmParams& a, hipStream_t s) {
-  const unsigned grid = (a.cols + 15) / 16;
-#ifndef NWAVES
-#define NWAVES 8
-#define NSTAGES 2
-#endif
-  few_rows_kernel<T, GATED, TB, NWAVES, NSTAGES><<<grid, 64 * NWAVES, 0, s>>>(a);
-  return hipGetLastError();
-}
-
-template <typename T, bool GATED>
-hipError_t launch_few_rows(const GemmParams& a, hipStream_t s) {
-  switch ((a.rows + 15) / 16) {
-    case 1: return launch_few_rows_tb<T, GATED, 1>(a, s);
-    case 2: return launch_few_rows_tb<T, GATED, 2>(a, s);
-    case 3: return launch_few_rows_tb<T, GATED, 3>(a, s);
-    default: return launch_few_rows_tb<T, GATED, 4>(a, s);
-  }
-}
-
-using BigTile = TileConfig<256, 256, 5, 1>;
-using MidTile = TileConfig<128, 128, 5, 2>;
-using SmallTile = TileConfig<64, 64, 6, 3>;
+// The tiles and what a step and a workgroup's start and end cost on a CU of its own, in us
+// (bf16 step, fp32 step, rest): fitted to 19 shapes from 24 x 4096 x 11008 to 4096 x 4096 x 2048
+// timed with every tile and split.
+using Tile0 = TileConfig<256, 256, 5, 1>;
+using Tile1 = TileConfig<256, 128, 6, 1>;
+using Tile2 = TileConfig<128, 256, 6, 1>;
+using Tile3 = TileConfig<128, 128, 10, 1>;
+using Tile4 = TileConfig<64, 128, 12, 1>;
+using Tile5 = TileConfig<64, 64, 10, 2>;
+constexpr int kTiles = 6;
+constexpr int kTileRows[kTiles] = {Tile0::BM, Tile1::BM, Tile2::BM, Tile3::BM, Tile4::BM, Tile5::BM};
+constexpr int kTileCols[kTiles] = {Tile0::BN, Tile1::BN, Tile2::BN, Tile3::BN, Tile4::BN, Tile5::BN};
+constexpr float kStep16[kTiles] = {1.5f, 0.93f, 0.93f, 0.60f, 0.45f, 0.30f};
+constexpr float kStep32[kTiles] = {7.5f, 3.9f, 3.9f, 2.05f, 1.1f, 0.65f};
+constexpr float kRest[kTiles] = {12.f, 6.f, 6.f, 4.5f, 3.5f, 3.f};
 
 template <typename T, typename C, bool GATED>
 hipError_t launch_tiles(GemmParams a, hipStream_t s) {
@@ -811,24 +719,33 @@ hipError_t launch_tiles(GemmParams a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Which tile, and into how many parts the contraction is split.
+// Which tile, and into how many parts the contraction is split: the least sum of rounds (256
+// workgroups at a time, one per CU) times the steps and the rest of each, and for a split the
+// join: a launch, and its parts written and read at about 4 TB/s.
 struct Plan {
-  int tile;    // 0: 256 x 256, 1: 128 x 128, 2: 64 x 64
+  int tile;
   int splits;
 };
-constexpr int kMaxSplits = 16;
 
 Plan plan_gemm(int64_t rows, int64_t cols, int64_t depth, int gated, int esz) {
-  const int64_t n = gated ? 2 * cols : cols;
-  auto tiles = [&](int64_t t) { return ((rows + t - 1) / t) * ((n + t - 1) / t); };
-  const int64_t steps = (depth * esz + 127) / 128;
-  if (tiles(256) >= 192) return {0, 1};
-  const int tile = tiles(128) >= 192 ? 1 : 2;
-  const int64_t have = tiles(tile == 1 ? 128 : 64);
-  int64_t splits = 512 / have;
-  if (splits > steps / 8) splits = steps / 8;
-  if (splits > kMaxSplits) splits = kMaxSplits;
-  return {tile, static_cast<int>(splits < 1 ? 1 : splits)};
+  const int64_t n = gated ? 2 * cols : cols, steps = (depth * esz + 127) / 128;
+  Plan best{0, 1};
+  float least = -1.f;
+  for (int t = 0; t < kTiles; ++t) {
+    const int64_t tiles = ((rows + kTileRows[t] - 1) / kTileRows[t]) * ((n + kTileCols[t] - 1) / kTileCols[t]);
+    const float step = esz == 2 ? kStep16[t] : kStep32[t];
+    for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      if (splits > 1 && (steps / splits < 3 || tiles * splits > 1024)) break;
+      const float rounds = static_cast<float>((tiles * splits + 255) / 256);
+      float us = rounds * (static_cast<float>((steps + splits - 1) / splits) * step + kRest[t]);
+      if (splits > 1) us += 3.f + static_cast<float>(splits * n * rows) * 8.f / 4e6f;
+      if (least < 0.f || us < least) {
+        least = us;
+        best = {t, splits};
+      }
+    }
+  }
+  return best;
 }
 
 int64_t plan_bytes(const Plan& p, int64_t rows, int64_t cols, int gated) {
@@ -837,14 +754,19 @@ int64_t plan_bytes(const Plan& p, int64_t rows, int64_t cols, int gated) {
 
 template <typename T, bool GATED>
 hipError_t launch_gemm(GemmParams a, float* part, hipStream_t s) {
-  if (a.rows <= kDotRows && a.row_split >= a.rows) return launch_dot<T, GATED>(a, s);
+  if (a.rows == 1) return launch_one_row<T, GATED>(a, s);
   if (few_rows(a, GATED, sizeof(T))) return launch_few_rows<T, GATED>(a, s);
   const Plan p = plan_gemm(a.rows, a.cols, a.depth, GATED, sizeof(T));
   a.splits = p.splits;
   a.part = part;
-  if (p.tile == 0) return launch_tiles<T, BigTile, GATED>(a, s);
-  if (p.tile == 1) return launch_tiles<T, MidTile, GATED>(a, s);
-  return launch_tiles<T, SmallTile, GATED>(a, s);
+  switch (p.tile) {
+    case 0: return launch_tiles<T, Tile0, GATED>(a, s);
+    case 1: return launch_tiles<T, Tile1, GATED>(a, s);
+    case 2: return launch_tiles<T, Tile2, GATED>(a, s);
+    case 3: return launch_tiles<T, Tile3, GATED>(a, s);
+    case 4: return launch_tiles<T, Tile4, GATED>(a, s);
+    default: return launch_tiles<T, Tile5, GATED>(a, s);
+  }
 }
 
 // ---- slopes and transposed copies ----------------------------------------------------
