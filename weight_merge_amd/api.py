@@ -8,6 +8,7 @@ caller does not pass are allocated here with torch, outside the C calls.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -362,34 +363,32 @@ def _act(act: str) -> int:
         raise ValueError(f"unknown activation {act!r}; expected one of {', '.join(_ACTS)}") from None
 
 
-def _mat(t, rows: int, cols: int, like: torch.Tensor, name: str):
-    """Pointer and row stride of a [rows, cols] matrix of like's dtype and device."""
+def _refuse(t, shape, dt, dev: int, name: str):
+    """The error for a tensor that is not of this shape, dtype and device with unit column stride."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype != dt:
+        raise TypeError(f"{name} must be {dt} like the other tensors, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not with the other tensors")
+    raise ValueError(f"{name} must have unit column stride" if len(shape) == 2 else f"{name} must be contiguous")
+
+
+def _mat(t, rows: int, cols: int, dt, dev: int, name: str):
+    """Pointer and row stride of a [rows, cols] matrix."""
     if t is None:
         return None, 0
-    if t.shape != (rows, cols):
-        raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype} like the other tensors, got {t.dtype}")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not {like.device}")
-    ld, unit = t.stride()
-    if unit != 1:
-        raise ValueError(f"{name} must have unit column stride")
-    return t.data_ptr(), ld if rows > 1 else cols
+    if t.shape != (rows, cols) or t.dtype is not dt or t.get_device() != dev or t.stride(1) != 1:
+        _refuse(t, (rows, cols), dt, dev, name)
+    return t.data_ptr(), t.stride(0) if rows > 1 else cols
 
 
-def _vec(t, n: int, like: torch.Tensor, name: str):
-    """Pointer of an [n] vector of like's dtype and device."""
+def _vec(t, n: int, dt, dev: int, name: str):
+    """Pointer of an [n] vector."""
     if t is None:
         return None
-    if t.shape != (n,):
-        raise ValueError(f"{name} must be [{n}], got {list(t.shape)}")
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype} like the other tensors, got {t.dtype}")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not {like.device}")
-    if t.stride(0) != 1:
-        raise ValueError(f"{name} must be contiguous")
+    if t.shape != (n,) or t.dtype is not dt or t.get_device() != dev or t.stride(0) != 1:
+        _refuse(t, (n,), dt, dev, name)
     return t.data_ptr()
 
 
@@ -399,72 +398,63 @@ def _sizes(x: torch.Tensor, w: torch.Tensor):
     return x.shape[0], w.shape[0], w.shape[1]
 
 
-def _current(t: torch.Tensor):
-    if not t.is_cuda:
+def _current(dev: int):
+    if dev < 0:
         raise ValueError("tensors must be on the device")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {t.device}, but cuda:{torch.cuda.current_device()} is current")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{dev}, but cuda:{torch.cuda.current_device()} is current")
 
 
-class _On:
-    """Allocations inside belong to the call's stream: made ready, and taken back, in its order."""
-
-    def __init__(self, stream):
-        self.ctx = None
-        if stream is not None:
-            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-            self.ctx = torch.cuda.stream(s)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _on(stream):
+    """Makes the call's stream the current one, so that what the call allocates is made ready,
+    and taken back, in that stream's order."""
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
 
 
-def _workspace(need: int, workspace, like: torch.Tensor, call: str):
+def _raw_stream(dev: int) -> int:
+    """Handle of the current stream (the public call builds a Stream object each time)."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev) if raw is not None else torch.cuda.current_stream().cuda_stream
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(call: str, *sizes) -> int:
+    n = int(getattr(_lib.load(), call)(*sizes))
+    _check(min(n, 0), call)
+    return n
+
+
+def _workspace(need: int, workspace, dev: int):
     """(pointer, bytes, tensor) of the caller's workspace, or of one allocated here."""
-    if need < 0:
-        _check(need, call)
     if workspace is not None:
         _contig(workspace, "workspace")
-        if workspace.device != like.device:
-            raise ValueError(f"workspace is on {workspace.device}, not {like.device}")
+        if workspace.get_device() != dev:
+            raise ValueError(f"workspace is on {workspace.device}, not with the other tensors")
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
     if need == 0:
         return None, 0, None
-    workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+    workspace = torch.empty(need, dtype=torch.uint8, device=f"cuda:{dev}")
     return workspace.data_ptr(), need, workspace
 
 
 def linear_workspace_bytes(rows: int, d_out: int, d_in: int, dtype: torch.dtype) -> int:
     """Bytes of workspace ada_linear needs at these sizes."""
-    n = int(_lib.load().ada_linear_workspace(rows, d_out, d_in, _DT[dtype]))
-    _check(min(n, 0), "ada_linear_workspace")
-    return n
+    return _workspace_bytes("ada_linear_workspace", rows, d_out, d_in, _DT[dtype])
 
 
 def glu_workspace_bytes(rows: int, d_out: int, d_in: int, dtype: torch.dtype) -> int:
     """Bytes of workspace ada_glu needs at these sizes."""
-    n = int(_lib.load().ada_glu_workspace(rows, d_out, d_in, _DT[dtype]))
-    _check(min(n, 0), "ada_glu_workspace")
-    return n
+    return _workspace_bytes("ada_glu_workspace", rows, d_out, d_in, _DT[dtype])
 
 
 def linear_backward_workspace_bytes(rows: int, d_out: int, d_in: int, act: str, dtype: torch.dtype) -> int:
     """Bytes of workspace ada_linear_backward needs at these sizes."""
-    n = int(_lib.load().ada_linear_backward_workspace(rows, d_out, d_in, _act(act), _DT[dtype]))
-    _check(min(n, 0), "ada_linear_backward_workspace")
-    return n
+    return _workspace_bytes("ada_linear_backward_workspace", rows, d_out, d_in, _act(act), _DT[dtype])
 
 
 def glu_backward_workspace_bytes(rows: int, d_out: int, d_in: int, act: str, dtype: torch.dtype) -> int:
     """Bytes of workspace ada_glu_backward needs at these sizes."""
-    n = int(_lib.load().ada_glu_backward_workspace(rows, d_out, d_in, _act(act), _DT[dtype]))
-    _check(min(n, 0), "ada_glu_backward_workspace")
-    return n
+    return _workspace_bytes("ada_glu_backward_workspace", rows, d_out, d_in, _act(act), _DT[dtype])
 
 
 def ada_linear(x: torch.Tensor, w: torch.Tensor, bias=None, residual=None, act: str = "none", y=None, pre=None,
@@ -474,24 +464,25 @@ def ada_linear(x: torch.Tensor, w: torch.Tensor, bias=None, residual=None, act: 
 
     act: "none", "relu", "silu", "gelu" (error function) or "gelu_tanh".  y may be the
     residual itself.  A workspace and a y not passed are allocated on the call's stream."""
+    if stream is not None:
+        with _on(stream):
+            return ada_linear(x, w, bias, residual, act, y, pre, workspace)
     rows, d_out, d_in = _sizes(x, w)
-    dt, code, lib = _dtype(x), _act(act), _lib.load()
-    px, ldx = _mat(x, rows, d_in, x, "x")
-    pw, ldw = _mat(w, d_out, d_in, x, "w")
-    pb = _vec(bias, d_out, x, "bias")
-    pr, ldr = _mat(residual, rows, d_out, x, "residual")
-    pp, ldp = _mat(pre, rows, d_out, x, "pre")
+    code, dc, dt, dev = _act(act), _dtype(x), x.dtype, x.get_device()
+    px, ldx = _mat(x, rows, d_in, dt, dev, "x")
+    pw, ldw = _mat(w, d_out, d_in, dt, dev, "w")
+    pb = _vec(bias, d_out, dt, dev, "bias")
+    pr, ldr = _mat(residual, rows, d_out, dt, dev, "residual")
+    pp, ldp = _mat(pre, rows, d_out, dt, dev, "pre")
     if y is not None:
-        py, ldy = _mat(y, rows, d_out, x, "y")
-    _current(x)
-    with _On(stream):
-        if y is None:
-            y = torch.empty((rows, d_out), dtype=x.dtype, device=x.device)
-            py, ldy = y.data_ptr(), d_out
-        ws, nbytes, _keep = _workspace(lib.ada_linear_workspace(rows, d_out, d_in, dt), workspace, x,
-                                       "ada_linear_workspace")
-        args = AdaLinearArgs(px, pw, pb, pr, py, pp, ldx, ldw, ldr, ldy, ldp, rows, d_out, d_in)
-        _check(lib.ada_linear(args, code, dt, ws, nbytes, _stream(stream)), "ada_linear")
+        py, ldy = _mat(y, rows, d_out, dt, dev, "y")
+    _current(dev)
+    if y is None:
+        y = torch.empty((rows, d_out), dtype=dt, device=x.device)
+        py, ldy = y.data_ptr(), d_out
+    ws, nbytes, _keep = _workspace(_workspace_bytes("ada_linear_workspace", rows, d_out, d_in, dc), workspace, dev)
+    args = AdaLinearArgs(px, pw, pb, pr, py, pp, ldx, ldw, ldr, ldy, ldp, rows, d_out, d_in)
+    _check(_lib.load().ada_linear(args, code, dc, ws, nbytes, _raw_stream(dev)), "ada_linear")
     return y
 
 
@@ -501,34 +492,36 @@ def ada_linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, pre=
     """(dx, dw, dbias) of ada_linear: dz = dy act'(pre), dx = dz w, dw = dz^T x, dbias the
     sum of dz over rows; None for what is neither passed nor wanted.  `pre` is what
     ada_linear saved (not needed for act "none")."""
+    if stream is not None:
+        with _on(stream):
+            return ada_linear_backward(dy, x, w, pre, act, dx, dw, dbias, want_dx, want_dw, want_dbias, workspace)
     rows, d_out, d_in = _sizes(x, w)
-    dt, code, lib = _dtype(x), _act(act), _lib.load()
+    code, dc, dt, dev = _act(act), _dtype(x), x.dtype, x.get_device()
     if code == 0:
         pre = None
     elif pre is None:
         raise ValueError("pre is needed for the slope of the activation")
-    pdy, lddy = _mat(dy, rows, d_out, x, "dy")
-    px, ldx = _mat(x, rows, d_in, x, "x")
-    pw, ldw = _mat(w, d_out, d_in, x, "w")
-    pp, ldp = _mat(pre, rows, d_out, x, "pre")
-    _mat(dx, rows, d_in, x, "dx")
-    _mat(dw, d_out, d_in, x, "dw")
-    _vec(dbias, d_out, x, "dbias")
-    _current(x)
-    with _On(stream):
-        if dx is None and want_dx:
-            dx = torch.empty((rows, d_in), dtype=x.dtype, device=x.device)
-        if dw is None and want_dw:
-            dw = torch.empty((d_out, d_in), dtype=x.dtype, device=x.device)
-        if dbias is None and want_dbias:
-            dbias = torch.empty(d_out, dtype=x.dtype, device=x.device)
-        pdx, lddx = _mat(dx, rows, d_in, x, "dx")
-        pdw, lddw = _mat(dw, d_out, d_in, x, "dw")
-        pdb = _vec(dbias, d_out, x, "dbias")
-        ws, nbytes, _keep = _workspace(lib.ada_linear_backward_workspace(rows, d_out, d_in, code, dt), workspace, x,
-                                       "ada_linear_backward_workspace")
-        args = AdaLinearGradArgs(pdy, px, pw, pp, pdx, pdw, pdb, lddy, ldx, ldw, ldp, lddx, lddw, rows, d_out, d_in)
-        _check(lib.ada_linear_backward(args, code, dt, ws, nbytes, _stream(stream)), "ada_linear_backward")
+    pdy, lddy = _mat(dy, rows, d_out, dt, dev, "dy")
+    px, ldx = _mat(x, rows, d_in, dt, dev, "x")
+    pw, ldw = _mat(w, d_out, d_in, dt, dev, "w")
+    pp, ldp = _mat(pre, rows, d_out, dt, dev, "pre")
+    pdx, lddx = _mat(dx, rows, d_in, dt, dev, "dx")
+    pdw, lddw = _mat(dw, d_out, d_in, dt, dev, "dw")
+    pdb = _vec(dbias, d_out, dt, dev, "dbias")
+    _current(dev)
+    if dx is None and want_dx:
+        dx = torch.empty((rows, d_in), dtype=dt, device=x.device)
+        pdx, lddx = dx.data_ptr(), d_in
+    if dw is None and want_dw:
+        dw = torch.empty((d_out, d_in), dtype=dt, device=x.device)
+        pdw, lddw = dw.data_ptr(), d_in
+    if dbias is None and want_dbias:
+        dbias = torch.empty(d_out, dtype=dt, device=x.device)
+        pdb = dbias.data_ptr()
+    ws, nbytes, _keep = _workspace(_workspace_bytes("ada_linear_backward_workspace", rows, d_out, d_in, code, dc),
+                                   workspace, dev)
+    args = AdaLinearGradArgs(pdy, px, pw, pp, pdx, pdw, pdb, lddy, ldx, ldw, ldp, lddx, lddw, rows, d_out, d_in)
+    _check(_lib.load().ada_linear_backward(args, code, dc, ws, nbytes, _raw_stream(dev)), "ada_linear_backward")
     return dx, dw, dbias
 
 
@@ -536,26 +529,28 @@ def ada_glu(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, bias_gate
             act: str = "silu", y=None, pre=None, workspace=None, stream=None):
     """y = act(g) u with g = x w_gate^T + bias_gate and u = x w_up^T + bias_up, in one pass;
     `pre`, if given, is a pair (g, u) of matrices to receive them for the backward pass."""
+    if stream is not None:
+        with _on(stream):
+            return ada_glu(x, w_gate, w_up, bias_gate, bias_up, act, y, pre, workspace)
     rows, d_out, d_in = _sizes(x, w_gate)
-    dt, code, lib = _dtype(x), _act(act), _lib.load()
-    px, ldx = _mat(x, rows, d_in, x, "x")
-    pg, ldg = _mat(w_gate, d_out, d_in, x, "w_gate")
-    pu, ldu = _mat(w_up, d_out, d_in, x, "w_up")
-    pbg = _vec(bias_gate, d_out, x, "bias_gate")
-    pbu = _vec(bias_up, d_out, x, "bias_up")
+    code, dc, dt, dev = _act(act), _dtype(x), x.dtype, x.get_device()
+    px, ldx = _mat(x, rows, d_in, dt, dev, "x")
+    pg, ldg = _mat(w_gate, d_out, d_in, dt, dev, "w_gate")
+    pu, ldu = _mat(w_up, d_out, d_in, dt, dev, "w_up")
+    pbg = _vec(bias_gate, d_out, dt, dev, "bias_gate")
+    pbu = _vec(bias_up, d_out, dt, dev, "bias_up")
     gate_pre, up_pre = pre if pre is not None else (None, None)
-    ppg, ldpg = _mat(gate_pre, rows, d_out, x, "gate_pre")
-    ppu, ldpu = _mat(up_pre, rows, d_out, x, "up_pre")
+    ppg, ldpg = _mat(gate_pre, rows, d_out, dt, dev, "gate_pre")
+    ppu, ldpu = _mat(up_pre, rows, d_out, dt, dev, "up_pre")
     if y is not None:
-        py, ldy = _mat(y, rows, d_out, x, "y")
-    _current(x)
-    with _On(stream):
-        if y is None:
-            y = torch.empty((rows, d_out), dtype=x.dtype, device=x.device)
-            py, ldy = y.data_ptr(), d_out
-        ws, nbytes, _keep = _workspace(lib.ada_glu_workspace(rows, d_out, d_in, dt), workspace, x, "ada_glu_workspace")
-        args = AdaGluArgs(px, pg, pu, pbg, pbu, py, ppg, ppu, ldx, ldg, ldu, ldy, ldpg, ldpu, rows, d_out, d_in)
-        _check(lib.ada_glu(args, code, dt, ws, nbytes, _stream(stream)), "ada_glu")
+        py, ldy = _mat(y, rows, d_out, dt, dev, "y")
+    _current(dev)
+    if y is None:
+        y = torch.empty((rows, d_out), dtype=dt, device=x.device)
+        py, ldy = y.data_ptr(), d_out
+    ws, nbytes, _keep = _workspace(_workspace_bytes("ada_glu_workspace", rows, d_out, d_in, dc), workspace, dev)
+    args = AdaGluArgs(px, pg, pu, pbg, pbu, py, ppg, ppu, ldx, ldg, ldu, ldy, ldpg, ldpu, rows, d_out, d_in)
+    _check(_lib.load().ada_glu(args, code, dc, ws, nbytes, _raw_stream(dev)), "ada_glu")
     return y
 
 
@@ -566,38 +561,44 @@ def ada_glu_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_
     """(dx, dw_gate, dw_up, dbias_gate, dbias_up) of ada_glu, given g and u as it saved them:
     dg = dy u act'(g), du = dy act(g), dx = dg w_gate + du w_up, dw = d^T x, dbias the sums
     over rows; None for what is neither passed nor wanted."""
+    if stream is not None:
+        with _on(stream):
+            return ada_glu_backward(dy, x, w_gate, w_up, gate_pre, up_pre, act, dx, dw_gate, dw_up, dbias_gate,
+                                    dbias_up, want_dx, want_dw, want_dbias, workspace)
     rows, d_out, d_in = _sizes(x, w_gate)
-    dt, code, lib = _dtype(x), _act(act), _lib.load()
+    code, dc, dt, dev = _act(act), _dtype(x), x.dtype, x.get_device()
     if gate_pre is None or up_pre is None:
         raise ValueError("gate_pre and up_pre are needed for the slopes")
-    pdy, lddy = _mat(dy, rows, d_out, x, "dy")
-    px, ldx = _mat(x, rows, d_in, x, "x")
-    pg, ldg = _mat(w_gate, d_out, d_in, x, "w_gate")
-    pu, ldu = _mat(w_up, d_out, d_in, x, "w_up")
-    ppg, ldpg = _mat(gate_pre, rows, d_out, x, "gate_pre")
-    ppu, ldpu = _mat(up_pre, rows, d_out, x, "up_pre")
-    _mat(dx, rows, d_in, x, "dx")
-    _mat(dw_gate, d_out, d_in, x, "dw_gate")
-    _mat(dw_up, d_out, d_in, x, "dw_up")
-    _vec(dbias_gate, d_out, x, "dbias_gate")
-    _vec(dbias_up, d_out, x, "dbias_up")
-    _current(x)
+    pdy, lddy = _mat(dy, rows, d_out, dt, dev, "dy")
+    px, ldx = _mat(x, rows, d_in, dt, dev, "x")
+    pg, ldg = _mat(w_gate, d_out, d_in, dt, dev, "w_gate")
+    pu, ldu = _mat(w_up, d_out, d_in, dt, dev, "w_up")
+    ppg, ldpg = _mat(gate_pre, rows, d_out, dt, dev, "gate_pre")
+    ppu, ldpu = _mat(up_pre, rows, d_out, dt, dev, "up_pre")
+    pdx, lddx = _mat(dx, rows, d_in, dt, dev, "dx")
+    pdg, lddg = _mat(dw_gate, d_out, d_in, dt, dev, "dw_gate")
+    pdu, lddu = _mat(dw_up, d_out, d_in, dt, dev, "dw_up")
+    pbg = _vec(dbias_gate, d_out, dt, dev, "dbias_gate")
+    pbu = _vec(dbias_up, d_out, dt, dev, "dbias_up")
+    _current(dev)
 
-    def made(t, want, *shape):
-        return torch.empty(shape, dtype=x.dtype, device=x.device) if t is None and want else t
+    def made(t, p, ld, *shape):
+        if t is not None:
+            return t, p, ld
+        t = torch.empty(shape, dtype=dt, device=x.device)
+        return t, t.data_ptr(), shape[-1]
 
-    with _On(stream):
-        dx = made(dx, want_dx, rows, d_in)
-        dw_gate, dw_up = made(dw_gate, want_dw, d_out, d_in), made(dw_up, want_dw, d_out, d_in)
-        dbias_gate, dbias_up = made(dbias_gate, want_dbias, d_out), made(dbias_up, want_dbias, d_out)
-        pdx, lddx = _mat(dx, rows, d_in, x, "dx")
-        pdg, lddg = _mat(dw_gate, d_out, d_in, x, "dw_gate")
-        pdu, lddu = _mat(dw_up, d_out, d_in, x, "dw_up")
-        pbg = _vec(dbias_gate, d_out, x, "dbias_gate")
-        pbu = _vec(dbias_up, d_out, x, "dbias_up")
-        ws, nbytes, _keep = _workspace(lib.ada_glu_backward_workspace(rows, d_out, d_in, code, dt), workspace, x,
-                                       "ada_glu_backward_workspace")
-        args = AdaGluGradArgs(pdy, px, pg, pu, ppg, ppu, pdx, pdg, pdu, pbg, pbu, lddy, ldx, ldg, ldu, ldpg, ldpu,
-                              lddx, lddg, lddu, rows, d_out, d_in)
-        _check(lib.ada_glu_backward(args, code, dt, ws, nbytes, _stream(stream)), "ada_glu_backward")
+    if want_dx:
+        dx, pdx, lddx = made(dx, pdx, lddx, rows, d_in)
+    if want_dw:
+        dw_gate, pdg, lddg = made(dw_gate, pdg, lddg, d_out, d_in)
+        dw_up, pdu, lddu = made(dw_up, pdu, lddu, d_out, d_in)
+    if want_dbias:
+        dbias_gate, pbg, _ = made(dbias_gate, pbg, 0, d_out)
+        dbias_up, pbu, _ = made(dbias_up, pbu, 0, d_out)
+    ws, nbytes, _keep = _workspace(_workspace_bytes("ada_glu_backward_workspace", rows, d_out, d_in, code, dc),
+                                   workspace, dev)
+    args = AdaGluGradArgs(pdy, px, pg, pu, ppg, ppu, pdx, pdg, pdu, pbg, pbu, lddy, ldx, ldg, ldu, ldpg, ldpu, lddx,
+                          lddg, lddu, rows, d_out, d_in)
+    _check(_lib.load().ada_glu_backward(args, code, dc, ws, nbytes, _raw_stream(dev)), "ada_glu_backward")
     return dx, dw_gate, dw_up, dbias_gate, dbias_up

@@ -141,6 +141,12 @@ struct GemmParams {
   int32_t tiles_n;
 };
 
+// One or two products in a grid: workgroups from `first` on belong to the second.
+struct GemmPair {
+  GemmParams a[2];
+  int32_t first;
+};
+
 // y, pre of eight consecutive columns n of row m, from the sums without the bias.
 template <typename T, bool GATED>
 __device__ __forceinline__ void finish8(const GemmParams& a, int64_t m, int64_t n, float (&z)[GATED ? 2 : 1][8]) {
@@ -226,8 +232,11 @@ struct TileConfig {
   static_assert((BM == BN || U % 2 == 0) && U >= 5 && lds <= 160 * 1024 && copies(U - 3) < 64, "ring");
 };
 
-template <typename T, typename C, bool GATED, bool PARTIAL>
-__global__ void __launch_bounds__(C::threads, C::per_simd) gemm_kernel(GemmParams a) {
+template <typename T, typename C, bool GATED>
+__global__ void __launch_bounds__(C::threads, C::per_simd) gemm_kernel(GemmPair pair) {
+  const int second = static_cast<int>(blockIdx.x) >= pair.first;
+  const GemmParams& a = pair.a[second];
+  const int block = static_cast<int>(blockIdx.x) - (second ? pair.first : 0);
   constexpr int NQ = GATED ? 2 : 1;
   constexpr int FM = C::BM / C::WM / 32, FN = C::BN / C::WN / 32;
   constexpr int CC = C::BN / NQ;  // output columns of a tile
@@ -238,7 +247,7 @@ __global__ void __launch_bounds__(C::threads, C::per_simd) gemm_kernel(GemmParam
   // consecutive workgroups go to the 8 XCDs in turn: give each XCD a run of tiles, walked
   // down groups of 8 row bands so that its L2 serves a compact block of the output
   const int total = a.tiles_m * a.tiles_n;
-  const int split = blockIdx.x / total, b = blockIdx.x - split * total;
+  const int split = block / total, b = block - split * total;
   const int xcd = b & 7, per = total >> 3, more = total & 7;
   const int tile = xcd * per + (xcd < more ? xcd : more) + (b >> 3);
   constexpr int kGroup = 8;
@@ -256,7 +265,7 @@ __global__ void __launch_bounds__(C::threads, C::per_simd) gemm_kernel(GemmParam
 
   // With one row band no W is shared between workgroups: each starts elsewhere in k, or all of
   // them would read the same few memory channels at a time.
-  const int turn = a.tiles_m == 1 && full > 0 ? static_cast<int>(blockIdx.x % 4096 * 61 % full) : 0;
+  const int turn = a.tiles_m == 1 && full > 0 ? block % 4096 * 61 % full : 0;
 
   // where this lane reads: copy j of the wave fills rows 8 (wave copies + j) + lane / 8 of a unit
   constexpr int kCopies[2] = {C::copies_p, C::copies_q};
@@ -401,7 +410,7 @@ __global__ void __launch_bounds__(C::threads, C::per_simd) gemm_kernel(GemmParam
         const float* from = win + r * C::win_pitch + (GATED ? (nc >> 4) * 32 + h * 16 + (nc & 15) : nc);
         load8(from, z[h]);
       }
-      if constexpr (PARTIAL) {
+      if (a.splits > 1) {
 #pragma unroll
         for (int h = 0; h < NQ; ++h) store8(a.part + ((int64_t(split) * NQ + h) * a.rows + m) * a.cols + n, z[h]);
       } else {
@@ -411,12 +420,12 @@ __global__ void __launch_bounds__(C::threads, C::per_simd) gemm_kernel(GemmParam
   }
 }
 
-// Join a split contraction: the parts' sums in order, then the epilogue.
+// Join a split contraction: eight columns per thread, the parts' sums in order, then the epilogue.
 template <typename T, bool GATED>
-__global__ void __launch_bounds__(256) join_kernel(GemmParams a) {
+__device__ __forceinline__ void join_parts(const GemmParams& a, int block) {
   constexpr int NQ = GATED ? 2 : 1;
   const int64_t groups = a.rows * (a.cols / 8);
-  const int64_t v = blockIdx.x * 256ll + threadIdx.x;
+  const int64_t v = block * 256ll + threadIdx.x;
   if (v >= groups) return;
   const int64_t m = v / (a.cols / 8);
   const int64_t n = (v - m * (a.cols / 8)) * 8;
@@ -440,6 +449,51 @@ __global__ void __launch_bounds__(256) join_kernel(GemmParams a) {
           if (s0 + s < a.splits) z[h][e] += t[s][h][e];
   }
   finish8<T, GATED>(a, m, n, z);
+}
+
+// dbias: the slope tiles' column sums in a fixed order, four chains per column; blocks of 64
+// columns, first dbias[0]'s, then dbias[1]'s.
+struct BiasParams {
+  const float* sums;  // [tiles][parts][cols]
+  int64_t tiles;
+  int32_t parts;
+  int32_t cols;
+  void* db[2];
+};
+
+template <typename T>
+__device__ __forceinline__ void join_bias(const BiasParams& b, int block) {
+  __shared__ float part[4][64];
+  const int per = (b.cols + 63) / 64, h = block >= per;
+  const int c = threadIdx.x & 63, w = threadIdx.x >> 6, n = (block - h * per) * 64 + c;
+  float s = 0.f;
+  if (n < b.cols)
+    for (int64_t i = w; i < b.tiles; i += 4) s += b.sums[(i * b.parts + h) * b.cols + n];
+  part[w][c] = s;
+  __syncthreads();
+  T* db = static_cast<T*>(b.db[h]);
+  if (w == 0 && n < b.cols && db != nullptr)
+    db[n] = from_f32<T>((part[0][c] + part[1][c]) + (part[2][c] + part[3][c]));
+}
+
+// What is left after the products, in one launch: up to two joins, then dbias.
+struct JoinParams {
+  GemmPair pair;       // first: blocks of the first join
+  int32_t bias_first;  // blocks of both joins
+  BiasParams bias;
+};
+
+template <typename T, bool GATED>
+__global__ void __launch_bounds__(256) join_kernel(JoinParams j) {
+  const int block = static_cast<int>(blockIdx.x);
+  if constexpr (!GATED) {
+    if (block >= j.bias_first) {
+      join_bias<T>(j.bias, block - j.bias_first);
+      return;
+    }
+  }
+  const int second = block >= j.pair.first;
+  join_parts<T, GATED>(j.pair.a[second], block - (second ? j.pair.first : 0));
 }
 
 // ---- few rows ------------------------------------------------------------------------
@@ -702,71 +756,149 @@ constexpr float kStep16[kTiles] = {1.5f, 0.93f, 0.93f, 0.60f, 0.45f, 0.30f};
 constexpr float kStep32[kTiles] = {7.5f, 3.9f, 3.9f, 2.05f, 1.1f, 0.65f};
 constexpr float kRest[kTiles] = {12.f, 6.f, 6.f, 4.5f, 3.5f, 3.f};
 
+#define ADA_TRY(call) \
+  if (const hipError_t e_ = (call); e_ != hipSuccess) return e_
+
+// Launch n = 1 or 2 products (their splits set) as one grid of this tile.
 template <typename T, typename C, bool GATED>
-hipError_t launch_tiles(GemmParams a, hipStream_t s) {
+hipError_t launch_tiles(const GemmParams* a, int n, hipStream_t s) {
   constexpr int cc = C::BN / (GATED ? 2 : 1);
-  a.tiles_m = static_cast<int32_t>((a.rows + C::BM - 1) / C::BM);
-  a.tiles_n = (a.cols + cc - 1) / cc;
-  const unsigned grid = static_cast<unsigned>(a.tiles_m) * a.tiles_n * a.splits;
-  if (a.splits > 1) {
-    gemm_kernel<T, C, GATED, true><<<grid, C::threads, 0, s>>>(a);
-    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    const int64_t groups = a.rows * (a.cols / 8);
-    join_kernel<T, GATED><<<static_cast<unsigned>((groups + 255) / 256), 256, 0, s>>>(a);
-  } else {
-    gemm_kernel<T, C, GATED, false><<<grid, C::threads, 0, s>>>(a);
+  GemmPair pair{};
+  int64_t grid = 0;
+  for (int i = 0; i < n; ++i) {
+    pair.a[i] = a[i];
+    pair.a[i].tiles_m = static_cast<int32_t>((a[i].rows + C::BM - 1) / C::BM);
+    pair.a[i].tiles_n = (a[i].cols + cc - 1) / cc;
+    if (i == 1) pair.first = static_cast<int32_t>(grid);
+    grid += int64_t(pair.a[i].tiles_m) * pair.a[i].tiles_n * a[i].splits;
   }
+  if (n == 1) pair.first = static_cast<int32_t>(grid);
+  gemm_kernel<T, C, GATED><<<static_cast<unsigned>(grid), C::threads, 0, s>>>(pair);
   return hipGetLastError();
 }
 
-// Which tile, and into how many parts the contraction is split: the least sum of rounds (256
+template <typename T, bool GATED>
+hipError_t launch_products(int tile, const GemmParams* a, int n, hipStream_t s) {
+  switch (tile) {
+    case 0: return launch_tiles<T, Tile0, GATED>(a, n, s);
+    case 1: return launch_tiles<T, Tile1, GATED>(a, n, s);
+    case 2: return launch_tiles<T, Tile2, GATED>(a, n, s);
+    case 3: return launch_tiles<T, Tile3, GATED>(a, n, s);
+    case 4: return launch_tiles<T, Tile4, GATED>(a, n, s);
+    default: return launch_tiles<T, Tile5, GATED>(a, n, s);
+  }
+}
+
+// The joins of n products (those with splits > 1), and dbias where asked for.
+template <typename T, bool GATED>
+hipError_t launch_joins(const GemmParams* a, int n, const BiasParams* bias, hipStream_t s) {
+  JoinParams j{};
+  int64_t grid = 0;
+  int used = 0;
+  for (int i = 0; i < n; ++i) {
+    if (a[i].splits <= 1) continue;
+    j.pair.a[used++] = a[i];
+    grid += (a[i].rows * (a[i].cols / 8) + 255) / 256;
+    if (used == 1) j.pair.first = static_cast<int32_t>(grid);
+  }
+  j.bias_first = static_cast<int32_t>(grid);
+  if (bias != nullptr) {
+    j.bias = *bias;
+    grid += int64_t(bias->parts) * ((bias->cols + 63) / 64);
+  }
+  if (grid == 0) return hipSuccess;
+  join_kernel<T, GATED><<<static_cast<unsigned>(grid), 256, 0, s>>>(j);
+  return hipGetLastError();
+}
+
+// Which tile, and into how many parts a contraction is split: the least sum of rounds (256
 // workgroups at a time, one per CU) times the steps and the rest of each, and for a split the
 // join: a launch, and its parts written and read at about 4 TB/s.
 struct Plan {
   int tile;
   int splits;
+  float us;
 };
 
-Plan plan_gemm(int64_t rows, int64_t cols, int64_t depth, int gated, int esz) {
-  const int64_t n = gated ? 2 * cols : cols, steps = (depth * esz + 127) / 128;
-  Plan best{0, 1};
-  float least = -1.f;
-  for (int t = 0; t < kTiles; ++t) {
-    const int64_t tiles = ((rows + kTileRows[t] - 1) / kTileRows[t]) * ((n + kTileCols[t] - 1) / kTileCols[t]);
-    const float step = esz == 2 ? kStep16[t] : kStep32[t];
-    for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
-      if (splits > 1 && (steps / splits < 3 || tiles * splits > 1024)) break;
-      const float rounds = static_cast<float>((tiles * splits + 255) / 256);
-      float us = rounds * (static_cast<float>((steps + splits - 1) / splits) * step + kRest[t]);
-      if (splits > 1) us += 3.f + static_cast<float>(splits * n * rows) * 8.f / 4e6f;
-      if (least < 0.f || us < least) {
-        least = us;
-        best = {t, splits};
-      }
-    }
+struct Product {
+  int64_t rows, cols, depth;  // cols: of all products together
+  int esz;
+  int64_t steps() const { return (depth * esz + 127) / 128; }
+  int64_t tiles(int t) const {
+    return ((rows + kTileRows[t] - 1) / kTileRows[t]) * ((cols + kTileCols[t] - 1) / kTileCols[t]);
   }
+  float one(int t, int splits) const {  // a workgroup's time
+    return static_cast<float>((steps() + splits - 1) / splits) * (esz == 2 ? kStep16[t] : kStep32[t]) + kRest[t];
+  }
+  float join(int splits) const { return splits > 1 ? static_cast<float>(splits * cols * rows) * 2e-6f : 0.f; }
+  bool may_split(int t, int splits) const {
+    return splits == 1 || (steps() / splits >= 3 && tiles(t) * splits <= 1024);
+  }
+};
+constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
+constexpr float kLaunch = 3.f;
+
+Plan plan_product(const Product& p) {
+  Plan best{0, 1, -1.f};
+  for (int t = 0; t < kTiles; ++t)
+    for (int splits : kSplits) {
+      if (!p.may_split(t, splits)) break;
+      const float us = static_cast<float>((p.tiles(t) * splits + 255) / 256) * p.one(t, splits) + p.join(splits) +
+                       (splits > 1 ? kLaunch : 0.f);
+      if (best.us < 0.f || us < best.us) best = {t, splits, us};
+    }
   return best;
 }
 
-int64_t plan_bytes(const Plan& p, int64_t rows, int64_t cols, int gated) {
-  return p.splits > 1 ? int64_t(p.splits) * (gated ? 2 : 1) * rows * cols * 4 : 0;
+// Two products: one after the other with a tile each, or side by side in one grid with one
+// tile, which fills the CUs that the other's last round leaves idle.
+struct PairPlan {
+  bool together;
+  Plan plan[2];
+};
+
+PairPlan plan_pair(const Product& p, const Product& q) {
+  PairPlan best{false, {plan_product(p), plan_product(q)}};
+  float least = best.plan[0].us + best.plan[1].us + kLaunch;
+  for (int t = 0; t < kTiles; ++t)
+    for (int sp : kSplits) {
+      if (!p.may_split(t, sp)) break;
+      for (int sq : kSplits) {
+        if (!q.may_split(t, sq)) break;
+        const int64_t np = p.tiles(t) * sp, nq = q.tiles(t) * sq;
+        const float op = p.one(t, sp), oq = q.one(t, sq), more = op > oq ? op : oq, less = op > oq ? oq : op;
+        // one round: the longer; else the work shared by all, and half of a short workgroup idle at the end
+        const float all = (static_cast<float>(np) * op + static_cast<float>(nq) * oq) / 256.f + 0.5f * less;
+        float us = np + nq <= 256 || all < more ? more : all;
+        us += p.join(sp) + q.join(sq) + (sp > 1 || sq > 1 ? kLaunch : 0.f);
+        if (us < least) {
+          least = us;
+          best = {true, {{t, sp, op}, {t, sq, oq}}};
+        }
+      }
+    }
+  return best;
+}
+
+int64_t part_bytes(const Product& p, int splits) { return splits > 1 ? splits * p.rows * p.cols * 4 : 0; }
+
+// A forward product's plan.  Few rows have a kernel of their own and come here only with rows
+// too far apart for it: no workspace for them.
+Plan plan_forward(int64_t rows, int64_t cols, int64_t depth, int gated, int esz) {
+  Plan p = plan_product({rows, gated ? 2 * cols : cols, depth, esz});
+  if (rows <= kFewRows) p = {kTiles - 1, 1, 0.f};
+  return p;
 }
 
 template <typename T, bool GATED>
-hipError_t launch_gemm(GemmParams a, float* part, hipStream_t s) {
+hipError_t launch_forward(GemmParams a, float* part, hipStream_t s) {
   if (a.rows == 1) return launch_one_row<T, GATED>(a, s);
   if (few_rows(a, GATED, sizeof(T))) return launch_few_rows<T, GATED>(a, s);
-  const Plan p = plan_gemm(a.rows, a.cols, a.depth, GATED, sizeof(T));
+  const Plan p = plan_forward(a.rows, a.cols, a.depth, GATED, sizeof(T));
   a.splits = p.splits;
   a.part = part;
-  switch (p.tile) {
-    case 0: return launch_tiles<T, Tile0, GATED>(a, s);
-    case 1: return launch_tiles<T, Tile1, GATED>(a, s);
-    case 2: return launch_tiles<T, Tile2, GATED>(a, s);
-    case 3: return launch_tiles<T, Tile3, GATED>(a, s);
-    case 4: return launch_tiles<T, Tile4, GATED>(a, s);
-    default: return launch_tiles<T, Tile5, GATED>(a, s);
-  }
+  ADA_TRY((launch_products<T, GATED>(p.tile, &a, 1, s)));
+  return launch_joins<T, GATED>(&a, 1, nullptr, s);
 }
 
 // ---- slopes and transposed copies ----------------------------------------------------
@@ -790,21 +922,33 @@ __device__ __forceinline__ void store_transposed(const T (*t)[kSide + 16 / sizeo
 
 // out[j][i] = m[i][j] for an [n_rows][cols] matrix and i < n_out, a multiple of 16 bytes; zeros
 // from n_rows on.
+struct TransposeJob {
+  MatIn m;
+  void* out;
+  int64_t ld_out;
+  int64_t n_out;
+  int64_t n_rows;
+  int64_t cols;
+  int32_t tiles_n;
+  int32_t first;  // its first block
+};
+
 template <typename T>
-__global__ void __launch_bounds__(256) transpose_kernel(MatIn m, T* out, int64_t ld_out, int64_t n_out,
-                                                        int64_t n_rows, int64_t cols, int64_t tiles_n) {
+using SideTile = T[kSide][kSide + 16 / sizeof(T)];
+
+template <typename T>
+__device__ __forceinline__ void transpose_tile(const TransposeJob& j, int block, SideTile<T>& t) {
   constexpr int VEC = 16 / sizeof(T), PER = kSide / VEC;
-  __shared__ __attribute__((aligned(16))) T t[kSide][kSide + VEC];
-  const int64_t m0 = (blockIdx.x / tiles_n) * kSide, n0 = (blockIdx.x % tiles_n) * kSide;
+  const int64_t m0 = int64_t(block / j.tiles_n) * kSide, n0 = int64_t(block % j.tiles_n) * kSide;
   for (int v = threadIdx.x; v < kSide * PER; v += 256) {
     const int r = v / PER, n = (v % PER) * VEC;
     Vec16<T> d = {};
-    if (m0 + r < n_rows && n0 + n < cols)
-      d = *reinterpret_cast<const Vec16<T>*>(static_cast<const T*>(m.p) + (m0 + r) * m.ld + n0 + n);
+    if (m0 + r < j.n_rows && n0 + n < j.cols)
+      d = *reinterpret_cast<const Vec16<T>*>(static_cast<const T*>(j.m.p) + (m0 + r) * j.m.ld + n0 + n);
     *reinterpret_cast<Vec16<T>*>(&t[r][n]) = d;
   }
   __syncthreads();
-  store_transposed<T>(t, out, ld_out, m0, n_out, n0, cols);
+  store_transposed<T>(t, static_cast<T*>(j.out), j.ld_out, m0, j.n_out, n0, j.cols);
 }
 
 struct SlopeParams {
@@ -824,12 +968,11 @@ struct SlopeParams {
 // dz = dy act'(z), or dg = dy u act'(g), du = dy act(g), in every form the products and the
 // bias gradients read, in one pass over dy and the saved pre-activations.
 template <typename T, bool GATED>
-__global__ void __launch_bounds__(256) slope_kernel(SlopeParams a) {
+__device__ __forceinline__ void slope_tile(const SlopeParams& a, int block, SideTile<T> (&t)[GATED ? 2 : 1]) {
   constexpr int VEC = 16 / sizeof(T), PER = kSide / VEC, RSTEP = 256 / PER;
   constexpr int NQ = GATED ? 2 : 1;
-  __shared__ __attribute__((aligned(16))) T t[NQ][kSide][kSide + VEC];
   __shared__ float part[RSTEP][kSide];
-  const int64_t m0 = int64_t(blockIdx.x / a.tiles_n) * kSide, n0 = int64_t(blockIdx.x % a.tiles_n) * kSide;
+  const int64_t m0 = int64_t(block / a.tiles_n) * kSide, n0 = int64_t(block % a.tiles_n) * kSide;
   const int n = (threadIdx.x % PER) * VEC;
   float sum[NQ][VEC] = {};
   for (int r = threadIdx.x / PER; r < kSide; r += RSTEP) {
@@ -881,26 +1024,33 @@ __global__ void __launch_bounds__(256) slope_kernel(SlopeParams a) {
       if (threadIdx.x < kSide && n0 + threadIdx.x < a.cols) {
         float s = 0.f;
         for (int r = 0; r < RSTEP; ++r) s += part[r][threadIdx.x];
-        a.sums[(int64_t(blockIdx.x / a.tiles_n) * NQ + h) * a.cols + n0 + threadIdx.x] = s;
+        a.sums[(int64_t(block / a.tiles_n) * NQ + h) * a.cols + n0 + threadIdx.x] = s;
       }
     }
   }
 }
 
-// dbias: the tiles' column sums in a fixed order, four chains per column.
-template <typename T>
-__global__ void __launch_bounds__(256) bias_grad_kernel(const float* sums, int64_t tiles, int parts, int cols, T* db0,
-                                                        T* db1) {
-  __shared__ float part[4][64];
-  const int c = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int h = blockIdx.y, n = blockIdx.x * 64 + c;
-  float s = 0.f;
-  if (n < cols)
-    for (int64_t i = w; i < tiles; i += 4) s += sums[(i * parts + h) * cols + n];
-  part[w][c] = s;
-  __syncthreads();
-  T* db = h == 0 ? db0 : db1;
-  if (w == 0 && n < cols && db != nullptr) db[n] = from_f32<T>((part[0][c] + part[1][c]) + (part[2][c] + part[3][c]));
+// Everything the products of a backward pass read, in one launch: slope tiles first, then the
+// tiles of the transposed copies.
+constexpr int kJobs = 3;  // both weights and x
+struct PrepareParams {
+  SlopeParams slope;
+  TransposeJob job[kJobs];
+  int32_t slope_blocks;
+  int32_t jobs;
+};
+
+template <typename T, bool GATED>
+__global__ void __launch_bounds__(256) prepare_kernel(PrepareParams p) {
+  __shared__ __attribute__((aligned(16))) SideTile<T> t[GATED ? 2 : 1];
+  const int block = static_cast<int>(blockIdx.x);
+  if (block < p.slope_blocks) {
+    slope_tile<T, GATED>(p.slope, block, t);
+    return;
+  }
+  int j = 0;
+  while (j < p.jobs - 1 && block >= p.job[j + 1].first) ++j;
+  transpose_tile<T>(p.job[j], block - p.job[j].first, t[0]);
 }
 
 template <typename T>
@@ -920,16 +1070,17 @@ hipError_t launch_linear_t(const LinearParams& p, void* ws, hipStream_t s) {
   a.cols = p.d_out;
   a.depth = p.d_in;
   a.act = p.act;
-  return p.gated ? launch_gemm<T, true>(a, static_cast<float*>(ws), s)
-                 : launch_gemm<T, false>(a, static_cast<float*>(ws), s);
+  return p.gated ? launch_forward<T, true>(a, static_cast<float*>(ws), s)
+                 : launch_forward<T, false>(a, static_cast<float*>(ws), s);
 }
 
 // Workspace of a backward pass (byte offsets): dz [rows][parts d_out] and the weights'
 // transposed copy [d_in][parts d_out] for dx; dz transposed [parts d_out][ld_t] and x
 // transposed [d_in][ld_t] for dW; column sums for dbias; parts of a split contraction.
 struct GradPlan {
-  int64_t dz, wt, dzt, xt, sums, part, total;
+  int64_t dz, wt, dzt, xt, sums, part[2], total;
   int64_t ld_t;
+  PairPlan pair;  // dx, dW: the same whichever of the two is asked for, and so are their sums
 };
 
 GradPlan plan_grad(int64_t rows, int64_t n, int64_t k, int act, int gated, int esz) {
@@ -946,19 +1097,11 @@ GradPlan plan_grad(int64_t rows, int64_t n, int64_t k, int act, int gated, int e
   g.dzt = take(parts * n * g.ld_t * esz);
   g.xt = take(k * g.ld_t * esz);
   g.sums = take((rows + kSide - 1) / kSide * parts * n * 4);
-  const int64_t dx = plan_bytes(plan_gemm(rows, k, parts * n, 0, esz), rows, k, 0);
-  const int64_t dw2 = plan_bytes(plan_gemm(parts * n, k, g.ld_t, 0, esz), parts * n, k, 0);
-  const int64_t dw1 = plan_bytes(plan_gemm(n, k, g.ld_t, 0, esz), n, k, 0);
-  g.part = take(dx > dw2 ? (dx > dw1 ? dx : dw1) : (dw2 > dw1 ? dw2 : dw1));
+  const Product dx{rows, k, parts * n, esz}, dw{parts * n, k, g.ld_t, esz};
+  g.pair = plan_pair(dx, dw);
+  g.part[0] = take(part_bytes(dx, g.pair.plan[0].splits));
+  g.part[1] = take(part_bytes(dw, g.pair.plan[1].splits));
   return g;
-}
-
-template <typename T>
-hipError_t launch_transpose(const MatIn& m, T* out, int64_t ld_out, int64_t n_out, int64_t n_rows, int64_t cols,
-                            hipStream_t s) {
-  const int64_t tm = (n_out + kSide - 1) / kSide, tn = (cols + kSide - 1) / kSide;
-  transpose_kernel<T><<<static_cast<unsigned>(tm * tn), 256, 0, s>>>(m, out, ld_out, n_out, n_rows, cols, tn);
-  return hipGetLastError();
 }
 
 template <typename T>
@@ -974,9 +1117,6 @@ hipError_t launch_zero(const MatOut& y, int64_t rows, int64_t cols, hipStream_t 
   zero_kernel<T><<<static_cast<unsigned>(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(y, rows, cols);
   return hipGetLastError();
 }
-
-#define ADA_TRY(call) \
-  if (const hipError_t e_ = (call); e_ != hipSuccess) return e_
 
 template <typename T>
 hipError_t launch_linear_grad_t(const LinearGradParams& p, void* ws, hipStream_t s) {
@@ -994,12 +1134,12 @@ hipError_t launch_linear_grad_t(const LinearGradParams& p, void* ws, hipStream_t
   T* wt = reinterpret_cast<T*>(base + g.wt);
   T* dzt = reinterpret_cast<T*>(base + g.dzt);
   T* xt = reinterpret_cast<T*>(base + g.xt);
-  float* part = reinterpret_cast<float*>(base + g.part);
   const bool want_dx = p.dx.p != nullptr, want_dw = p.dw[0].p != nullptr || p.dw[1].p != nullptr;
   const bool want_db = p.dbias[0] != nullptr || p.dbias[1] != nullptr;
   const bool own_dz = p.gated || p.act != ADA_ACT_NONE;  // else dz is dy
 
-  SlopeParams sl{};
+  PrepareParams pre{};
+  SlopeParams& sl = pre.slope;
   sl.dy = p.dy;
   sl.pre[0] = p.pre[0];
   sl.pre[1] = p.pre[1];
@@ -1013,55 +1153,71 @@ hipError_t launch_linear_grad_t(const LinearGradParams& p, void* ws, hipStream_t
   sl.tiles_n = (p.d_out + kSide - 1) / kSide;
   sl.act = p.act;
   const int64_t tiles_m = (p.rows + kSide - 1) / kSide;
-  if (sl.dz != nullptr || sl.dzt != nullptr || sl.sums != nullptr) {
-    const unsigned grid = static_cast<unsigned>(tiles_m * sl.tiles_n);
-    if (p.gated)
-      slope_kernel<T, true><<<grid, 256, 0, s>>>(sl);
-    else
-      slope_kernel<T, false><<<grid, 256, 0, s>>>(sl);
-    ADA_TRY(hipGetLastError());
+  int64_t blocks = sl.dz != nullptr || sl.dzt != nullptr || sl.sums != nullptr ? tiles_m * sl.tiles_n : 0;
+  pre.slope_blocks = static_cast<int32_t>(blocks);
+  auto transpose = [&](const MatIn& m, T* out, int64_t ld_out, int64_t n_out, int64_t n_rows, int64_t cols) {
+    const int64_t tn = (cols + kSide - 1) / kSide;
+    pre.job[pre.jobs++] = {m, out, ld_out, n_out, n_rows, cols, static_cast<int32_t>(tn), static_cast<int32_t>(blocks)};
+    blocks += (n_out + kSide - 1) / kSide * tn;
+  };
+  if (want_dx)
+    for (int h = 0; h < parts; ++h) transpose(p.w[h], wt + h * n, parts * n, n, n, k);
+  if (want_dw) transpose(p.x, xt, g.ld_t, g.ld_t, p.rows, k);
+  if (p.gated)
+    prepare_kernel<T, true><<<static_cast<unsigned>(blocks), 256, 0, s>>>(pre);
+  else
+    prepare_kernel<T, false><<<static_cast<unsigned>(blocks), 256, 0, s>>>(pre);
+  ADA_TRY(hipGetLastError());
+
+  GemmParams a[2] = {};
+  int tile[2], count = 0;
+  auto add = [&](int i) {  // product i of the pair is a[count]
+    a[count].splits = g.pair.plan[i].splits;
+    a[count].part = reinterpret_cast<float*>(base + g.part[i]);
+    tile[count] = g.pair.plan[i].tile;
+    return &a[count++];
+  };
+  // longer workgroups first
+  for (int i : {g.pair.plan[0].us >= g.pair.plan[1].us ? 0 : 1, g.pair.plan[0].us >= g.pair.plan[1].us ? 1 : 0}) {
+    if (i == 0 && want_dx) {
+      GemmParams* d = add(0);
+      d->p = own_dz ? MatIn{base + g.dz, parts * n} : p.dy;
+      d->q[0] = MatIn{wt, parts * n};
+      d->y[0] = p.dx;
+      d->rows = p.rows;
+      d->row_split = p.rows;
+      d->cols = p.d_in;
+      d->depth = parts * n;
+    } else if (i == 1 && want_dw) {
+      const bool both = p.gated && p.dw[0].p != nullptr && p.dw[1].p != nullptr;
+      const int h = p.dw[0].p != nullptr ? 0 : 1;
+      GemmParams* d = add(1);
+      d->p = MatIn{dzt + h * n * g.ld_t, g.ld_t};
+      d->q[0] = MatIn{xt, g.ld_t};
+      d->y[0] = p.dw[h];
+      d->y[1] = p.dw[1];
+      d->rows = both ? 2 * n : n;
+      d->row_split = n;
+      d->cols = p.d_in;
+      d->depth = g.ld_t;
+    }
   }
-  if (want_db) {
-    bias_grad_kernel<T><<<dim3((p.d_out + 63) / 64, parts), 256, 0, s>>>(sl.sums, tiles_m, parts, p.d_out,
-                                                                         static_cast<T*>(p.dbias[0]),
-                                                                         static_cast<T*>(p.dbias[1]));
-    ADA_TRY(hipGetLastError());
+  if (count == 2 && g.pair.together) {
+    ADA_TRY((launch_products<T, false>(tile[0], a, 2, s)));
+  } else {
+    for (int i = 0; i < count; ++i) ADA_TRY((launch_products<T, false>(tile[i], a + i, 1, s)));
   }
-  if (want_dx) {
-    for (int h = 0; h < parts; ++h) ADA_TRY(launch_transpose<T>(p.w[h], wt + h * n, parts * n, n, n, k, s));
-    GemmParams a{};
-    a.p = own_dz ? MatIn{base + g.dz, parts * n} : p.dy;
-    a.q[0] = MatIn{wt, parts * n};
-    a.y[0] = p.dx;
-    a.rows = p.rows;
-    a.row_split = p.rows;
-    a.cols = p.d_in;
-    a.depth = parts * n;
-    ADA_TRY((launch_gemm<T, false>(a, part, s)));
-  }
-  if (want_dw) {
-    ADA_TRY(launch_transpose<T>(p.x, xt, g.ld_t, g.ld_t, p.rows, k, s));
-    const bool both = p.gated && p.dw[0].p != nullptr && p.dw[1].p != nullptr;
-    const int h = p.dw[0].p != nullptr ? 0 : 1;
-    GemmParams a{};
-    a.p = MatIn{dzt + h * n * g.ld_t, g.ld_t};
-    a.q[0] = MatIn{xt, g.ld_t};
-    a.y[0] = p.dw[h];
-    a.y[1] = p.dw[1];
-    a.rows = both ? 2 * n : n;
-    a.row_split = n;
-    a.cols = p.d_in;
-    a.depth = g.ld_t;
-    ADA_TRY((launch_gemm<T, false>(a, part, s)));
-  }
-  return hipSuccess;
+  BiasParams bias{sl.sums, tiles_m, parts, p.d_out, {p.dbias[0], p.dbias[1]}};
+  return launch_joins<T, false>(a, count, want_db ? &bias : nullptr, s);
 }
 
 }  // namespace
 
 int64_t linear_workspace(int64_t rows, int32_t d_out, int32_t d_in, int gated, int dtype) {
   if (rows == 0) return 0;
-  return plan_bytes(plan_gemm(rows, d_out, d_in, gated, dtype == ADA_BF16 ? 2 : 4), rows, d_out, gated);
+  const int esz = dtype == ADA_BF16 ? 2 : 4;
+  return part_bytes({rows, gated ? 2 * int64_t(d_out) : d_out, d_in, esz},
+                    plan_forward(rows, d_out, d_in, gated, esz).splits);
 }
 
 int64_t linear_grad_workspace(int64_t rows, int32_t d_out, int32_t d_in, int act, int gated, int dtype) {
