@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(256) join_kernel(JoinParams j) {
 }
 
 // ---- few rows ------------------------------------------------------------------------
-// Two to 16 rows: bound by reading W once.  A workgroup takes 16 output columns (gated: of both
+// Two to 48 rows, in TB blocks of 16: bound by reading W once.  A workgroup takes 16 output columns (gated: of both
 // products) and its NW waves share the contraction in windows of 256 bytes of k, dealt out in
 // turn.  A wave streams its windows of W and of x through an LDS ring of its own, S windows
 // deep, by direct copies (4 rows x 256 bytes each), so no barrier is met before the end.
@@ -522,20 +522,20 @@ __device__ __forceinline__ void wait_copies() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-template <bool GATED, int NW, int S>
+template <bool GATED, int TB, int NW, int S>
 struct FewRows {
   static constexpr int NQ = GATED ? 2 : 1;
-  static constexpr int window = (NQ + 1) * 4096;  // bytes of a window: 16 rows of each W, then of x
-  static constexpr int pitch = 20;                // floats of a row of 16 sums
-  static constexpr int sums = NQ * 16 * pitch * 4;
+  static constexpr int window = (NQ + TB) * 4096;  // bytes of a window: 16 rows of each W, then blocks of x
+  static constexpr int pitch = 20;                 // floats of a row of 16 sums
+  static constexpr int sums = NQ * TB * 16 * pitch * 4;
   static constexpr int lds = NW * S * window;
-  static_assert(S >= 2 && S * window >= sums && lds <= 160 * 1024 && 4 * (S - 1) * (NQ + 1) < 64, "ring");
+  static_assert(S >= 2 && S * window >= sums && lds <= 160 * 1024 && 4 * (S - 1) * (NQ + TB) < 64, "ring");
 };
 
-template <typename T, bool GATED, int NW, int S>
+template <typename T, bool GATED, int TB, int NW, int S>
 __device__ __forceinline__ void few_rows_product(const GemmParams& a, unsigned char* lds) {
-  using F = FewRows<GATED, NW, S>;
-  constexpr int NQ = F::NQ, NO = NQ + 1;  // operands: the weights, then x
+  using F = FewRows<GATED, TB, NW, S>;
+  constexpr int NQ = F::NQ, NO = NQ + TB;  // operands: the weights, then x's blocks
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, q = lane >> 4;
   const int64_t col0 = int64_t(blockIdx.x) * 16;
@@ -559,7 +559,7 @@ __device__ __forceinline__ void few_rows_product(const GemmParams& a, unsigned c
 #pragma unroll
   for (int h = 0; h < NO; ++h) {
     const MatIn& o = h < NQ ? a.q[h] : a.p;
-    const int64_t ld = o.ld * int64_t(sizeof(T)), first = h < NQ ? col0 : 0, rows = h < NQ ? a.cols : a.rows;
+    const int64_t ld = o.ld * int64_t(sizeof(T)), first = h < NQ ? col0 : 16 * (h - NQ), rows = h < NQ ? a.cols : a.rows;
     const int64_t last = rows - 1 - first < 15 ? rows - 1 - first : 15;
     m[h] = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<unsigned char*>(static_cast<const unsigned char*>(o.p) + first * ld), 0,
@@ -596,7 +596,7 @@ __device__ __forceinline__ void few_rows_product(const GemmParams& a, unsigned c
         }
     }
   };
-  f32x4 acc[NQ] = {};
+  f32x4 acc[NQ][TB] = {};
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) copy_or_tail(i);
   for (int i = 0; i < n; ++i) {
@@ -610,9 +610,15 @@ __device__ __forceinline__ void few_rows_product(const GemmParams& a, unsigned c
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const int v = ((4 * s + q) ^ c) * 16;
-      const u32x4 x = *reinterpret_cast<const u32x4*>(at + NQ * 4096 + v);
+      u32x4 x[TB];
 #pragma unroll
-      for (int h = 0; h < NQ; ++h) acc[h] = mfma16<T>(*reinterpret_cast<const u32x4*>(at + h * 4096 + v), x, acc[h]);
+      for (int b = 0; b < TB; ++b) x[b] = *reinterpret_cast<const u32x4*>(at + (NQ + b) * 4096 + v);
+#pragma unroll
+      for (int h = 0; h < NQ; ++h) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(at + h * 4096 + v);
+#pragma unroll
+        for (int b = 0; b < TB; ++b) acc[h][b] = mfma16<T>(w, x[b], acc[h][b]);
+      }
     }
     // the window's reads are done before its slot is copied to again
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -623,7 +629,9 @@ __device__ __forceinline__ void few_rows_product(const GemmParams& a, unsigned c
   constexpr int kWave = F::sums / 4;
 #pragma unroll
   for (int h = 0; h < NQ; ++h)
-    *reinterpret_cast<f32x4*>(sums + wave * kWave + (h * 16 + c) * F::pitch + 4 * q) = acc[h];
+#pragma unroll
+    for (int b = 0; b < TB; ++b)
+      *reinterpret_cast<f32x4*>(sums + wave * kWave + ((h * TB + b) * 16 + c) * F::pitch + 4 * q) = acc[h][b];
   __syncthreads();
   for (int v = threadIdx.x; v < 2 * a.rows; v += 64 * NW) {
     const int r = v >> 1, nc = (v & 1) * 8;
@@ -634,7 +642,7 @@ __device__ __forceinline__ void few_rows_product(const GemmParams& a, unsigned c
 #pragma unroll
       for (int h = 0; h < NQ; ++h) {
         float t[8];
-        load8(sums + w * kWave + (h * 16 + r) * F::pitch + nc, t);
+        load8(sums + w * kWave + (h * TB * 16 + r) * F::pitch + nc, t);
 #pragma unroll
         for (int e = 0; e < 8; ++e) z[h][e] += t[e];
       }
@@ -642,18 +650,21 @@ __device__ __forceinline__ void few_rows_product(const GemmParams& a, unsigned c
   }
 }
 
-template <typename T, bool GATED, int NW, int S>
+template <typename T, bool GATED, int TB, int NW, int S>
 __global__ void __launch_bounds__(64 * NW) few_rows_kernel(GemmParams a) {
-  __shared__ __attribute__((aligned(16))) unsigned char lds[FewRows<GATED, NW, S>::lds];
-  few_rows_product<T, GATED, NW, S>(a, lds);
+  __shared__ __attribute__((aligned(16))) unsigned char lds[FewRows<GATED, TB, NW, S>::lds];
+  few_rows_product<T, GATED, TB, NW, S>(a, lds);
 }
 
-constexpr int kFewRows = 16;
+// Sizes that take the few-rows kernel.  Up to 32 rows it is ahead of the tiles everywhere (24 x
+// 4096 x 11008: 22.2 against 26.9 us); with a third block of x next to W only while the
+// workgroups fit twice on the card (48 x 4096 x 4096: 11.8 against 15.0 us, 48 x 11008 x 4096:
+// 31.5 against 26.8 us).
+bool few_rows_sizes(int64_t rows, int64_t cols) { return rows <= 32 || (rows <= 48 && cols <= 8192); }
 
-// Whether a product takes the few-rows kernel: up to 16 rows, within the 32-bit offsets of its
-// buffer copies.
+// ... and whose operands lie within the 32-bit offsets of its buffer copies.
 bool few_rows(const GemmParams& a, int gated, int esz) {
-  if (a.rows > kFewRows || a.row_split < a.rows) return false;
+  if (!few_rows_sizes(a.rows, a.cols)) return false;
   for (int h = 0; h < (gated ? 3 : 2); ++h)
     if ((15 * (h == 0 ? a.p : a.q[h - 1]).ld + a.depth) * esz >= (int64_t(1) << 31)) return false;
   return true;
@@ -663,7 +674,12 @@ template <typename T, bool GATED>
 hipError_t launch_few_rows(const GemmParams& a, hipStream_t s) {
   const unsigned grid = (a.cols + 15) / 16;
   constexpr int waves = GATED ? 4 : 8;
-  few_rows_kernel<T, GATED, waves, 2><<<grid, 64 * waves, 0, s>>>(a);
+  if (a.rows <= 16)
+    few_rows_kernel<T, GATED, 1, waves, 2><<<grid, 64 * waves, 0, s>>>(a);
+  else if (a.rows <= 32)
+    few_rows_kernel<T, GATED, 2, 4, 2><<<grid, 256, 0, s>>>(a);
+  else
+    few_rows_kernel<T, GATED, 3, 4, 2><<<grid, 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -886,7 +902,7 @@ int64_t part_bytes(const Product& p, int splits) { return splits > 1 ? splits * 
 // too far apart for it: no workspace for them.
 Plan plan_forward(int64_t rows, int64_t cols, int64_t depth, int gated, int esz) {
   Plan p = plan_product({rows, gated ? 2 * cols : cols, depth, esz});
-  if (rows <= kFewRows) p = {kTiles - 1, 1, 0.f};
+  if (few_rows_sizes(rows, cols)) p = {kTiles - 1, 1, 0.f};
   return p;
 }
 
