@@ -6,8 +6,8 @@
 //            dx = dz W (dg Wg + du Wu), dW = dz^T x, db = sum over rows of dz
 //
 // Every product is D(i, j) = sum_k P(i, k) Q(j, k) on the matrix instructions with fp32
-// sums and both operands read along k: x and W of the forward pass as they are, W of dx and
-// dz and x of dW from transposed copies in the workspace.  Matrix instruction layout (32 x
+// sums; an operand is read along k (x and W of the forward pass, dz of dx) or across it, k being
+// the row of its memory (W of dx, dz and x of dW).  Matrix instruction layout (32 x
 // 32 tile): lane l = 32 q + c supplies Q(c, k) as the row operand and P(c, k) as the column
 // operand for its k slice, and receives D(i = c, j = 8 g + 4 q + e) in register 4 g + e:
 // groups of four consecutive columns of an output row.  A 16-byte vector per lane feeds one
@@ -124,8 +124,10 @@ __device__ __forceinline__ float act_slope(float z, int act) {
 #define ADA_LDS __attribute__((address_space(3)))
 
 struct GemmParams {
-  MatIn p;                // [rows][depth]
-  MatIn q[2];             // [cols][depth]; gated: the gate's and the up projection's weights
+  MatIn p;                // [rows][depth]; dW: [depth][rows]
+  MatIn q[2];             // [cols][depth]; gated: the gate's and the up projection's weights;
+                          // dx: [depth][cols], q[1] from row `seam` on; dW: [depth][cols]
+  int64_t seam;
   const void* bias[2];
   MatIn res;
   MatOut y[2];            // rows from row_split on go to y[1] (the two halves of dW)
@@ -139,6 +141,14 @@ struct GemmParams {
   int32_t splits;
   int32_t tiles_m;
   int32_t tiles_n;
+  int32_t form;           // a Form
+};
+
+// How a product reads its operands.
+enum Form : int32_t {
+  kForward = 0,  // both along k
+  kDx = 1,       // P along, Q across
+  kDw = 2        // both across
 };
 
 // One or two products in a grid: workgroups from `first` on belong to the second.
@@ -210,12 +220,16 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 q, u32x4 p, f32x16 acc) {
 
 // A tile of BM x BN outputs (gated: BN counts the columns of both products, 16 of the gate's
 // next to 16 of the up projection's, so a wave holds both for its columns) by WM x WN waves.
-// A step is 128 bytes of k.  One operand's rows of one step are a unit; units go to LDS by
-// direct copies into a ring of U slots: 2 t holds P of step t, 2 t + 1 holds Q.  Vector v of a
-// staged row r lies at r * 128 + 16 (v ^ (r >> 1 & 7)), which spreads the rows of a fragment
-// read over all banks.  The depth's last part of a step (depth is a multiple of 16 bytes) goes
-// through registers, zeros behind its end.  Rows past an operand's end repeat its last row and
-// are not stored.
+// A step is 64 (bf16) or 32 (fp32) of k.  One operand's rows of one step are a unit; units go to
+// LDS by direct copies into a ring of U slots: 2 t holds P of step t, 2 t + 1 holds Q.  The
+// depth's last part of a step goes through registers, zeros behind its end.  Rows past an
+// operand's end repeat its last ones and are not stored.
+// A unit along k holds 128 bytes of every row: vector v of row r at r * 128 + 16 (v ^ (r >> 1 & 7)),
+// which spreads the 32 rows of a fragment read over all banks.  A unit across k holds the operand's
+// memory rows, one k each, read one k at a time: in bf16 a lane reads as many neighbouring columns
+// as its wave has fragments (F = 4: 8 bytes, F = 2: 4 bytes), fragment x taking columns F c + x,
+// and byte permutes pair the k of each column while the matrix instructions run.  Vector v of row
+// k lies at v ^ spread(k), so that the two halves of a wave, eight k apart, read different banks.
 template <int BM_, int BN_, int U_, int WAVES_PER_SIMD_>
 struct TileConfig {
   static constexpr int BM = BM_, BN = BN_, WM = 2, WN = 2, U = U_, waves = WM * WN;
@@ -227,20 +241,26 @@ struct TileConfig {
   static constexpr int lds = ring > waves * window ? ring : waves * window;
   // where slot s lies (an even ring keeps P in even slots)
   __device__ static int slot(int s) { return BM == BN ? s * BM * 128 : (s >> 1) * (BM + BN) * 128 + (s & 1) * BM * 128; }
+  // of a unit across k with B rows: vectors of a k, and where vector v of k lies
+  template <typename T, int B>
+  struct Across {
+    static constexpr int vecs = B * int(sizeof(T)) / 16;
+    __device__ static int spread(int k) { return sizeof(T) == 2 ? (8 * ((k >> 3) & 1)) & (vecs - 1) : 0; }
+  };
   // copies of n units from a P unit on
   static constexpr int copies(int n) { return (n + 1) / 2 * copies_p + n / 2 * copies_q; }
   static_assert((BM == BN || U % 2 == 0) && U >= 5 && lds <= 160 * 1024 && copies(U - 3) < 64, "ring");
 };
 
-template <typename T, typename C, bool GATED>
-__global__ void __launch_bounds__(C::threads, C::per_simd) gemm_kernel(GemmPair pair) {
-  const int second = static_cast<int>(blockIdx.x) >= pair.first;
-  const GemmParams& a = pair.a[second];
-  const int block = static_cast<int>(blockIdx.x) - (second ? pair.first : 0);
+template <typename T, typename C, bool GATED, int FORM>
+__device__ __forceinline__ void product(const GemmParams& a, int block, unsigned char* lds) {
+  constexpr bool kAcross[2] = {FORM == kDw, FORM != kForward};
+  constexpr int KS = 128 / sizeof(T), VEC = 16 / sizeof(T);  // k of a step, elements of a vector
+  using AP = typename C::template Across<T, C::BM>;
+  using AQ = typename C::template Across<T, C::BN>;
   constexpr int NQ = GATED ? 2 : 1;
   constexpr int FM = C::BM / C::WM / 32, FN = C::BN / C::WN / 32;
   constexpr int CC = C::BN / NQ;  // output columns of a tile
-  __shared__ __attribute__((aligned(16))) unsigned char lds[C::lds];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 31, q = lane >> 5;
 
@@ -265,30 +285,68 @@ __global__ void __launch_bounds__(C::threads, C::per_simd) gemm_kernel(GemmPair 
 
   // With one row band no W is shared between workgroups: each starts elsewhere in k, or all of
   // them would read the same few memory channels at a time.
-  const int turn = a.tiles_m == 1 && full > 0 ? block % 4096 * 61 % full : 0;
+  const int turn = FORM == kForward && a.tiles_m == 1 && full > 0 ? block % 4096 * 61 % full : 0;
 
-  // where this lane reads: copy j of the wave fills rows 8 (wave copies + j) + lane / 8 of a unit
+  // Where this lane reads.  Along k, copy j of the wave fills rows 8 (wave copies + j) + lane / 8
+  // of a unit; across it, rows of k.
   constexpr int kCopies[2] = {C::copies_p, C::copies_q};
   constexpr int kMost = C::copies_p > C::copies_q ? C::copies_p : C::copies_q;
+  constexpr int kVecs[2] = {AP::vecs, AQ::vecs};
+  auto unit_row = [&](int h, int j) {  // the unit's row (of its k) that copy j reads in this lane
+    const int per = kAcross[h] ? kVecs[h] : 8;
+    return 64 / per * (wave * kCopies[h] + j) + lane / per;
+  };
   const unsigned char* src[2][kMost];
+  int64_t by[2];                     // from a step to the next
+  const unsigned char* cross[kMost];  // dx: where a copy goes on in the second weight,
+  int cross_at[kMost];                // and from which step
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int h = 0; h < 2; ++h) {
+    by[h] = kAcross[h] ? (h == 0 ? a.p : a.q[0]).ld * int64_t(128) : 128;
 #pragma unroll
     for (int j = 0; j < kCopies[h]; ++j) {
-      const int r = 8 * (wave * kCopies[h] + j) + (lane >> 3);
+      const int r = unit_row(h, j);
+      const int64_t n = h == 0 ? a.rows : a.cols;
+      if constexpr (kAcross[0] || kAcross[1]) {
+        if (kAcross[h]) {
+          const int v = (lane % kVecs[h]) ^ (h == 0 ? AP::spread(r) : AQ::spread(r));
+          const int64_t at = (h == 0 ? row0 : col0) + v * VEC, i = at < n ? at : n - VEC;
+          const int64_t k = int64_t(step0) * KS + r;
+          const MatIn& m = h == 0 ? a.p : a.q[0];
+          src[h][j] = static_cast<const unsigned char*>(m.p) + (k * m.ld + i) * int64_t(sizeof(T));
+          if (FORM == kDx && h == 1) {
+            // k = seam and on lie in the second weight
+            const int64_t over = a.seam - k, at_step = over <= 0 ? 0 : (over + KS - 1) / KS;
+            cross[j] = static_cast<const unsigned char*>(a.q[1].p) +
+                       ((k + at_step * KS - a.seam) * a.q[1].ld + i) * int64_t(sizeof(T));
+            cross_at[j] = at_step < (1 << 30) ? static_cast<int>(at_step) : 1 << 30;
+            if (at_step == 0) src[h][j] = cross[j];
+          }
+          continue;
+        }
+      }
       const MatIn& m = h == 0 ? a.p : a.q[GATED ? (r >> 4) & 1 : 0];
       const int64_t at = h == 0 ? row0 + r : col0 + (GATED ? (r >> 5) * 16 + (r & 15) : r);
-      const int64_t n = h == 0 ? a.rows : a.cols;
       src[h][j] = static_cast<const unsigned char*>(m.p) + (at < n ? at : n - 1) * m.ld * int64_t(sizeof(T)) +
                   int64_t(step0 + turn) * 128 + ((lane & 7) ^ ((r >> 1) & 7)) * 16;
     }
-  auto advance = [&](int t) { return t == full - 1 - turn ? 128 - full * 128 : 128; };  // bytes from step t to t + 1
+  }
+  const int64_t by_seam = FORM == kDx ? a.q[1].ld * int64_t(128) : 0;
+  // the lane's place in step t + 1, from its place in step t
+  auto advance = [&](int h, int j, int t) {
+    if (FORM == kDx && h == 1) {
+      const unsigned char* next = src[h][j] + (t >= cross_at[j] ? by_seam : by[h]);
+      src[h][j] = t + 1 == cross_at[j] ? cross[j] : next;
+    } else {
+      src[h][j] += FORM == kForward && t == full - 1 - turn ? 128 - full * 128 : by[h];
+    }
+  };
   auto copy_unit = [&](int t, int slot, int h) {
     unsigned char* at = lds + C::slot(slot) + wave * kCopies[h] * 1024;
 #pragma unroll
     for (int j = 0; j < kCopies[h]; ++j) {
       copy_to_lds(src[h][j], at + j * 1024);
-      src[h][j] += advance(t);
+      advance(h, j, t);
     }
   };
   auto copy_unit_or_tail = [&](int u, int slot, int h) {
@@ -298,9 +356,11 @@ __global__ void __launch_bounds__(C::threads, C::per_simd) gemm_kernel(GemmPair 
       unsigned char* at = lds + C::slot(slot) + wave * kCopies[h] * 1024;
 #pragma unroll
       for (int j = 0; j < kCopies[h]; ++j) {
-        const int r = 8 * (wave * kCopies[h] + j) + (lane >> 3);
+        const int r = unit_row(h, j);
+        const bool in = kAcross[h] ? r * int(sizeof(T)) < tail : ((lane & 7) ^ ((r >> 1) & 7)) * 16 < tail;
+        const int64_t back = FORM == kForward ? (full - turn) * 128 : 0;
         u32x4 d = {0, 0, 0, 0};
-        if (((lane & 7) ^ ((r >> 1) & 7)) * 16 < tail) d = *reinterpret_cast<const u32x4*>(src[h][j] + (full - turn) * 128);
+        if (in) d = *reinterpret_cast<const u32x4*>(src[h][j] + back);
         *reinterpret_cast<u32x4*>(at + j * 1024 + lane * 16) = d;
       }
     }
@@ -308,33 +368,97 @@ __global__ void __launch_bounds__(C::threads, C::per_simd) gemm_kernel(GemmPair 
 
   f32x16 acc[FM][FN] = {};
   const int wm = wave / C::WN, wn = wave % C::WN;
-  const int rd = 16 * (q ^ ((c >> 1) & 7));  // vector 2 s + q of the row lies at rd ^ 32 s
-  const int rp = (wm * FM * 32 + c) * 128, rq = (wn * FN * 32 + c) * 128;
+  // Fragments of an operand read along k, or in fp32: the x-th, slice s = 0 .. 3 of a step.
+  const int rd = 16 * (q ^ ((c >> 1) & 7));  // along: vector 2 s + q of the row lies at rd ^ 32 s
+  const int along[2] = {(wm * FM * 32 + c) * 128, (wn * FN * 32 + c) * 128};
+  constexpr int kFrags[2] = {FM, FN};
+  constexpr bool kPaired[2] = {kAcross[0] && sizeof(T) == 2, kAcross[1] && sizeof(T) == 2};
+  int across[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int base = (h == 0 ? wm : wn) * kFrags[h] * 32, width = kVecs[h] * 16;  // first column, bytes of a k
+    if constexpr (sizeof(T) == 2) {
+      const int col = base + (kFrags[h] > 1 ? kFrags[h] * c : c & ~1);
+      across[h] = 8 * q * width + ((col / 8) ^ (h == 0 ? AP::spread(8 * q) : AQ::spread(8 * q))) * 16 + col % 8 * 2;
+    } else {
+      across[h] = 4 * q * width + (base + c) * 4;
+    }
+  }
+  auto fragment = [&](int h, int slot, int x, int s) -> u32x4 {
+    const unsigned char* unit = lds + C::slot(slot);
+    if (!kAcross[h]) return *reinterpret_cast<const u32x4*>(unit + along[h] + (rd ^ (s * 32)) + x * 4096);
+    const int width = kVecs[h] * 16;
+    u32x4 d;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      d[r] = *reinterpret_cast<const uint32_t*>(unit + across[h] + x * 128 + (8 * s + r) * width);
+    return d;
+  };
+  // bf16 across k: the lane's columns of k = 16 s + 8 q + kk, and word d (k = 2 d, 2 d + 1) of
+  // fragment x paired from them.
+  auto columns = [&](int h, int slot, int s, int kk, uint32_t (&to)[2]) {
+    const unsigned char* from = lds + C::slot(slot) + across[h] + (16 * s + kk) * kVecs[h] * 16;
+    if (kFrags[h] == 4) {
+      typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+      const u32x2 d = *reinterpret_cast<const u32x2*>(from);
+      to[0] = d[0];
+      to[1] = d[1];
+    } else {
+      to[0] = *reinterpret_cast<const uint32_t*>(from);
+    }
+  };
+  constexpr uint32_t kLow = 0x05040100, kHigh = 0x07060302;  // low and high halves of two words
+  const uint32_t mine = c & 1 ? kHigh : kLow;
+  auto paired = [&](int h, const uint32_t (&raw)[8][2], int x, int d) {
+    const int w = kFrags[h] == 4 ? x >> 1 : 0;
+    return __builtin_amdgcn_perm(raw[2 * d + 1][w], raw[2 * d][w], kFrags[h] == 1 ? mine : x & 1 ? kHigh : kLow);
+  };
   // A step has two halves; the fragments of one are read while the other is multiplied.  One
   // barrier a step, between them: behind it every wave has read step t's units, and step t + 1's
   // are complete for every wave.  Unit 2 t + U takes unit 2 t's slot from there on, unit
   // 2 t + U + 1 the next one in the first half of step t + 1: the copies spread evenly over
   // the multiplications, and the last of a step's own has half a step to arrive.
   u32x4 p0[2][FM], q0[2][FN], p1[2][FM], q1[2][FN];
-  auto read = [&](int slot_p, int slot_q, int half, u32x4 (&pv)[2][FM], u32x4 (&qv)[2][FN]) {
+  auto read = [&](int slot_p, int slot_q, u32x4 (&pv)[2][FM], u32x4 (&qv)[2][FN]) {  // the first half of a step
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int v = rd ^ (half * 64 + s * 32);
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
-        qv[s][j] = *reinterpret_cast<const u32x4*>(lds + C::slot(slot_q) + rq + v + j * 4096);
+      for (int h = 0; h < 2; ++h) {
+        const int slot = h == 0 ? slot_p : slot_q;
+        uint32_t raw[8][2];
+        if (kPaired[h]) {
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
-        pv[s][i] = *reinterpret_cast<const u32x4*>(lds + C::slot(slot_p) + rp + v + i * 4096);
-    }
+          for (int kk = 0; kk < 8; ++kk) columns(h, slot, s, kk, raw[kk]);
+        }
+#pragma unroll
+        for (int x = 0; x < kFrags[h]; ++x) {
+          u32x4 d;
+          if (kPaired[h]) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) d[w] = paired(h, raw, x, w);
+          } else {
+            d = fragment(h, slot, x, s);
+          }
+          if (h == 0)
+            pv[s][x] = d;
+          else
+            qv[s][x] = d;
+        }
+      }
   };
-  // One half multiplied, with the other's fragment reads (over its first three quarters) and one
-  // unit's copies spread evenly between the multiplications, in exactly this order.
-  constexpr int kMults = 2 * FM * FN, kReads = 2 * (FM + FN), kEarly = kMults * 3 / 4 > 0 ? kMults * 3 / 4 : 1;
+  // One half multiplied, with the other's fragment reads and one unit's copies spread evenly
+  // between the multiplications, in exactly this order: the reads over the first three quarters,
+  // or, where columns are paired, over the first half, and the pairing over the second.
+  constexpr bool kPairs = kPaired[0] || kPaired[1];
+  constexpr int kMults = 2 * FM * FN;
+  constexpr int kReadsOf[2] = {kPaired[0] ? 8 : FM, kPaired[1] ? 8 : FN}, kReads = 2 * (kReadsOf[0] + kReadsOf[1]);
+  constexpr int kPairsOf[2] = {kPaired[0] ? 4 * FM : 0, kPaired[1] ? 4 * FN : 0};
+  constexpr int kPairings = 2 * (kPairsOf[0] + kPairsOf[1]);
+  constexpr int kEarly = kMults * (kPairs ? 2 : 3) / 4 > 0 ? kMults * (kPairs ? 2 : 3) / 4 : 1;
   auto half_step = [&](const u32x4 (&pa)[2][FM], const u32x4 (&qa)[2][FN], int slot_p, int slot_q, int half,
                        u32x4 (&pb)[2][FM], u32x4 (&qb)[2][FN], int step, int slot_copy, int h, bool copies) {
     unsigned char* at = lds + C::slot(slot_copy) + wave * kCopies[h] * 1024;
-    const int by = advance(step);
+    uint32_t raw_p[2][8][2], raw_q[2][8][2];
 #pragma unroll
     for (int m = 0; m < kMults; ++m) {
       const int s = m / (FM * FN), i = m / FN % FM, j = m % FN;
@@ -342,17 +466,36 @@ __global__ void __launch_bounds__(C::threads, C::per_simd) gemm_kernel(GemmPair 
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int r = m < kEarly ? kReads * m / kEarly : kReads; r < (m < kEarly ? kReads * (m + 1) / kEarly : kReads); ++r) {
-        const int rs = r / (FM + FN), x = r % (FM + FN), v = rd ^ (half * 64 + rs * 32);
-        if (x < FN)
-          qb[rs][x] = *reinterpret_cast<const u32x4*>(lds + C::slot(slot_q) + rq + v + x * 4096);
-        else
-          pb[rs][x - FN] = *reinterpret_cast<const u32x4*>(lds + C::slot(slot_p) + rp + v + (x - FN) * 4096);
+        const int rs = r / (kReads / 2), x = r % (kReads / 2), y = x - kReadsOf[1];
+        if (x < kReadsOf[1]) {
+          if (kPaired[1])
+            columns(1, slot_q, 2 * half + rs, x, raw_q[rs][x]);
+          else
+            qb[rs][x] = fragment(1, slot_q, x, 2 * half + rs);
+        } else {
+          if (kPaired[0])
+            columns(0, slot_p, 2 * half + rs, y, raw_p[rs][y]);
+          else
+            pb[rs][y] = fragment(0, slot_p, y, 2 * half + rs);
+        }
       }
       if (copies) {
 #pragma unroll
         for (int k = kCopies[h] * m / kMults; k < kCopies[h] * (m + 1) / kMults; ++k) {
           copy_to_lds(src[h][k], at + k * 1024);
-          src[h][k] += by;
+          advance(h, k, step);
+        }
+      }
+      if constexpr (kPairs) {
+        constexpr int kLate = kMults - kEarly;
+        const int l = m - kEarly;
+#pragma unroll
+        for (int r = l < 0 ? 0 : kPairings * l / kLate; r < (l < 0 ? 0 : kPairings * (l + 1) / kLate); ++r) {
+          const int rs = r / (kPairings / 2), x = r % (kPairings / 2), y = x - kPairsOf[1];
+          if (x < kPairsOf[1])
+            qb[rs][x / 4][x % 4] = paired(1, raw_q[rs], x / 4, x % 4);
+          else
+            pb[rs][y / 4][y % 4] = paired(0, raw_p[rs], y / 4, y % 4);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -365,7 +508,7 @@ __global__ void __launch_bounds__(C::threads, C::per_simd) gemm_kernel(GemmPair 
     copies_then_barrier<C::copies(C::U - 3)>();
   else
     copies_then_barrier<0>();
-  read(0, 1, 0, p0, q0);
+  read(0, 1, p0, q0);
   int t = 0, slot = 0;  // slot of unit 2 t
   for (; (2 * t + C::U) / 2 < full; ++t) {
     half_step(p0, q0, slot, after(slot, 1), 1, p1, q1, (2 * t + C::U - 1) / 2, after(slot, C::U - 1),
@@ -395,14 +538,24 @@ __global__ void __launch_bounds__(C::threads, C::per_simd) gemm_kernel(GemmPair 
 #pragma unroll
     for (int j = 0; j < FN; ++j)
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
-        *reinterpret_cast<f32x4*>(win + c * C::win_pitch + 32 * j + 8 * g + 4 * q) =
-            f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+      for (int g = 0; g < 4; ++g) {
+        float* row = win + c * C::win_pitch;
+        if constexpr (kPaired[1] && FN == 4) {  // fragment x holds columns 4 r + x: here those of r = 8 g + 4 q + j
+          const int r = 4 * g + j;
+          *reinterpret_cast<f32x4*>(row + 4 * (8 * g + 4 * q + j)) = f32x4{acc[i][0][r], acc[i][1][r], acc[i][2][r], acc[i][3][r]};
+        } else if constexpr (kPaired[1] && FN == 2) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) row[2 * (8 * g + 4 * q + e) + j] = acc[i][j][4 * g + e];
+        } else {
+          *reinterpret_cast<f32x4*>(row + 32 * j + 8 * g + 4 * q) =
+              f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+        }
+      }
     lds_wave_sync();
 #pragma unroll 1
     for (int v = lane; v < 32 * LANES; v += 64) {
       const int r = v / LANES, nc = (v % LANES) * 8;
-      const int64_t m = row0 + (wm * FM + i) * 32 + r, n = col0 + wn * CW + nc;
+      const int64_t m = row0 + wm * FM * 32 + (kPaired[0] ? FM * r + i : 32 * i + r), n = col0 + wn * CW + nc;
       if (m >= a.rows || n >= a.cols) continue;
       float z[NQ][8];
 #pragma unroll
@@ -417,6 +570,23 @@ __global__ void __launch_bounds__(C::threads, C::per_simd) gemm_kernel(GemmPair 
         finish8<T, GATED>(a, m, n, z);
       }
     }
+  }
+}
+
+// The forward products, or those of a backward pass (GRAD).
+template <typename T, typename C, bool GATED, bool GRAD>
+__global__ void __launch_bounds__(C::threads, C::per_simd) gemm_kernel(GemmPair pair) {
+  __shared__ __attribute__((aligned(16))) unsigned char lds[C::lds];
+  const int second = static_cast<int>(blockIdx.x) >= pair.first;
+  const GemmParams& a = pair.a[second];
+  const int block = static_cast<int>(blockIdx.x) - (second ? pair.first : 0);
+  if constexpr (!GRAD) {
+    product<T, C, GATED, kForward>(a, block, lds);
+  } else {
+    if (a.form == kDx)
+      product<T, C, false, kDx>(a, block, lds);
+    else
+      product<T, C, false, kDw>(a, block, lds);
   }
 }
 
@@ -776,7 +946,7 @@ constexpr float kRest[kTiles] = {12.f, 6.f, 6.f, 4.5f, 3.5f, 3.f};
   if (const hipError_t e_ = (call); e_ != hipSuccess) return e_
 
 // Launch n = 1 or 2 products (their splits set) as one grid of this tile.
-template <typename T, typename C, bool GATED>
+template <typename T, typename C, bool GATED, bool GRAD>
 hipError_t launch_tiles(const GemmParams* a, int n, hipStream_t s) {
   constexpr int cc = C::BN / (GATED ? 2 : 1);
   GemmPair pair{};
@@ -789,19 +959,19 @@ hipError_t launch_tiles(const GemmParams* a, int n, hipStream_t s) {
     grid += int64_t(pair.a[i].tiles_m) * pair.a[i].tiles_n * a[i].splits;
   }
   if (n == 1) pair.first = static_cast<int32_t>(grid);
-  gemm_kernel<T, C, GATED><<<static_cast<unsigned>(grid), C::threads, 0, s>>>(pair);
+  gemm_kernel<T, C, GATED, GRAD><<<static_cast<unsigned>(grid), C::threads, 0, s>>>(pair);
   return hipGetLastError();
 }
 
-template <typename T, bool GATED>
+template <typename T, bool GATED, bool GRAD>
 hipError_t launch_products(int tile, const GemmParams* a, int n, hipStream_t s) {
   switch (tile) {
-    case 0: return launch_tiles<T, Tile0, GATED>(a, n, s);
-    case 1: return launch_tiles<T, Tile1, GATED>(a, n, s);
-    case 2: return launch_tiles<T, Tile2, GATED>(a, n, s);
-    case 3: return launch_tiles<T, Tile3, GATED>(a, n, s);
-    case 4: return launch_tiles<T, Tile4, GATED>(a, n, s);
-    default: return launch_tiles<T, Tile5, GATED>(a, n, s);
+    case 0: return launch_tiles<T, Tile0, GATED, GRAD>(a, n, s);
+    case 1: return launch_tiles<T, Tile1, GATED, GRAD>(a, n, s);
+    case 2: return launch_tiles<T, Tile2, GATED, GRAD>(a, n, s);
+    case 3: return launch_tiles<T, Tile3, GATED, GRAD>(a, n, s);
+    case 4: return launch_tiles<T, Tile4, GATED, GRAD>(a, n, s);
+    default: return launch_tiles<T, Tile5, GATED, GRAD>(a, n, s);
   }
 }
 
@@ -913,67 +1083,19 @@ hipError_t launch_forward(GemmParams a, float* part, hipStream_t s) {
   const Plan p = plan_forward(a.rows, a.cols, a.depth, GATED, sizeof(T));
   a.splits = p.splits;
   a.part = part;
-  ADA_TRY((launch_products<T, GATED>(p.tile, &a, 1, s)));
+  ADA_TRY((launch_products<T, GATED, false>(p.tile, &a, 1, s)));
   return launch_joins<T, GATED>(&a, 1, nullptr, s);
 }
 
-// ---- slopes and transposed copies ----------------------------------------------------
-// 64 x 64 tiles; a transposed copy goes through LDS so that both sides move 16-byte vectors.
+// ---- slopes ---------------------------------------------------------------------------
+// 64 x 64 tiles of dz.
 constexpr int kSide = 64;
-
-// Store the tile t[row][col] as out[col][row]: columns n0 .. (< cols), rows m0 .. (< m_end).
-template <typename T>
-__device__ __forceinline__ void store_transposed(const T (*t)[kSide + 16 / sizeof(T)], T* out, int64_t ld, int64_t m0,
-                                                 int64_t m_end, int64_t n0, int64_t cols) {
-  constexpr int VEC = 16 / sizeof(T), PER = kSide / VEC;
-  for (int v = threadIdx.x; v < kSide * PER; v += 256) {
-    const int n = v / PER, m = (v % PER) * VEC;
-    if (n0 + n >= cols || m0 + m >= m_end) continue;
-    Vec16<T> d;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) d.e[e] = t[m + e][n];
-    *reinterpret_cast<Vec16<T>*>(out + (n0 + n) * ld + m0 + m) = d;
-  }
-}
-
-// out[j][i] = m[i][j] for an [n_rows][cols] matrix and i < n_out, a multiple of 16 bytes; zeros
-// from n_rows on.
-struct TransposeJob {
-  MatIn m;
-  void* out;
-  int64_t ld_out;
-  int64_t n_out;
-  int64_t n_rows;
-  int64_t cols;
-  int32_t tiles_n;
-  int32_t first;  // its first block
-};
-
-template <typename T>
-using SideTile = T[kSide][kSide + 16 / sizeof(T)];
-
-template <typename T>
-__device__ __forceinline__ void transpose_tile(const TransposeJob& j, int block, SideTile<T>& t) {
-  constexpr int VEC = 16 / sizeof(T), PER = kSide / VEC;
-  const int64_t m0 = int64_t(block / j.tiles_n) * kSide, n0 = int64_t(block % j.tiles_n) * kSide;
-  for (int v = threadIdx.x; v < kSide * PER; v += 256) {
-    const int r = v / PER, n = (v % PER) * VEC;
-    Vec16<T> d = {};
-    if (m0 + r < j.n_rows && n0 + n < j.cols)
-      d = *reinterpret_cast<const Vec16<T>*>(static_cast<const T*>(j.m.p) + (m0 + r) * j.m.ld + n0 + n);
-    *reinterpret_cast<Vec16<T>*>(&t[r][n]) = d;
-  }
-  __syncthreads();
-  store_transposed<T>(t, static_cast<T*>(j.out), j.ld_out, m0, j.n_out, n0, j.cols);
-}
 
 struct SlopeParams {
   MatIn dy;
   MatIn pre[2];
   void* dz;        // null or [rows][ld_z]: dz, or dg in columns 0 .., du in columns cols ..
   int64_t ld_z;
-  void* dzt;       // null or [cols (x 2)][ld_t]: the same transposed, zeros behind rows
-  int64_t ld_t;
   float* sums;     // null or [tile rows][cols (x 2)]: column sums of each 64-row tile
   int64_t rows;
   int32_t cols;
@@ -981,13 +1103,14 @@ struct SlopeParams {
   int32_t act;
 };
 
-// dz = dy act'(z), or dg = dy u act'(g), du = dy act(g), in every form the products and the
-// bias gradients read, in one pass over dy and the saved pre-activations.
+// dz = dy act'(z), or dg = dy u act'(g), du = dy act(g), and the tile's column sums, in one pass
+// over dy and the saved pre-activations: bound by memory.
 template <typename T, bool GATED>
-__device__ __forceinline__ void slope_tile(const SlopeParams& a, int block, SideTile<T> (&t)[GATED ? 2 : 1]) {
+__global__ void __launch_bounds__(256) slope_kernel(SlopeParams a) {
   constexpr int VEC = 16 / sizeof(T), PER = kSide / VEC, RSTEP = 256 / PER;
   constexpr int NQ = GATED ? 2 : 1;
   __shared__ float part[RSTEP][kSide];
+  const int block = static_cast<int>(blockIdx.x);
   const int64_t m0 = int64_t(block / a.tiles_n) * kSide, n0 = int64_t(block % a.tiles_n) * kSide;
   const int n = (threadIdx.x % PER) * VEC;
   float sum[NQ][VEC] = {};
@@ -1020,15 +1143,6 @@ __device__ __forceinline__ void slope_tile(const SlopeParams& a, int block, Side
           *reinterpret_cast<Vec16<T>*>(static_cast<T*>(a.dz) + m * a.ld_z + h * a.cols + n0 + n) = out[h];
       }
     }
-#pragma unroll
-    for (int h = 0; h < NQ; ++h) *reinterpret_cast<Vec16<T>*>(&t[h][r][n]) = out[h];
-  }
-  __syncthreads();
-  if (a.dzt != nullptr) {
-#pragma unroll
-    for (int h = 0; h < NQ; ++h)
-      store_transposed<T>(t[h], static_cast<T*>(a.dzt) + int64_t(h) * a.cols * a.ld_t, a.ld_t, m0, a.ld_t, n0,
-                          a.cols);
   }
   if (a.sums != nullptr) {
 #pragma unroll
@@ -1044,29 +1158,6 @@ __device__ __forceinline__ void slope_tile(const SlopeParams& a, int block, Side
       }
     }
   }
-}
-
-// Everything the products of a backward pass read, in one launch: slope tiles first, then the
-// tiles of the transposed copies.
-constexpr int kJobs = 3;  // both weights and x
-struct PrepareParams {
-  SlopeParams slope;
-  TransposeJob job[kJobs];
-  int32_t slope_blocks;
-  int32_t jobs;
-};
-
-template <typename T, bool GATED>
-__global__ void __launch_bounds__(256) prepare_kernel(PrepareParams p) {
-  __shared__ __attribute__((aligned(16))) SideTile<T> t[GATED ? 2 : 1];
-  const int block = static_cast<int>(blockIdx.x);
-  if (block < p.slope_blocks) {
-    slope_tile<T, GATED>(p.slope, block, t);
-    return;
-  }
-  int j = 0;
-  while (j < p.jobs - 1 && block >= p.job[j + 1].first) ++j;
-  transpose_tile<T>(p.job[j], block - p.job[j].first, t[0]);
 }
 
 template <typename T>
@@ -1090,12 +1181,10 @@ hipError_t launch_linear_t(const LinearParams& p, void* ws, hipStream_t s) {
                  : launch_forward<T, false>(a, static_cast<float*>(ws), s);
 }
 
-// Workspace of a backward pass (byte offsets): dz [rows][parts d_out] and the weights'
-// transposed copy [d_in][parts d_out] for dx; dz transposed [parts d_out][ld_t] and x
-// transposed [d_in][ld_t] for dW; column sums for dbias; parts of a split contraction.
+// Workspace of a backward pass (byte offsets): dz [rows][parts d_out], column sums for dbias,
+// parts of split contractions.
 struct GradPlan {
-  int64_t dz, wt, dzt, xt, sums, part[2], total;
-  int64_t ld_t;
+  int64_t dz, sums, part[2], total;
   PairPlan pair;  // dx, dW: the same whichever of the two is asked for, and so are their sums
 };
 
@@ -1107,13 +1196,9 @@ GradPlan plan_grad(int64_t rows, int64_t n, int64_t k, int act, int gated, int e
     g.total += (bytes + 255) / 256 * 256;
     return at;
   };
-  g.ld_t = (rows + 16 / esz - 1) / (16 / esz) * (16 / esz);
   g.dz = take(gated || act != ADA_ACT_NONE ? rows * parts * n * esz : 0);
-  g.wt = take(k * parts * n * esz);
-  g.dzt = take(parts * n * g.ld_t * esz);
-  g.xt = take(k * g.ld_t * esz);
   g.sums = take((rows + kSide - 1) / kSide * parts * n * 4);
-  const Product dx{rows, k, parts * n, esz}, dw{parts * n, k, g.ld_t, esz};
+  const Product dx{rows, k, parts * n, esz}, dw{parts * n, k, rows, esz};
   g.pair = plan_pair(dx, dw);
   g.part[0] = take(part_bytes(dx, g.pair.plan[0].splits));
   g.part[1] = take(part_bytes(dw, g.pair.plan[1].splits));
@@ -1147,43 +1232,31 @@ hipError_t launch_linear_grad_t(const LinearGradParams& p, void* ws, hipStream_t
   }
   const GradPlan g = plan_grad(p.rows, n, k, p.act, p.gated, sizeof(T));
   unsigned char* base = static_cast<unsigned char*>(ws);
-  T* wt = reinterpret_cast<T*>(base + g.wt);
-  T* dzt = reinterpret_cast<T*>(base + g.dzt);
-  T* xt = reinterpret_cast<T*>(base + g.xt);
   const bool want_dx = p.dx.p != nullptr, want_dw = p.dw[0].p != nullptr || p.dw[1].p != nullptr;
   const bool want_db = p.dbias[0] != nullptr || p.dbias[1] != nullptr;
   const bool own_dz = p.gated || p.act != ADA_ACT_NONE;  // else dz is dy
 
-  PrepareParams pre{};
-  SlopeParams& sl = pre.slope;
+  SlopeParams sl{};
   sl.dy = p.dy;
   sl.pre[0] = p.pre[0];
   sl.pre[1] = p.pre[1];
-  sl.dz = own_dz && want_dx ? base + g.dz : nullptr;
+  sl.dz = own_dz && (want_dx || want_dw) ? base + g.dz : nullptr;
   sl.ld_z = parts * n;
-  sl.dzt = want_dw ? dzt : nullptr;
-  sl.ld_t = g.ld_t;
   sl.sums = want_db ? reinterpret_cast<float*>(base + g.sums) : nullptr;
   sl.rows = p.rows;
   sl.cols = p.d_out;
   sl.tiles_n = (p.d_out + kSide - 1) / kSide;
   sl.act = p.act;
   const int64_t tiles_m = (p.rows + kSide - 1) / kSide;
-  int64_t blocks = sl.dz != nullptr || sl.dzt != nullptr || sl.sums != nullptr ? tiles_m * sl.tiles_n : 0;
-  pre.slope_blocks = static_cast<int32_t>(blocks);
-  auto transpose = [&](const MatIn& m, T* out, int64_t ld_out, int64_t n_out, int64_t n_rows, int64_t cols) {
-    const int64_t tn = (cols + kSide - 1) / kSide;
-    pre.job[pre.jobs++] = {m, out, ld_out, n_out, n_rows, cols, static_cast<int32_t>(tn), static_cast<int32_t>(blocks)};
-    blocks += (n_out + kSide - 1) / kSide * tn;
-  };
-  if (want_dx)
-    for (int h = 0; h < parts; ++h) transpose(p.w[h], wt + h * n, parts * n, n, n, k);
-  if (want_dw) transpose(p.x, xt, g.ld_t, g.ld_t, p.rows, k);
-  if (p.gated)
-    prepare_kernel<T, true><<<static_cast<unsigned>(blocks), 256, 0, s>>>(pre);
-  else
-    prepare_kernel<T, false><<<static_cast<unsigned>(blocks), 256, 0, s>>>(pre);
-  ADA_TRY(hipGetLastError());
+  if (sl.dz != nullptr || sl.sums != nullptr) {
+    const unsigned grid = static_cast<unsigned>(tiles_m * sl.tiles_n);
+    if (p.gated)
+      slope_kernel<T, true><<<grid, 256, 0, s>>>(sl);
+    else
+      slope_kernel<T, false><<<grid, 256, 0, s>>>(sl);
+    ADA_TRY(hipGetLastError());
+  }
+  const MatIn dz = own_dz ? MatIn{base + g.dz, parts * n} : p.dy;
 
   GemmParams a[2] = {};
   int tile[2], count = 0;
@@ -1197,8 +1270,11 @@ hipError_t launch_linear_grad_t(const LinearGradParams& p, void* ws, hipStream_t
   for (int i : {g.pair.plan[0].us >= g.pair.plan[1].us ? 0 : 1, g.pair.plan[0].us >= g.pair.plan[1].us ? 1 : 0}) {
     if (i == 0 && want_dx) {
       GemmParams* d = add(0);
-      d->p = own_dz ? MatIn{base + g.dz, parts * n} : p.dy;
-      d->q[0] = MatIn{wt, parts * n};
+      d->form = kDx;
+      d->p = dz;
+      d->q[0] = p.w[0];
+      d->q[1] = p.gated ? p.w[1] : p.w[0];
+      d->seam = p.gated ? n : INT64_MAX / 2;
       d->y[0] = p.dx;
       d->rows = p.rows;
       d->row_split = p.rows;
@@ -1208,20 +1284,21 @@ hipError_t launch_linear_grad_t(const LinearGradParams& p, void* ws, hipStream_t
       const bool both = p.gated && p.dw[0].p != nullptr && p.dw[1].p != nullptr;
       const int h = p.dw[0].p != nullptr ? 0 : 1;
       GemmParams* d = add(1);
-      d->p = MatIn{dzt + h * n * g.ld_t, g.ld_t};
-      d->q[0] = MatIn{xt, g.ld_t};
+      d->form = kDw;
+      d->p = MatIn{static_cast<const T*>(dz.p) + h * n, dz.ld};
+      d->q[0] = p.x;
       d->y[0] = p.dw[h];
       d->y[1] = p.dw[1];
       d->rows = both ? 2 * n : n;
       d->row_split = n;
       d->cols = p.d_in;
-      d->depth = g.ld_t;
+      d->depth = p.rows;
     }
   }
   if (count == 2 && g.pair.together) {
-    ADA_TRY((launch_products<T, false>(tile[0], a, 2, s)));
+    ADA_TRY((launch_products<T, false, true>(tile[0], a, 2, s)));
   } else {
-    for (int i = 0; i < count; ++i) ADA_TRY((launch_products<T, false>(tile[i], a + i, 1, s)));
+    for (int i = 0; i < count; ++i) ADA_TRY((launch_products<T, false, true>(tile[i], a + i, 1, s)));
   }
   BiasParams bias{sl.sums, tiles_m, parts, p.d_out, {p.dbias[0], p.dbias[1]}};
   return launch_joins<T, false>(a, count, want_db ? &bias : nullptr, s);
