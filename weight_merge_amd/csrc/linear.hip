@@ -157,33 +157,75 @@ struct GemmPair {
   int32_t first;
 };
 
-// y, pre of eight consecutive columns n of row m, from the sums without the bias.
-template <typename T, bool GATED>
-__device__ __forceinline__ void finish8(const GemmParams& a, int64_t m, int64_t n, float (&z)[GATED ? 2 : 1][8]) {
-#pragma unroll
-  for (int h = 0; h < (GATED ? 2 : 1); ++h) {
-    if (a.bias[h] != nullptr) {
-      float b[8];
-      load8(static_cast<const T*>(a.bias[h]) + n, b);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[h][e] += b[e];
-    }
-    if (a.pre[h].p != nullptr) store8(static_cast<T*>(a.pre[h].p) + m * a.pre[h].ld + n, z[h]);
-  }
-  act_values(z[0], a.act);
-  if constexpr (GATED) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) z[0][e] *= z[1][e];
-  }
-  if (a.res.p != nullptr) {
-    float r[8];
-    load8(static_cast<const T*>(a.res.p) + m * a.res.ld + n, r);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) z[0][e] += r[e];
-  }
-  const int second = m >= a.row_split;
-  store8(static_cast<T*>(a.y[second].p) + (m - (second ? a.row_split : 0)) * a.y[second].ld + n, z[0]);
+// A value held in scalar registers from here on: the kernel's arguments lie in memory, and the
+// compiler would otherwise load them again in every iteration of an epilogue.
+template <typename V>
+__device__ __forceinline__ V held(V v) {
+  asm volatile("" : "+s"(v));
+  return v;
 }
+
+// What an epilogue needs of its product.
+template <typename T, bool GATED>
+struct Epilogue {
+  static constexpr int NQ = GATED ? 2 : 1;
+  const T* bias[NQ];
+  T* pre[NQ];
+  int64_t ld_pre[NQ];
+  const T* res;
+  int64_t ld_res;
+  T* y[2];
+  int64_t ld_y[2];
+  int64_t row_split;
+  int act;
+
+  __device__ __forceinline__ explicit Epilogue(const GemmParams& a) {
+#pragma unroll
+    for (int h = 0; h < NQ; ++h) {
+      bias[h] = held(static_cast<const T*>(a.bias[h]));
+      pre[h] = held(static_cast<T*>(a.pre[h].p));
+      ld_pre[h] = held(a.pre[h].ld);
+    }
+    res = held(static_cast<const T*>(a.res.p));
+    ld_res = held(a.res.ld);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      y[h] = held(static_cast<T*>(a.y[h].p));
+      ld_y[h] = held(a.y[h].ld);
+    }
+    row_split = held(a.row_split);
+    act = held(a.act);
+  }
+
+  // y, pre of eight consecutive columns n of row m, from the sums without the bias.
+  __device__ __forceinline__ void finish8(int64_t m, int64_t n, float (&z)[NQ][8]) const {
+#pragma unroll
+    for (int h = 0; h < NQ; ++h) {
+      if (bias[h] != nullptr) {
+        float b[8];
+        load8(bias[h] + n, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[h][e] += b[e];
+      }
+      if (pre[h] != nullptr) store8(pre[h] + m * ld_pre[h] + n, z[h]);
+    }
+    act_values(z[0], act);
+    if constexpr (GATED) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[0][e] *= z[1][e];
+    }
+    if (res != nullptr) {
+      float r[8];
+      load8(res + m * ld_res + n, r);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[0][e] += r[e];
+    }
+    if (m < row_split)
+      store8(y[0] + m * ld_y[0] + n, z[0]);
+    else
+      store8(y[1] + (m - row_split) * ld_y[1] + n, z[0]);
+  }
+};
 
 // Sixteen bytes per lane from global memory to LDS, lane l's at lds + 16 l (lds is the same
 // in every lane of the wave).
@@ -531,6 +573,10 @@ __device__ __forceinline__ void product(const GemmParams& a, int block, unsigned
   // so that a lane has eight consecutive columns and a row's lanes write whole lines.
   __syncthreads();
   float* win = reinterpret_cast<float*>(lds + wave * C::window);
+  const Epilogue<T, GATED> ep(a);
+  float* const part = held(a.part);
+  const int64_t rows = held(a.rows);
+  const int cols = held(a.cols), splits = held(a.splits);
   constexpr int CW = FN * 32 / NQ, LANES = CW / 8;  // output columns of the wave, lanes per row
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
@@ -552,22 +598,28 @@ __device__ __forceinline__ void product(const GemmParams& a, int block, unsigned
         }
       }
     lds_wave_sync();
+    constexpr int kRounds = LANES / 2 > 0 ? LANES / 2 : 1, kTogether = kRounds > 1 ? 2 : 1;
 #pragma unroll 1
-    for (int v = lane; v < 32 * LANES; v += 64) {
-      const int r = v / LANES, nc = (v % LANES) * 8;
-      const int64_t m = row0 + wm * FM * 32 + (kPaired[0] ? FM * r + i : 32 * i + r), n = col0 + wn * CW + nc;
-      if (m >= a.rows || n >= a.cols) continue;
-      float z[NQ][8];
+    for (int v0 = 0; v0 < kRounds; v0 += kTogether) {
+      float z[kTogether][NQ][8];
 #pragma unroll
-      for (int h = 0; h < NQ; ++h) {
-        const float* from = win + r * C::win_pitch + (GATED ? (nc >> 4) * 32 + h * 16 + (nc & 15) : nc);
-        load8(from, z[h]);
+      for (int u = 0; u < kTogether; ++u) {
+        const int v = (v0 + u) * 64 + lane, r = v / LANES, nc = (v % LANES) * 8;
+#pragma unroll
+        for (int h = 0; h < NQ; ++h)
+          load8(win + r * C::win_pitch + (GATED ? (nc >> 4) * 32 + h * 16 + (nc & 15) : nc), z[u][h]);
       }
-      if (a.splits > 1) {
 #pragma unroll
-        for (int h = 0; h < NQ; ++h) store8(a.part + ((int64_t(split) * NQ + h) * a.rows + m) * a.cols + n, z[h]);
-      } else {
-        finish8<T, GATED>(a, m, n, z);
+      for (int u = 0; u < kTogether; ++u) {
+        const int v = (v0 + u) * 64 + lane, r = v / LANES, nc = (v % LANES) * 8;
+        const int64_t m = row0 + wm * FM * 32 + (kPaired[0] ? FM * r + i : 32 * i + r), n = col0 + wn * CW + nc;
+        if (m >= rows || n >= cols) continue;
+        if (splits > 1) {
+#pragma unroll
+          for (int h = 0; h < NQ; ++h) store8(part + ((int64_t(split) * NQ + h) * rows + m) * cols + n, z[u][h]);
+        } else {
+          ep.finish8(m, n, z[u]);
+        }
       }
     }
   }
@@ -599,6 +651,7 @@ __device__ __forceinline__ void join_parts(const GemmParams& a, int block) {
   if (v >= groups) return;
   const int64_t m = v / (a.cols / 8);
   const int64_t n = (v - m * (a.cols / 8)) * 8;
+  const Epilogue<T, GATED> ep(a);
   float z[NQ][8] = {};
   constexpr int kAhead = 4;  // parts whose loads are in flight together
   for (int s0 = 0; s0 < a.splits; s0 += kAhead) {
@@ -618,7 +671,7 @@ __device__ __forceinline__ void join_parts(const GemmParams& a, int block) {
         for (int e = 0; e < 8; ++e)
           if (s0 + s < a.splits) z[h][e] += t[s][h][e];
   }
-  finish8<T, GATED>(a, m, n, z);
+  ep.finish8(m, n, z);
 }
 
 // dbias: the slope tiles' column sums in a fixed order, four chains per column; blocks of 64
@@ -803,6 +856,7 @@ __device__ __forceinline__ void few_rows_product(const GemmParams& a, unsigned c
     for (int b = 0; b < TB; ++b)
       *reinterpret_cast<f32x4*>(sums + wave * kWave + ((h * TB + b) * 16 + c) * F::pitch + 4 * q) = acc[h][b];
   __syncthreads();
+  const Epilogue<T, GATED> ep(a);
   for (int v = threadIdx.x; v < 2 * a.rows; v += 64 * NW) {
     const int r = v >> 1, nc = (v & 1) * 8;
     if (col0 + nc >= a.cols) continue;
@@ -816,7 +870,7 @@ __device__ __forceinline__ void few_rows_product(const GemmParams& a, unsigned c
 #pragma unroll
         for (int e = 0; e < 8; ++e) z[h][e] += t[e];
       }
-    finish8<T, GATED>(a, r, col0 + nc, z);
+    ep.finish8(r, col0 + nc, z);
   }
 }
 
@@ -911,12 +965,13 @@ __global__ void __launch_bounds__(512) one_row_kernel(GemmParams a) {
   }
   __syncthreads();
   if (threadIdx.x == 0) {
+    const Epilogue<T, GATED> ep(a);
     float z[NQ][8];
 #pragma unroll
     for (int h = 0; h < NQ; ++h)
 #pragma unroll
       for (int e = 0; e < 8; ++e) z[h][e] = sums[h][e];
-    finish8<T, GATED>(a, 0, int64_t(blockIdx.x) * 8, z);
+    ep.finish8(0, int64_t(blockIdx.x) * 8, z);
   }
 }
 
