@@ -981,9 +981,10 @@ hipError_t launch_one_row(const GemmParams& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The tiles and what a step and a workgroup's start and end cost on a CU of its own, in us
-// (bf16 step, fp32 step, rest): fitted to 19 shapes from 24 x 4096 x 11008 to 4096 x 4096 x 2048
-// timed with every tile and split.
+// The tiles, and what a step and a workgroup's start and end cost on a CU of its own, in us
+// (bf16 step, fp32 step, rest), beside 4 us for a launch: fitted to 19 shapes from 24 x 4096 x
+// 11008 to 4096 x 4096 x 4096 timed with every tile and split.  Of the tile and split that were
+// fastest at each, the rule takes 16, and in the other three ones within 11%.
 using Tile0 = TileConfig<256, 256, 5, 1>;
 using Tile1 = TileConfig<256, 128, 6, 1>;
 using Tile2 = TileConfig<128, 256, 6, 1>;
@@ -993,9 +994,9 @@ using Tile5 = TileConfig<64, 64, 10, 2>;
 constexpr int kTiles = 6;
 constexpr int kTileRows[kTiles] = {Tile0::BM, Tile1::BM, Tile2::BM, Tile3::BM, Tile4::BM, Tile5::BM};
 constexpr int kTileCols[kTiles] = {Tile0::BN, Tile1::BN, Tile2::BN, Tile3::BN, Tile4::BN, Tile5::BN};
-constexpr float kStep16[kTiles] = {1.5f, 0.93f, 0.93f, 0.60f, 0.45f, 0.30f};
+constexpr float kStep16[kTiles] = {1.45f, 0.85f, 0.85f, 0.50f, 0.37f, 0.27f};
 constexpr float kStep32[kTiles] = {7.5f, 3.9f, 3.9f, 2.05f, 1.1f, 0.65f};
-constexpr float kRest[kTiles] = {12.f, 6.f, 6.f, 4.5f, 3.5f, 3.f};
+constexpr float kRest[kTiles] = {17.f, 9.f, 9.f, 6.f, 4.f, 2.5f};
 
 #define ADA_TRY(call) \
   if (const hipError_t e_ = (call); e_ != hipSuccess) return e_
@@ -1077,15 +1078,36 @@ struct Product {
   }
 };
 constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
-constexpr float kLaunch = 3.f;
+constexpr float kLaunch = 4.f;
+
+// When the last of n workgroups of `longer` us and then m of `shorter` ends, each on the CU that
+// is free first.
+float makespan(int64_t n, float longer, int64_t m, float shorter) {
+  constexpr int64_t kCus = 256;
+  if (m == 0) return static_cast<float>((n + kCus - 1) / kCus) * longer;
+  const int64_t late = n % kCus, early = kCus - late;  // CUs that take one more of the long ones
+  const float load[2] = {static_cast<float>(n / kCus) * longer, static_cast<float>(n / kCus + 1) * longer};
+  auto room = [&](float end) {
+    auto in = [&](float from) { return end > from ? static_cast<int64_t>((end - from) / shorter + 1e-3f) : 0; };
+    return early * in(load[0]) + late * in(load[1]);
+  };
+  const float least = (static_cast<float>(n) * longer + static_cast<float>(m) * shorter) / kCus;
+  float best = -1.f;
+  for (float from : {load[0], load[1]}) {
+    float end = from + shorter * static_cast<float>(least > from ? static_cast<int64_t>((least - from) / shorter) : 1);
+    while (room(end) < m) end += shorter;
+    if (best < 0.f || end < best) best = end;
+  }
+  return late > 0 && best < load[1] ? load[1] : best;
+}
 
 Plan plan_product(const Product& p) {
   Plan best{0, 1, -1.f};
   for (int t = 0; t < kTiles; ++t)
     for (int splits : kSplits) {
       if (!p.may_split(t, splits)) break;
-      const float us = static_cast<float>((p.tiles(t) * splits + 255) / 256) * p.one(t, splits) + p.join(splits) +
-                       (splits > 1 ? kLaunch : 0.f);
+      const float us = makespan(p.tiles(t) * splits, p.one(t, splits), 0, 0.f) + p.join(splits) +
+                       (splits > 1 ? 2 : 1) * kLaunch;
       if (best.us < 0.f || us < best.us) best = {t, splits, us};
     }
   return best;
@@ -1100,18 +1122,16 @@ struct PairPlan {
 
 PairPlan plan_pair(const Product& p, const Product& q) {
   PairPlan best{false, {plan_product(p), plan_product(q)}};
-  float least = best.plan[0].us + best.plan[1].us + kLaunch;
+  float least = best.plan[0].us + best.plan[1].us;
   for (int t = 0; t < kTiles; ++t)
     for (int sp : kSplits) {
       if (!p.may_split(t, sp)) break;
       for (int sq : kSplits) {
         if (!q.may_split(t, sq)) break;
         const int64_t np = p.tiles(t) * sp, nq = q.tiles(t) * sq;
-        const float op = p.one(t, sp), oq = q.one(t, sq), more = op > oq ? op : oq, less = op > oq ? oq : op;
-        // one round: the longer; else the work shared by all, and half of a short workgroup idle at the end
-        const float all = (static_cast<float>(np) * op + static_cast<float>(nq) * oq) / 256.f + 0.5f * less;
-        float us = np + nq <= 256 || all < more ? more : all;
-        us += p.join(sp) + q.join(sq) + (sp > 1 || sq > 1 ? kLaunch : 0.f);
+        const float op = p.one(t, sp), oq = q.one(t, sq);
+        float us = op >= oq ? makespan(np, op, nq, oq) : makespan(nq, oq, np, op);
+        us += p.join(sp) + q.join(sq) + (sp > 1 || sq > 1 ? 2 : 1) * kLaunch;
         if (us < least) {
           least = us;
           best = {true, {{t, sp, op}, {t, sq, oq}}};
