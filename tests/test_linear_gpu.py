@@ -394,3 +394,121 @@ def test_large_gradients(shape, dtype):
     """Many tiles of dx (depth d_out) in one shape, of dW (depth rows) in the other."""
     check_linear_backward(*shape, dtype, "silu", seed=23)
     check_glu_backward(*shape, dtype, "silu", seed=24)
+
+
+# every tile at both of its kinds of rounds, every few-rows block, split contractions, ragged ends
+VARIANTS = [(17, 1000, 4096), (33, 1000, 4096), (48, 8200, 264), (49, 8200, 264), (64, 4096, 1000),
+            (250, 1000, 4104), (509, 4104, 520), (1000, 1032, 2056), (1021, 4104, 264), (2047, 4096, 264)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ("fp32", "bf16"))
+@pytest.mark.parametrize("shape", VARIANTS, ids=lambda s: "x".join(map(str, s)))
+def test_variants(shape, dtype):
+    check_linear(*shape, dtype, "relu", pad=8, seed=31)
+    check_glu(*shape, dtype, "silu", seed=32)
+    check_linear_backward(*shape, dtype, "relu", pad=8, seed=33)
+    check_glu_backward(*shape, dtype, "silu", pad=8, seed=34)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ("fp32", "bf16"))
+@pytest.mark.parametrize("d_out", (8, 56, 64, 72, 128, 200))
+def test_seam_between_the_weights(d_out, dtype):
+    """dx reads w_gate, then w_up, across its contraction: the seam inside a step, at its end and
+    behind the first step, with different row strides."""
+    check_glu_backward(70, d_out, 136, dtype, "silu", pad=8, seed=41)
+    check_glu_backward(300, d_out, 264, dtype, "silu", pad=16, seed=42)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", (1, 2, 17, 40))
+def test_rows_far_apart(rows):
+    """Rows of x, y and the residual as the last tokens of long sequences: row strides whose
+    offsets pass 32 bits."""
+    ld = (1 << 28) // 3 // 8 * 8
+    n, d = inputs(51, rows, 136, 264, "bf16")
+    base = torch.empty(rows * ld, dtype=torch.bfloat16, device=DEV)
+    x = base.as_strided((rows, 264), (ld, 1))
+    y = base.as_strided((rows, 136), (ld, 1), 1024)
+    res = base.as_strided((rows, 136), (ld, 1), 2048)
+    x.copy_(d["x"])
+    res.copy_(d["res"])
+    A.ada_linear(x, d["w0"], bias=d["b0"], residual=res, act="gelu", y=y)
+    by, _ = H.linear_bounds(n["x"], n["w0"], n["b0"], n["res"], "gelu", "bf16")
+    H.assert_within(y, OL.linear(n["x"], n["w0"], n["b0"], n["res"], "gelu")[0], by, "y")
+    dx = base.as_strided((rows, 264), (ld, 1), 4096)
+    dw = A.ada_linear_backward(d["dy"], x, d["w0"], dx=dx)[1]
+    bounds = H.grad_bounds([n["dy"]], [np.zeros_like(n["dy"])], n["x"], [n["w0"]], "bf16")
+    rx, rw, _, _ = OL.linear_backward(n["dy"], n["x"], n["w0"], None)
+    H.assert_within(dx, rx, bounds[0], "dx")
+    H.assert_within(dw, rw, bounds[1], "dw")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ("fp32", "bf16"))
+def test_weights_far_apart(dtype):
+    """Weight rows with a stride past 32-bit byte offsets, read along and across the contraction."""
+    ld = (1 << 29) // 5 // 8 * 8
+    rows, d_out, d_in = 20, 24, 72
+    n, d = inputs(52, rows, d_out, d_in, dtype)
+    w = torch.empty(d_out * ld, dtype=H.TD[dtype], device=DEV).as_strided((d_out, d_in), (ld, 1))
+    w.copy_(d["w0"])
+    by, _ = H.linear_bounds(n["x"], n["w0"], n["b0"], None, "none", dtype)
+    ref = OL.linear(n["x"], n["w0"], n["b0"])[0]
+    H.assert_within(A.ada_linear(d["x"], w, bias=d["b0"]), ref, by, "y")
+    H.assert_within(A.ada_linear(d["x"][:1], w, bias=d["b0"]), ref[:1], by[:1], "y of one row")
+    dx = A.ada_linear_backward(d["dy"], d["x"], w, want_dw=False)[0]
+    H.assert_within(dx, n["dy"] @ n["w0"], H.grad_bounds([n["dy"]], [np.zeros_like(n["dy"])], n["x"], [n["w0"]], dtype)[0],
+                    "dx")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ("fp32", "bf16"))
+def test_two_streams_at_once(dtype):
+    """Calls that overlap in time, each with a workspace of its own, do not touch each other."""
+    n, d = inputs(53, 300, 1032, 2056, dtype, parts=2)
+    _, z = saved(54, 300, 1032, dtype, 0)
+    ref = A.ada_glu(d["x"], d["w0"], d["w1"])
+    gref = A.ada_glu_backward(d["dy"], d["x"], d["w0"], d["w1"], z, z, want_dbias=True)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    out = []
+    for rep in range(4):
+        for s in streams:
+            out.append((A.ada_glu(d["x"], d["w0"], d["w1"], stream=s),
+                        A.ada_glu_backward(d["dy"], d["x"], d["w0"], d["w1"], z, z, want_dbias=True, stream=s)))
+    torch.cuda.synchronize()
+    for y, g in out:
+        assert torch.equal(y, ref) and all(torch.equal(a, b) for a, b in zip(g, gref))
+
+
+@pytest.mark.gpu
+def test_workspace_exactly_as_large_as_asked():
+    """The workspace's bytes behind what the call asks for stay as they were, and its contents
+    before the call do not matter."""
+    rows, d_out, d_in = 250, 1000, 4104
+    n, d = inputs(55, rows, d_out, d_in, "bf16", parts=2)
+    _, z = saved(56, rows, d_out, "bf16", 0)
+    calls = [(A.linear_workspace_bytes(rows, d_out, d_in, torch.bfloat16),
+              lambda ws: [A.ada_linear(d["x"], d["w0"], workspace=ws)]),
+             (A.glu_workspace_bytes(rows, d_out, d_in, torch.bfloat16),
+              lambda ws: [A.ada_glu(d["x"], d["w0"], d["w1"], workspace=ws)]),
+             (A.linear_backward_workspace_bytes(rows, d_out, d_in, "silu", torch.bfloat16),
+              lambda ws: A.ada_linear_backward(d["dy"], d["x"], d["w0"], pre=z, act="silu", want_dbias=True,
+                                               workspace=ws)),
+             (A.glu_backward_workspace_bytes(rows, d_out, d_in, "silu", torch.bfloat16),
+              lambda ws: A.ada_glu_backward(d["dy"], d["x"], d["w0"], d["w1"], z, z, want_dbias=True, workspace=ws))]
+    for need, call in calls:
+        ref = call(None)
+        buf = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device=DEV)  # NaN in either type
+        got = call(buf[:need]) if need else call(None)
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
+        assert (buf[need:] == 0xFF).all()
+
+
+def test_public_names():
+    import weight_merge_amd
+
+    for name in ("ada_linear", "ada_linear_backward", "ada_glu", "ada_glu_backward"):
+        assert getattr(weight_merge_amd, name) is getattr(A, name)
