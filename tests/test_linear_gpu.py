@@ -512,3 +512,14 @@ def test_public_names():
 
     for name in ("ada_linear", "ada_linear_backward", "ada_glu", "ada_glu_backward"):
         assert getattr(weight_merge_amd, name) is getattr(A, name)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ("fp32", "bf16"))
+@pytest.mark.parametrize("shape", [(2, 72, 8968), (12, 264, 28552), (16, 24, 16392), (30, 136, 17000), (48, 520, 9000),
+                                   (5, 6000, 264), (20, 4200, 2056), (40, 4200, 520)], ids=lambda s: "x".join(map(str, s)))
+def test_few_rows_variants(shape, dtype):
+    """Few rows with the contraction split over workgroups (few columns, long rows), and with two
+    waves a workgroup (many columns, short rows)."""
+    check_linear(*shape, dtype, "gelu", pad=8, seed=61)
+    check_glu(*shape, dtype, "silu", pad=8, seed=62)

@@ -761,18 +761,22 @@ __device__ __forceinline__ void few_rows_product(const GemmParams& a, unsigned c
   constexpr int NQ = F::NQ, NO = NQ + TB;  // operands: the weights, then x's blocks
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, q = lane >> 4;
-  const int64_t col0 = int64_t(blockIdx.x) * 16;
+  const int blocks = (a.cols + 15) / 16, split = __builtin_amdgcn_readfirstlane(static_cast<int>(blockIdx.x) / blocks);
+  const int column = static_cast<int>(blockIdx.x) - split * blocks;  // of workgroups: the same for all splits
+  const int64_t col0 = column * int64_t(16);
   const int64_t bytes = a.depth * sizeof(T);
   const int whole = static_cast<int>(bytes >> 8), windows = static_cast<int>((bytes + 255) >> 8);
   const int tail = static_cast<int>(bytes & 255);  // bytes of the last window if short
-  const int n = wave < windows ? (windows - wave + NW - 1) / NW : 0;  // this wave's: wave, wave + NW, ...
-  const int full = n - (tail != 0 && n > 0 && wave + (n - 1) * NW == windows - 1);
-  // Each workgroup starts elsewhere in k: side by side, their 16 rows a stride apart, they would
+  // this wave's windows: place, place + stride, ...
+  const int place = split * NW + wave, stride = NW * a.splits;
+  const int n = place < windows ? (windows - place + stride - 1) / stride : 0;
+  const int full = n - (tail != 0 && n > 0 && place + (n - 1) * stride == windows - 1);
+  // Each column starts elsewhere in k: side by side, their 16 rows a stride apart, they would
   // read the same few memory channels at a time (11008-long rows: 20.3 us, turned 16.6 us).
-  const int turn = whole > 0 ? static_cast<int>(blockIdx.x % 4096 * 61 % whole) : 0;
+  const int turn = whole > 0 ? column % 4096 * 61 % whole : 0;
   auto window = [&](int i) {  // byte offset of this wave's window i
-    const int p = wave + i * NW, r = p + turn;
-    return 256 * (p >= whole ? p : r >= whole ? r - whole : r);
+    const int p = place + i * stride, r = p + turn;
+    return __builtin_amdgcn_readfirstlane(256 * (p >= whole ? p : r >= whole ? r - whole : r));
   };
 
   // buffer copies: an operand's first row as base, 32-bit offsets to its others (rows past its
@@ -870,7 +874,13 @@ __device__ __forceinline__ void few_rows_product(const GemmParams& a, unsigned c
 #pragma unroll
         for (int e = 0; e < 8; ++e) z[h][e] += t[e];
       }
-    ep.finish8(r, col0 + nc, z);
+    if (a.splits > 1) {
+#pragma unroll
+      for (int h = 0; h < NQ; ++h)
+        store8(a.part + ((int64_t(split) * NQ + h) * a.rows + r) * a.cols + col0 + nc, z[h]);
+    } else {
+      ep.finish8(r, col0 + nc, z);
+    }
   }
 }
 
@@ -894,17 +904,38 @@ bool few_rows(const GemmParams& a, int gated, int esz) {
   return true;
 }
 
+// Into how many parts the contraction is split over workgroups: where the columns leave most CUs
+// idle and k is long (14 x 216 x 13456: 12.0 against 19.7 us; fp32 12 x 1016 x 28552: 33 against
+// 79 us), at least 32 windows a part.
+int few_rows_splits(int64_t cols, int64_t depth, int esz) {
+  const int64_t blocks = (cols + 15) / 16, windows = (depth * esz + 255) / 256;
+  int64_t splits = 256 / blocks;
+  if (splits > windows / 32) splits = windows / 32;
+  return static_cast<int>(splits < 2 ? 1 : splits > 16 ? 16 : splits);
+}
+
+template <typename T, bool GATED, int TB, int NW>
+hipError_t launch_few_rows_waves(const GemmParams& a, hipStream_t s) {
+  const unsigned grid = static_cast<unsigned>((a.cols + 15) / 16 * a.splits);
+  few_rows_kernel<T, GATED, TB, NW, 2><<<grid, 64 * NW, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+// Two waves a workgroup, and several workgroups on a CU, where there are more of them than CUs
+// and k is short (8 x 11008 x 1024: 6.8 against 10.5 us, 8 x 11008 x 4096: 17.5 against 20.6 us);
+// else as many waves as have room for their rings (16 x 4096 x 4096: 9.4 against 10.9 us).
+template <typename T, bool GATED, int TB>
+hipError_t launch_few_rows_block(const GemmParams& a, hipStream_t s) {
+  constexpr int waves = !GATED && TB == 1 ? 8 : 4, short_k = (GATED && TB > 1 ? 16 : 32) * 256;  // bytes
+  if (a.cols > 256 * 16 && a.depth * int64_t(sizeof(T)) <= short_k) return launch_few_rows_waves<T, GATED, TB, 2>(a, s);
+  return launch_few_rows_waves<T, GATED, TB, waves>(a, s);
+}
+
 template <typename T, bool GATED>
 hipError_t launch_few_rows(const GemmParams& a, hipStream_t s) {
-  const unsigned grid = (a.cols + 15) / 16;
-  constexpr int waves = GATED ? 4 : 8;
-  if (a.rows <= 16)
-    few_rows_kernel<T, GATED, 1, waves, 2><<<grid, 64 * waves, 0, s>>>(a);
-  else if (a.rows <= 32)
-    few_rows_kernel<T, GATED, 2, 4, 2><<<grid, 256, 0, s>>>(a);
-  else
-    few_rows_kernel<T, GATED, 3, 4, 2><<<grid, 256, 0, s>>>(a);
-  return hipGetLastError();
+  if (a.rows <= 16) return launch_few_rows_block<T, GATED, 1>(a, s);
+  if (a.rows <= 32) return launch_few_rows_block<T, GATED, 2>(a, s);
+  return launch_few_rows_block<T, GATED, 3>(a, s);
 }
 
 // ---- one row -------------------------------------------------------------------------
@@ -998,8 +1029,10 @@ constexpr float kStep16[kTiles] = {1.45f, 0.85f, 0.85f, 0.50f, 0.37f, 0.27f};
 constexpr float kStep32[kTiles] = {7.5f, 3.9f, 3.9f, 2.05f, 1.1f, 0.65f};
 constexpr float kRest[kTiles] = {17.f, 9.f, 9.f, 6.f, 4.f, 2.5f};
 
-#define ADA_TRY(call) \
-  if (const hipError_t e_ = (call); e_ != hipSuccess) return e_
+#define ADA_TRY(call)                                              \
+  do {                                                             \
+    if (const hipError_t e_ = (call); e_ != hipSuccess) return e_; \
+  } while (0)
 
 // Launch n = 1 or 2 products (their splits set) as one grid of this tile.
 template <typename T, typename C, bool GATED, bool GRAD>
@@ -1143,22 +1176,23 @@ PairPlan plan_pair(const Product& p, const Product& q) {
 
 int64_t part_bytes(const Product& p, int splits) { return splits > 1 ? splits * p.rows * p.cols * 4 : 0; }
 
-// A forward product's plan.  Few rows have a kernel of their own and come here only with rows
-// too far apart for it: no workspace for them.
+// A forward product's plan.  Few rows have a kernel of their own; the tile is for those with
+// rows too far apart for it.
 Plan plan_forward(int64_t rows, int64_t cols, int64_t depth, int gated, int esz) {
   Plan p = plan_product({rows, gated ? 2 * cols : cols, depth, esz});
-  if (few_rows_sizes(rows, cols)) p = {kTiles - 1, 1, 0.f};
+  if (rows == 1 || few_rows_sizes(rows, cols)) p = {kTiles - 1, rows == 1 ? 1 : few_rows_splits(cols, depth, esz), 0.f};
   return p;
 }
 
 template <typename T, bool GATED>
 hipError_t launch_forward(GemmParams a, float* part, hipStream_t s) {
   if (a.rows == 1) return launch_one_row<T, GATED>(a, s);
-  if (few_rows(a, GATED, sizeof(T))) return launch_few_rows<T, GATED>(a, s);
   const Plan p = plan_forward(a.rows, a.cols, a.depth, GATED, sizeof(T));
   a.splits = p.splits;
   a.part = part;
-  ADA_TRY((launch_products<T, GATED, false>(p.tile, &a, 1, s)));
+  const hipError_t e = few_rows(a, GATED, sizeof(T)) ? launch_few_rows<T, GATED>(a, s)
+                                                     : launch_products<T, GATED, false>(p.tile, &a, 1, s);
+  if (e != hipSuccess) return e;
   return launch_joins<T, GATED>(&a, 1, nullptr, s);
 }
 
