@@ -544,12 +544,15 @@ __device__ __forceinline__ void product(const GemmParams& a, int block, unsigned
     }
   };
   auto after = [](int slot, int by) { return slot + by >= C::U ? slot + by - C::U : slot + by; };
+  if ((C::U - 2) / 2 < full) {
 #pragma unroll
-  for (int u = 0; u < C::U - 1; ++u) copy_unit_or_tail(u, u, u & 1);
-  if ((C::U - 2) / 2 < full)
+    for (int u = 0; u < C::U - 1; ++u) copy_unit(u >> 1, u, u & 1);
     copies_then_barrier<C::copies(C::U - 3)>();
-  else
+  } else {
+#pragma unroll
+    for (int u = 0; u < C::U - 1; ++u) copy_unit_or_tail(u, u, u & 1);
     copies_then_barrier<0>();
+  }
   read(0, 1, p0, q0);
   int t = 0, slot = 0;  // slot of unit 2 t
   for (; (2 * t + C::U) / 2 < full; ++t) {
@@ -578,25 +581,31 @@ __device__ __forceinline__ void product(const GemmParams& a, int block, unsigned
   const int64_t rows = held(a.rows);
   const int cols = held(a.cols), splits = held(a.splits);
   constexpr int CW = FN * 32 / NQ, LANES = CW / 8;  // output columns of the wave, lanes per row
-#pragma unroll
+  // (the rows' loop stays rolled: its body holds every activation)
+#pragma unroll 1
   for (int i = 0; i < FM; ++i) {
     lds_wave_sync();
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
+    for (int f = 0; f < FM; ++f) {
+      if (f != i) continue;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        float* row = win + c * C::win_pitch;
-        if constexpr (kPaired[1] && FN == 4) {  // fragment x holds columns 4 r + x: here those of r = 8 g + 4 q + j
-          const int r = 4 * g + j;
-          *reinterpret_cast<f32x4*>(row + 4 * (8 * g + 4 * q + j)) = f32x4{acc[i][0][r], acc[i][1][r], acc[i][2][r], acc[i][3][r]};
-        } else if constexpr (kPaired[1] && FN == 2) {
+      for (int j = 0; j < FN; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) row[2 * (8 * g + 4 * q + e) + j] = acc[i][j][4 * g + e];
-        } else {
-          *reinterpret_cast<f32x4*>(row + 32 * j + 8 * g + 4 * q) =
-              f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+        for (int g = 0; g < 4; ++g) {
+          float* row = win + c * C::win_pitch;
+          if constexpr (kPaired[1] && FN == 4) {  // fragment x holds columns 4 r + x: here those of r = 8 g + 4 q + j
+            const int r = 4 * g + j;
+            *reinterpret_cast<f32x4*>(row + 4 * (8 * g + 4 * q + j)) =
+                f32x4{acc[f][0][r], acc[f][1][r], acc[f][2][r], acc[f][3][r]};
+          } else if constexpr (kPaired[1] && FN == 2) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) row[2 * (8 * g + 4 * q + e) + j] = acc[f][j][4 * g + e];
+          } else {
+            *reinterpret_cast<f32x4*>(row + 32 * j + 8 * g + 4 * q) =
+                f32x4{acc[f][j][4 * g], acc[f][j][4 * g + 1], acc[f][j][4 * g + 2], acc[f][j][4 * g + 3]};
+          }
         }
-      }
+    }
     lds_wave_sync();
     constexpr int kRounds = LANES / 2 > 0 ? LANES / 2 : 1, kTogether = kRounds > 1 ? 2 : 1;
 #pragma unroll 1
