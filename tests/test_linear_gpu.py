@@ -523,3 +523,43 @@ def test_few_rows_variants(shape, dtype):
     waves a workgroup (many columns, short rows)."""
     check_linear(*shape, dtype, "gelu", pad=8, seed=61)
     check_glu(*shape, dtype, "silu", pad=8, seed=62)
+
+
+@pytest.mark.gpu
+def test_default_stream_by_handle():
+    """The default stream given as a Stream, and as its handle 0."""
+    n, d = inputs(71, 20, 72, 136, "bf16", parts=2)
+    ref = A.ada_glu(d["x"], d["w0"], d["w1"])
+    for s in (torch.cuda.default_stream(), 0):
+        got = A.ada_glu(d["x"], d["w0"], d["w1"], stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(got, ref)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ("fp32", "bf16"))
+def test_few_far_apart_rows_of_a_long_contraction(dtype):
+    """Rows too far apart for the few-rows kernel and a contraction that it would split."""
+    rows, d_out, d_in, ld = 3, 40, 17000, (1 << 29) // 5 // 8 * 8
+    n, d = inputs(72, rows, d_out, d_in, dtype)
+    x = torch.empty(rows * ld, dtype=H.TD[dtype], device=DEV).as_strided((rows, d_in), (ld, 1))
+    x.copy_(d["x"])
+    by, _ = H.linear_bounds(n["x"], n["w0"], n["b0"], n["res"], "gelu", dtype)
+    H.assert_within(A.ada_linear(x, d["w0"], bias=d["b0"], residual=d["res"], act="gelu"),
+                    OL.linear(n["x"], n["w0"], n["b0"], n["res"], "gelu")[0], by, "y")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ("fp32", "bf16"))
+def test_one_matrix_for_both_projections(dtype):
+    """The same weight, bias and saved matrix given twice: inputs may be one tensor."""
+    n, d = inputs(73, 33, 136, 264, dtype)
+    y = A.ada_glu(d["x"], d["w0"], d["w0"], bias_gate=d["b0"], bias_up=d["b0"], act="none")
+    by = H.glu_bounds(n["x"], n["w0"], n["w0"], n["b0"], n["b0"], "none", dtype)[0]
+    H.assert_within(y, OL.glu(n["x"], n["w0"], n["w0"], n["b0"], n["b0"], "none")[0], by, "y")
+    same = A.ada_glu(d["x"], d["w0"], d["w0"].clone(), bias_gate=d["b0"], bias_up=d["b0"].clone(), act="none")
+    assert torch.equal(y, same)
+    _, z = saved(74, 33, 136, dtype, 0)
+    a = A.ada_glu_backward(d["dy"], d["x"], d["w0"], d["w0"], z, z, act="relu", want_dbias=True)
+    b = A.ada_glu_backward(d["dy"], d["x"], d["w0"], d["w0"].clone(), z, z.clone(), act="relu", want_dbias=True)
+    assert all(torch.equal(s, t) for s, t in zip(a, b))
