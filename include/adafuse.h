@@ -18,8 +18,8 @@
  *   - Every tensor pointer is a DEVICE pointer unless stated otherwise, 16-byte
  *     aligned, row-major, owned by the caller.  The library never allocates or
  *     frees caller memory, and the hot calls (pregate, merge, unmerge, switch,
- *     decode_gemv, decode_gemv_layer, lora_apply, lora_layer, lora_batch) allocate
- *     nothing at all.
+ *     decode_gemv, decode_gemv_layer, lora_apply, lora_layer, lora_batch, linear, glu
+ *     and their backward calls) allocate nothing at all.
  *   - `stream` is a hipStream_t passed as void* (NULL = the default stream).  All
  *     calls are asynchronous on that stream and return once the work is enqueued.
  *   - Return value: ADA_OK (0) or a negative ada_status.  All argument checks run
@@ -278,9 +278,11 @@ typedef enum {
  *   - Matrices are row-major with a row stride ld (elements, at least the row's length, at
  *     most 2^36): row i of a matrix of c columns is elements [i ld, i ld + c).  Every
  *     pointer and every row stride is 16-byte aligned.
- *   - No matrix has more than 2^35 elements.  rows: 0 <= rows <= 2^22, odd ones included.  With rows = 0 the matrices of `rows`
- *     rows may be NULL; the forward calls then write nothing, and the gradients summed
- *     over rows are zeros.
+ *   - No matrix has more than 2^35 elements.  rows: 0 <= rows <= 2^22, odd ones included.
+ *     With rows = 0 the matrices of `rows` rows may be NULL; the forward calls then write
+ *     nothing, and the gradients summed over rows are zeros.
+ *   - Equal calls give equal bits, and a gradient's do not depend on which others are asked
+ *     for.
  *   - An output may not overlap an input or another output, except that y may be the
  *     residual itself (same pointer and row stride; the residual stream updated in place).
  *     Views of one buffer that interleave (column ranges of its rows) do not overlap when

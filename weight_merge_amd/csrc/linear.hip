@@ -278,6 +278,13 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 q, u32x4 p, f32x16 acc) {
 // as its wave has fragments (F = 4: 8 bytes, F = 2: 4 bytes), fragment x taking columns F c + x,
 // and byte permutes pair the k of each column while the matrix instructions run.  Vector v of row
 // k lies at v ^ spread(k), so that the two halves of a wave, eight k apart, read different banks.
+//
+// The large tiles are bound by the matrix pipes at the clock that their power allows (256 x 256
+// at 4096 x 8192 x 28672: 1.40 ms, 1370 TFLOP/s, pipes 84% busy; with its copies taken out, 1640).
+// One wave per SIMD with 128 x 128 sums in its accumulation registers reads two thirds of the LDS
+// bytes of two waves with 128 x 64 each (1280 TFLOP/s).  128 bytes of k a row, because 64-byte
+// segments cost the caches a third of their rate (1130 TFLOP/s).  The smaller tiles, for fewer
+// rows, are bound by the latency of their copies, hence the longer rings.
 template <int BM_, int BN_, int U_, int WAVES_PER_SIMD_>
 struct TileConfig {
   static constexpr int BM = BM_, BN = BN_, WM = 2, WN = 2, U = U_, waves = WM * WN;
@@ -496,7 +503,9 @@ __device__ __forceinline__ void product(const GemmParams& a, int block, unsigned
   };
   // One half multiplied, with the other's fragment reads and one unit's copies spread evenly
   // between the multiplications, in exactly this order: the reads over the first three quarters,
-  // or, where columns are paired, over the first half, and the pairing over the second.
+  // or, where columns are paired, over the first half, and the pairing over the second.  A burst
+  // of copies holds up the wave that issues it, and with it its matrix instructions: with them
+  // issued together the 256 x 256 tile reached 1100 TFLOP/s at 4096 x 8192 x 28672, spread 1400.
   constexpr bool kPairs = kPaired[0] || kPaired[1];
   constexpr int kMults = 2 * FM * FN;
   constexpr int kReadsOf[2] = {kPaired[0] ? 8 : FM, kPaired[1] ? 8 : FN}, kReads = 2 * (kReadsOf[0] + kReadsOf[1]);
@@ -735,7 +744,8 @@ __global__ void __launch_bounds__(256) join_kernel(JoinParams j) {
 }
 
 // ---- few rows ------------------------------------------------------------------------
-// Two to 48 rows, in TB blocks of 16: bound by reading W once.  A workgroup takes 16 output columns (gated: of both
+// Two to 48 rows, in TB blocks of 16: bound by reading W once (24 x 4096 x 11008: 20.4 us, 4.5
+// TB/s).  A workgroup takes 16 output columns (gated: of both
 // products) and its NW waves share the contraction in windows of 256 bytes of k, dealt out in
 // turn.  A wave streams its windows of W and of x through an LDS ring of its own, S windows
 // deep, by direct copies (4 rows x 256 bytes each), so no barrier is met before the end.
@@ -954,10 +964,11 @@ hipError_t launch_few_rows(const GemmParams& a, hipStream_t s) {
 }
 
 // ---- one row -------------------------------------------------------------------------
-// Bound by reading W once: one wave per W row (gated: per pair), lanes along it with 16-byte
-// loads, U vectors of each row in flight before any is used, x from the caches.  Eight waves
-// hold eight consecutive columns, which the epilogue takes together.  Past the row's end a
-// lane re-reads its first vector and multiplies it by a zero x.
+// Bound by reading W once (4096 x 4096: 7.1 us, 4.7 TB/s; gated 11008 x 4096: 30.4 us, 5.9 TB/s):
+// one wave per W row (gated: per pair), lanes along it with 16-byte loads, U vectors of each row
+// in flight before any is used, x from the caches.  Eight waves hold eight consecutive columns,
+// which the epilogue takes together.  Past the row's end a lane re-reads its first vector and
+// multiplies it by a zero x.
 template <typename T>
 __device__ __forceinline__ float dot16(u32x4 w, u32x4 x, float acc) {
 #pragma unroll
@@ -1029,8 +1040,9 @@ hipError_t launch_one_row(const GemmParams& a, hipStream_t s) {
 
 // The tiles, and what a step and a workgroup's start and end cost on a CU of its own, in us
 // (bf16 step, fp32 step, rest), beside 4 us for a launch: fitted to 19 shapes from 24 x 4096 x
-// 11008 to 4096 x 4096 x 4096 timed with every tile and split.  Of the tile and split that were
-// fastest at each, the rule takes 16, and in the other three ones within 11%.
+// 11008 to 4096 x 4096 x 4096 timed with every tile and split.  At 30 other shapes, drawn from 92
+// to 3508 rows of either type, gated and not, the choice is within 4% of the fastest tile and
+// split 23 times, within 11% 29 times, and 18% behind once (fp32, 670 x 2024 x 1816).
 using Tile0 = TileConfig<256, 256, 5, 1>;
 using Tile1 = TileConfig<256, 128, 6, 1>;
 using Tile2 = TileConfig<128, 256, 6, 1>;
@@ -1228,7 +1240,8 @@ struct SlopeParams {
 };
 
 // dz = dy act'(z), or dg = dy u act'(g), du = dy act(g), and the tile's column sums, in one pass
-// over dy and the saved pre-activations: bound by memory.
+// over dy and the saved pre-activations: bound by memory (gated, 4096 x 11008: 450 MB in 86 us,
+// 5.2 TB/s).
 template <typename T, bool GATED>
 __global__ void __launch_bounds__(256) slope_kernel(SlopeParams a) {
   constexpr int VEC = 16 / sizeof(T), PER = kSide / VEC, RSTEP = 256 / PER;
