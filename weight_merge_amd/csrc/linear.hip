@@ -677,7 +677,7 @@ __device__ __forceinline__ void join_parts(const GemmParams& a, int block) {
   const int64_t n = (v - m * (a.cols / 8)) * 8;
   const Epilogue<T, GATED> ep(a);
   float z[NQ][8] = {};
-  constexpr int kAhead = 4;  // parts whose loads are in flight together
+  constexpr int kAhead = GATED ? 4 : 8;  // parts whose loads are in flight together
   for (int s0 = 0; s0 < a.splits; s0 += kAhead) {
     float t[kAhead][NQ][8];
 #pragma unroll
@@ -1223,6 +1223,256 @@ hipError_t launch_forward(GemmParams a, float* part, hipStream_t s) {
   return launch_joins<T, GATED>(&a, 1, nullptr, s);
 }
 
+// ---- gradients of few rows -------------------------------------------------------------
+// Up to 32 rows: dx is bound by reading W once, dW by writing it once, so no operand goes
+// through LDS.  Both products have an operand whose rows lie across the contraction (W, x): a
+// lane reads VEC neighbouring columns of VEC such rows, 16 bytes each, and has with them VEC
+// fragments whose x-th column is its VEC c + x; the sums of all fragments in a lane are then VEC
+// neighbouring outputs of a row, again 16 bytes.  32 x 32 instructions: lane l = 32 h + c supplies
+// the contraction's elements 2 VEC t + VEC h + i of step t, i = 0 .. VEC - 1.
+template <typename T>
+struct FewGrad {
+  static constexpr int VEC = 16 / sizeof(T);
+  static constexpr int cols = 32 * VEC;            // a wave's output columns
+  static constexpr int step = 2 * VEC;             // of the contraction
+  static constexpr int ahead = sizeof(T) == 2 ? 2 : 4;  // dx: steps of W in flight in a wave
+  static constexpr int dw_rows = 256;              // dW: rows of a workgroup, 64 a wave
+};
+
+// The x-th fragment of VEC rows of VEC columns.
+template <typename T>
+__device__ __forceinline__ u32x4 across_fragment(const u32x4 (&raw)[16 / sizeof(T)], int x) {
+  u32x4 f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (sizeof(T) == 2)
+      f[j] = __builtin_amdgcn_perm(raw[2 * j + 1][x >> 1], raw[2 * j][x >> 1], x & 1 ? 0x07060302u : 0x05040100u);
+    else
+      f[j] = raw[j][x];
+  }
+  return f;
+}
+
+// VEC outputs of a row.
+template <typename T>
+__device__ __forceinline__ void store_vec(T* p, const float (&z)[16 / sizeof(T)]) {
+  Vec16<T> d;
+#pragma unroll
+  for (int e = 0; e < int(16 / sizeof(T)); ++e) d.e[e] = from_f32<T>(z[e]);
+  __builtin_nontemporal_store(__builtin_bit_cast(u32x4, d), (ADA_GLOBAL u32x4*)p);
+}
+
+// dW = dz^T x over up to ROWS rows: a wave holds x's fragments of its columns for all of them.
+template <typename T, int ROWS>
+__device__ __forceinline__ void few_rows_dw(const GemmParams& a, int block) {
+  using F = FewGrad<T>;
+  constexpr int VEC = F::VEC, kSteps = ROWS / F::step;
+  typedef uint32_t Two __attribute__((ext_vector_type(sizeof(T) / 2)));  // two neighbours of dz
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 31, h = lane >> 5;
+  const int strips = (a.cols + F::cols - 1) / F::cols;
+  const int64_t n0 = int64_t(block / strips) * F::dw_rows + wave * 64, rows = held(a.rows);
+  if (n0 >= rows) return;
+  const int col = block % strips * F::cols + VEC * c;
+  const bool in = col < a.cols;
+  const int depth = static_cast<int>(a.depth);
+  const int64_t ld_z = held(a.p.ld), ld_x = held(a.q[0].ld);
+  // rows 2 c and 2 c + 1 of this wave's 64: the 0th and 1st fragment of dz
+  const T* dz = static_cast<const T*>(a.p.p) + (n0 + 2 * c < rows ? n0 + 2 * c : 0);
+  const T* xs = static_cast<const T*>(a.q[0].p) + (in ? col : 0);
+  u32x4 raw[kSteps][VEC];
+  Two two[kSteps][VEC];
+#pragma unroll
+  for (int t = 0; t < kSteps; ++t)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const int r = t * F::step + VEC * h + i;
+      const int64_t at = r < depth ? r : 0;
+      two[t][i] = *(const ADA_GLOBAL Two*)(dz + at * ld_z);
+      raw[t][i] = *(const ADA_GLOBAL u32x4*)(xs + at * ld_x);
+    }
+  T* const y[2] = {held(static_cast<T*>(a.y[0].p)), held(static_cast<T*>(a.y[1].p))};
+  const int64_t ld_y[2] = {held(a.y[0].ld), held(a.y[1].ld)}, row_split = held(a.row_split);
+  __builtin_amdgcn_sched_barrier(0);  // all loads in flight before the first is used
+  u32x4 x[kSteps][VEC], z[kSteps][2];
+#pragma unroll
+  for (int t = 0; t < kSteps; ++t) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (t * F::step + VEC * h + i >= depth) {  // behind the last row: zeros on both sides
+        raw[t][i] = u32x4{0, 0, 0, 0};
+        two[t][i] = Two(0);
+      }
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 2)
+          z[t][f][j] = __builtin_amdgcn_perm(two[t][2 * j + 1][0], two[t][2 * j][0], f ? 0x07060302u : 0x05040100u);
+        else
+          z[t][f][j] = two[t][j][f];
+      }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) x[t][e] = across_fragment<T>(raw[t], e);
+  }
+#pragma unroll 1  // straight-line code once through waits for its instructions
+  for (int f = 0; f < 2; ++f) {
+    f32x16 acc[VEC] = {};
+#pragma unroll
+    for (int t = 0; t < kSteps; ++t) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) acc[e] = mfma32<T>(z[t][0], x[t][e], acc[e]);
+      z[t][0] = z[t][1];
+    }
+#pragma unroll
+    for (int g = 0; g < 16; ++g) {
+      const int64_t n = n0 + 2 * (8 * (g >> 2) + 4 * h + (g & 3)) + f;
+      float v[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[e] = acc[e][g];
+      const bool up = n >= row_split;
+      T* row = (up ? y[1] : y[0]) + (n - (up ? row_split : 0)) * (up ? ld_y[1] : ld_y[0]);
+      if (in && n < rows) store_vec<T>(row + col, v);
+    }
+  }
+}
+
+// dx = dz W: the waves of all workgroups of a strip of columns share W's rows, step by step in
+// turn; a workgroup's sums meet in LDS in a fixed order, and the workgroups' in the join.
+template <typename T>
+__device__ __forceinline__ void few_rows_dx(const GemmParams& a, int block, f32x4* lds) {
+  using F = FewGrad<T>;
+  constexpr int VEC = F::VEC, D = F::ahead;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 31, h = lane >> 5;
+  const int cols = held(a.cols), strips = (cols + F::cols - 1) / F::cols, splits = held(a.splits);
+  const int split = block / strips;
+  const int col = block % strips * F::cols + VEC * c;
+  const bool in = col < cols;
+  const int64_t depth = held(a.depth), rows = held(a.rows), seam = held(a.seam);
+  const int64_t stride = int64_t(4) * splits * F::step;  // of the contraction, from step to step
+  const int64_t first = (int64_t(split) * 4 + wave) * F::step;
+  const int64_t steps = first < depth ? (depth - first + stride - 1) / stride : 0;
+  // rows behind the last repeat it and are not stored
+  const T* zs = static_cast<const T*>(a.p.p) + (c < rows ? c : rows - 1) * a.p.ld;
+  const T* const q[2] = {held(static_cast<const T*>(a.q[0].p)), held(static_cast<const T*>(a.q[1].p))};
+  const int64_t ld_q[2] = {held(a.q[0].ld), held(a.q[1].ld)};
+  u32x4 w[D][VEC], z[D];
+  auto load = [&](int slot, int64_t t) {
+    const int64_t k = first + t * stride + VEC * h;
+    const int64_t at = k < depth ? k : 0;
+    const bool up = at >= seam;
+    const int64_t ld = up ? ld_q[1] : ld_q[0];
+    const T* row = (up ? q[1] : q[0]) + (at - (up ? seam : 0)) * ld + (in ? col : 0);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      w[slot][i] = __builtin_nontemporal_load((const ADA_GLOBAL u32x4*)(row + i * ld));
+    z[slot] = *(const ADA_GLOBAL u32x4*)(zs + at);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  f32x16 acc[VEC] = {};
+  if (steps > 0) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(d, d);
+    for (int64_t t = 0; t < steps; t += D) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        const bool live = first + (t + d) * stride + VEC * h < depth;  // else zeros on both sides
+        u32x4 raw[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) raw[i] = live ? w[d][i] : u32x4{0, 0, 0, 0};
+        const u32x4 zf = live ? z[d] : u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[e] = mfma32<T>(zf, across_fragment<T>(raw, e), acc[e]);
+        load(d, t + d + D);
+      }
+    }
+  }
+  float* const part = held(a.part);
+  T* const y = held(static_cast<T*>(a.y[0].p));
+  const int64_t ld_y = held(a.y[0].ld);
+  // waves 2 and 3 to 0 and 1, then 1 to 0
+#pragma unroll 1
+  for (int half = 2; half >= 1; half >>= 1) {
+    if (wave >= half && wave < 2 * half) {
+      f32x4* to = lds + (wave - half) * VEC * 256 + lane;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          to[(e * 4 + v) * 64] = f32x4{acc[e][4 * v], acc[e][4 * v + 1], acc[e][4 * v + 2], acc[e][4 * v + 3]};
+    }
+    __syncthreads();
+    if (wave < half) {
+      const f32x4* from = lds + wave * VEC * 256 + lane;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const f32x4 o = from[(e * 4 + v) * 64];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[e][4 * v + i] += o[i];
+        }
+    }
+    __syncthreads();
+  }
+  if (wave != 0 || !in) return;
+#pragma unroll
+  for (int g = 0; g < 16; ++g) {
+    const int64_t r = 8 * (g >> 2) + 4 * h + (g & 3);
+    if (r >= rows) continue;
+    float v[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] = acc[e][g];
+    if (splits > 1) {
+      float* to = part + (split * rows + r) * cols + col;
+#pragma unroll
+      for (int e = 0; e < VEC; e += 4) *(ADA_GLOBAL f32x4*)(to + e) = f32x4{v[e], v[e + 1], v[e + 2], v[e + 3]};
+    } else {
+      store_vec<T>(y + r * ld_y + col, v);
+    }
+  }
+}
+
+// dx and dW, or one of them, in one grid: the one reads while the other writes.
+template <typename T, int ROWS>
+__global__ void __launch_bounds__(256, 2) few_rows_grad_kernel(GemmPair pair) {
+  __shared__ f32x4 lds[2 * FewGrad<T>::VEC * 256];
+  const int second = static_cast<int>(blockIdx.x) >= pair.first;
+  const GemmParams& a = pair.a[second];
+  const int block = static_cast<int>(blockIdx.x) - (second ? pair.first : 0);
+  if (a.form == kDx)
+    few_rows_dx<T>(a, block, lds);
+  else
+    few_rows_dw<T, ROWS>(a, block);
+}
+
+bool few_rows_grad(int64_t rows) { return rows <= 32; }
+
+// Into how many parts dx's contraction is split over workgroups.
+int few_rows_dx_splits(int64_t cols, int64_t depth, int esz) {
+  const int64_t strips = (cols * esz + 511) / 512, steps = (depth * esz + 31) / 32;
+  int64_t splits = 256 / strips;
+  if (splits > steps / 16) splits = steps / 16;
+  return static_cast<int>(splits < 2 ? 1 : splits > 32 ? 32 : splits);
+}
+
+template <typename T, int ROWS>
+hipError_t launch_few_rows_grad(const GemmParams* a, int n, hipStream_t s) {
+  using F = FewGrad<T>;
+  GemmPair pair{};
+  int64_t grid = 0;
+  for (int i = 0; i < n; ++i) {
+    pair.a[i] = a[i];
+    if (i == 1) pair.first = static_cast<int32_t>(grid);
+    const int64_t strips = (a[i].cols + F::cols - 1) / F::cols;
+    grid += strips * (a[i].form == kDx ? a[i].splits : (a[i].rows + F::dw_rows - 1) / F::dw_rows);
+  }
+  if (n == 1) pair.first = static_cast<int32_t>(grid);
+  few_rows_grad_kernel<T, ROWS><<<static_cast<unsigned>(grid), 256, 0, s>>>(pair);
+  return hipGetLastError();
+}
+
 // ---- slopes ---------------------------------------------------------------------------
 // 64 x 64 tiles of dz.
 constexpr int kSide = 64;
@@ -1336,7 +1586,10 @@ GradPlan plan_grad(int64_t rows, int64_t n, int64_t k, int act, int gated, int e
   g.dz = take(gated || act != ADA_ACT_NONE ? rows * parts * n * esz : 0);
   g.sums = take((rows + kSide - 1) / kSide * parts * n * 4);
   const Product dx{rows, k, parts * n, esz}, dw{parts * n, k, rows, esz};
-  g.pair = plan_pair(dx, dw);
+  if (few_rows_grad(rows))
+    g.pair = {true, {{0, few_rows_dx_splits(k, parts * n, esz), 1.f}, {0, 1, 0.f}}};
+  else
+    g.pair = plan_pair(dx, dw);
   g.part[0] = take(part_bytes(dx, g.pair.plan[0].splits));
   g.part[1] = take(part_bytes(dw, g.pair.plan[1].splits));
   return g;
@@ -1432,7 +1685,12 @@ hipError_t launch_linear_grad_t(const LinearGradParams& p, void* ws, hipStream_t
       d->depth = p.rows;
     }
   }
-  if (count == 2 && g.pair.together) {
+  if (count > 0 && few_rows_grad(p.rows)) {
+    if (p.rows <= 16)
+      ADA_TRY((launch_few_rows_grad<T, 16>(a, count, s)));
+    else
+      ADA_TRY((launch_few_rows_grad<T, 32>(a, count, s)));
+  } else if (count == 2 && g.pair.together) {
     ADA_TRY((launch_products<T, false, true>(tile[0], a, 2, s)));
   } else {
     for (int i = 0; i < count; ++i) ADA_TRY((launch_products<T, false, true>(tile[i], a + i, 1, s)));
