@@ -563,3 +563,94 @@ def test_one_matrix_for_both_projections(dtype):
     a = A.ada_glu_backward(d["dy"], d["x"], d["w0"], d["w0"], z, z, act="relu", want_dbias=True)
     b = A.ada_glu_backward(d["dy"], d["x"], d["w0"], d["w0"].clone(), z, z.clone(), act="relu", want_dbias=True)
     assert all(torch.equal(s, t) for s, t in zip(a, b))
+
+
+# weights large enough for the few-rows gradients: a row or two, around 16 and 32 rows and past
+# them; d_out and d_in off the waves' 64 rows, 256 columns and contraction steps; long and short
+# contractions (in many parts, in one)
+FEW_GRADS = [(1, 1288, 2056), (2, 33000, 72), (7, 2056, 1288), (15, 4104, 520), (16, 72, 33000), (17, 520, 8200),
+             (31, 18056, 264), (32, 1288, 4104)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ("fp32", "bf16"))
+@pytest.mark.parametrize("shape", FEW_GRADS, ids=lambda s: "x".join(map(str, s)))
+def test_few_rows_gradients(shape, dtype):
+    check_linear_backward(*shape, dtype, "silu", pad=8, seed=51)
+    check_glu_backward(*shape, dtype, "relu", pad=16, seed=52)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(33, 4104, 4120), (49, 1288, 13064), (64, 16904, 1000)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_two_blocks_of_rows_gradients(shape):
+    check_linear_backward(*shape, "bf16", "none", seed=53)
+    rows, d_out, d_in = shape
+    check_glu_backward(rows, d_out // 16 * 8, d_in, "bf16", "silu", pad=8, seed=54)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ("fp32", "bf16"))
+@pytest.mark.parametrize("rows", (5, 17, 50))
+def test_few_rows_gradients_alone_captured_and_with_infinities(rows, dtype):
+    d_out, d_in = 4104, 4120
+    n, d = inputs(55, rows, d_out, d_in, dtype, parts=2)
+    z, u = H.normal(56, (rows, d_out), 1.0, dtype).to(DEV), H.normal(57, (rows, d_out), 1.0, dtype).to(DEV)
+    args = (d["dy"], d["x"], d["w0"], d["w1"], z, u)
+    full = A.ada_glu_backward(*args, want_dbias=True)
+    dx = torch.empty_like(full[0])
+    A.ada_glu_backward(*args, dx=dx, want_dw=False)
+    assert torch.equal(dx, full[0])
+    for h, name in ((1, "dw_gate"), (2, "dw_up")):
+        one = torch.full_like(full[h], float("nan"))
+        A.ada_glu_backward(*args, **{name: one}, want_dx=False, want_dw=False)
+        assert torch.equal(one, full[h]), name
+
+    outs = [torch.empty_like(t) for t in full]
+    ws = torch.empty(A.glu_backward_workspace_bytes(rows, d_out, d_in, "silu", H.TD[dtype]), dtype=torch.uint8, device=DEV)
+
+    def call():
+        A.ada_glu_backward(*args, dx=outs[0], dw_gate=outs[1], dw_up=outs[2], dbias_gate=outs[3], dbias_up=outs[4],
+                           workspace=ws)
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(3):
+        for t in outs:
+            t.fill_(float("nan"))
+        ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, full))
+        A.ada_glu_backward(*args)
+
+    # an infinity reaches its own column of a gradient and no other element
+    dz, x, w = d["dy"], d["x"].clone(), d["w0"].clone()
+    dx, dw, _ = A.ada_linear_backward(dz, x, w)
+    x[0, 5], w[0, 7], w[d_out - 1, 9] = float("inf"), float("-inf"), float("inf")
+    ix, iw, _ = A.ada_linear_backward(dz, x, w)
+    fx, fw = ix.isfinite(), iw.isfinite()
+    assert not fx[:, [7, 9]].any() and not fw[:, 5].any()
+    fx[:, [7, 9]], fw[:, 5] = True, True
+    assert fx.all() and fw.all()
+    keep_x, keep_w = torch.ones(d_in, dtype=torch.bool, device=DEV), torch.ones(d_in, dtype=torch.bool, device=DEV)
+    keep_x[[7, 9]] = False
+    keep_w[5] = False
+    assert torch.equal(ix[:, keep_x], dx[:, keep_x]) and torch.equal(iw[:, keep_w], dw[:, keep_w])
+
+
+@pytest.mark.gpu
+def test_few_rows_gradients_of_far_apart_rows():
+    rows, d_out, d_in, ld = 19, 4104, 520, 600_000  # 4.9 GB from the first row to the last
+    n, d = inputs(58, rows, d_out, d_in, "bf16")
+    w = torch.empty((d_out, ld), dtype=torch.bfloat16, device=DEV)[:, :d_in]
+    dw = torch.empty((d_out, ld), dtype=torch.bfloat16, device=DEV)[:, :d_in]
+    w.copy_(d["w0"])
+    dx, _, _ = A.ada_linear_backward(d["dy"], d["x"], w, dw=dw)
+    rx, rw, _, _ = OL.linear_backward(n["dy"], n["x"], n["w0"], None)
+    bounds = H.grad_bounds([n["dy"]], [np.zeros_like(n["dy"])], n["x"], [n["w0"]], "bf16")
+    H.assert_within(dx, rx, bounds[0], "dx")
+    H.assert_within(dw, rw, bounds[1], "dw")

@@ -666,25 +666,32 @@ __global__ void __launch_bounds__(C::threads, C::per_simd) gemm_kernel(GemmPair 
   }
 }
 
-// Join a split contraction: eight columns per thread, the parts' sums in order, then the epilogue.
+// Lanes that share eight columns' parts in a join: with many parts of a small matrix there are
+// few threads, each with a long chain of loads (dx of 17 x 18048 x 1784 in 32 parts: 31.3 us with
+// one lane, 24.1 with four).
+__host__ __device__ inline int join_lanes(int splits) { return splits >= 8 ? 4 : 1; }
+
+// Join a split contraction: eight columns per thread or four threads, the parts' sums in a fixed
+// order, then the epilogue.
 template <typename T, bool GATED>
 __device__ __forceinline__ void join_parts(const GemmParams& a, int block) {
   constexpr int NQ = GATED ? 2 : 1;
   const int64_t groups = a.rows * (a.cols / 8);
-  const int64_t v = block * 256ll + threadIdx.x;
+  const int lanes = join_lanes(a.splits), lane = threadIdx.x & (lanes - 1);
+  const int64_t v = block * int64_t(256 / lanes) + threadIdx.x / lanes;
   if (v >= groups) return;
   const int64_t m = v / (a.cols / 8);
   const int64_t n = (v - m * (a.cols / 8)) * 8;
   const Epilogue<T, GATED> ep(a);
   float z[NQ][8] = {};
   constexpr int kAhead = GATED ? 4 : 8;  // parts whose loads are in flight together
-  for (int s0 = 0; s0 < a.splits; s0 += kAhead) {
+  for (int s0 = lane; s0 < a.splits; s0 += kAhead * lanes) {
     float t[kAhead][NQ][8];
 #pragma unroll
     for (int s = 0; s < kAhead; ++s)
 #pragma unroll
       for (int h = 0; h < NQ; ++h) {
-        const int from = s0 + s < a.splits ? s0 + s : s0;
+        const int from = s0 + s * lanes < a.splits ? s0 + s * lanes : s0;
         load8(a.part + ((int64_t(from) * NQ + h) * a.rows + m) * a.cols + n, t[s][h]);
       }
 #pragma unroll
@@ -693,7 +700,17 @@ __device__ __forceinline__ void join_parts(const GemmParams& a, int block) {
       for (int h = 0; h < NQ; ++h)
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (s0 + s < a.splits) z[h][e] += t[s][h][e];
+          if (s0 + s * lanes < a.splits) z[h][e] += t[s][h][e];
+  }
+  if (lanes > 1) {  // the four threads of a group are next to each other, and all here
+#pragma unroll
+    for (int h = 0; h < NQ; ++h)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        z[h][e] += __shfl_xor(z[h][e], 1, 64);
+        z[h][e] += __shfl_xor(z[h][e], 2, 64);
+      }
+    if (lane != 0) return;
   }
   ep.finish8(m, n, z);
 }
@@ -1100,7 +1117,7 @@ hipError_t launch_joins(const GemmParams* a, int n, const BiasParams* bias, hipS
   for (int i = 0; i < n; ++i) {
     if (a[i].splits <= 1) continue;
     j.pair.a[used++] = a[i];
-    grid += (a[i].rows * (a[i].cols / 8) + 255) / 256;
+    grid += (a[i].rows * (a[i].cols / 8) * join_lanes(a[i].splits) + 255) / 256;
     if (used == 1) j.pair.first = static_cast<int32_t>(grid);
   }
   j.bias_first = static_cast<int32_t>(grid);
@@ -1224,7 +1241,8 @@ hipError_t launch_forward(GemmParams a, float* part, hipStream_t s) {
 }
 
 // ---- gradients of few rows -------------------------------------------------------------
-// Up to 32 rows: dx is bound by reading W once, dW by writing it once, so no operand goes
+// Up to 32 or 64 rows: dx is bound by reading W once, dW by writing it once (32 x 11008 x 4096: 29
+// and 21 us, both in one grid 40, 4.5 TB/s; on the tiles 57, 77 and 95), so no operand goes
 // through LDS.  Both products have an operand whose rows lie across the contraction (W, x): a
 // lane reads VEC neighbouring columns of VEC such rows, 16 bytes each, and has with them VEC
 // fragments whose x-th column is its VEC c + x; the sums of all fragments in a lane are then VEC
@@ -1337,9 +1355,10 @@ __device__ __forceinline__ void few_rows_dw(const GemmParams& a, int block) {
   }
 }
 
-// dx = dz W: the waves of all workgroups of a strip of columns share W's rows, step by step in
-// turn; a workgroup's sums meet in LDS in a fixed order, and the workgroups' in the join.
-template <typename T>
+// dx = dz W, QF blocks of 32 rows: the waves of all workgroups of a strip of columns share W's
+// rows, step by step in turn; a workgroup's sums meet in LDS in a fixed order, and the workgroups'
+// in the join.
+template <typename T, int QF>
 __device__ __forceinline__ void few_rows_dx(const GemmParams& a, int block, f32x4* lds) {
   using F = FewGrad<T>;
   constexpr int VEC = F::VEC, D = F::ahead;
@@ -1354,10 +1373,13 @@ __device__ __forceinline__ void few_rows_dx(const GemmParams& a, int block, f32x
   const int64_t first = (int64_t(split) * 4 + wave) * F::step;
   const int64_t steps = first < depth ? (depth - first + stride - 1) / stride : 0;
   // rows behind the last repeat it and are not stored
-  const T* zs = static_cast<const T*>(a.p.p) + (c < rows ? c : rows - 1) * a.p.ld;
+  const T* zs[QF];
+#pragma unroll
+  for (int f = 0; f < QF; ++f)
+    zs[f] = static_cast<const T*>(a.p.p) + (32 * f + c < rows ? 32 * f + c : rows - 1) * a.p.ld;
   const T* const q[2] = {held(static_cast<const T*>(a.q[0].p)), held(static_cast<const T*>(a.q[1].p))};
   const int64_t ld_q[2] = {held(a.q[0].ld), held(a.q[1].ld)};
-  u32x4 w[D][VEC], z[D];
+  u32x4 w[D][VEC], z[D][QF];
   auto load = [&](int slot, int64_t t) {
     const int64_t k = first + t * stride + VEC * h;
     const int64_t at = k < depth ? k : 0;
@@ -1367,10 +1389,11 @@ __device__ __forceinline__ void few_rows_dx(const GemmParams& a, int block, f32x
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
       w[slot][i] = __builtin_nontemporal_load((const ADA_GLOBAL u32x4*)(row + i * ld));
-    z[slot] = *(const ADA_GLOBAL u32x4*)(zs + at);
+#pragma unroll
+    for (int f = 0; f < QF; ++f) z[slot][f] = *(const ADA_GLOBAL u32x4*)(zs[f] + at);
     __builtin_amdgcn_sched_barrier(0);
   };
-  f32x16 acc[VEC] = {};
+  f32x16 acc[QF][VEC] = {};
   if (steps > 0) {
 #pragma unroll
     for (int d = 0; d < D; ++d) load(d, d);
@@ -1378,12 +1401,17 @@ __device__ __forceinline__ void few_rows_dx(const GemmParams& a, int block, f32x
 #pragma unroll
       for (int d = 0; d < D; ++d) {
         const bool live = first + (t + d) * stride + VEC * h < depth;  // else zeros on both sides
-        u32x4 raw[VEC];
+        u32x4 raw[VEC], zf[QF];
 #pragma unroll
         for (int i = 0; i < VEC; ++i) raw[i] = live ? w[d][i] : u32x4{0, 0, 0, 0};
-        const u32x4 zf = live ? z[d] : u32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) acc[e] = mfma32<T>(zf, across_fragment<T>(raw, e), acc[e]);
+        for (int f = 0; f < QF; ++f) zf[f] = live ? z[d][f] : u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const u32x4 wf = across_fragment<T>(raw, e);
+#pragma unroll
+          for (int f = 0; f < QF; ++f) acc[f][e] = mfma32<T>(zf[f], wf, acc[f][e]);
+        }
         load(d, t + d + D);
       }
     }
@@ -1391,65 +1419,78 @@ __device__ __forceinline__ void few_rows_dx(const GemmParams& a, int block, f32x
   float* const part = held(a.part);
   T* const y = held(static_cast<T*>(a.y[0].p));
   const int64_t ld_y = held(a.y[0].ld);
-  // waves 2 and 3 to 0 and 1, then 1 to 0
+#pragma unroll
+  for (int f = 0; f < QF; ++f) {
+    // waves 2 and 3 to 0 and 1, then 1 to 0
 #pragma unroll 1
-  for (int half = 2; half >= 1; half >>= 1) {
-    if (wave >= half && wave < 2 * half) {
-      f32x4* to = lds + (wave - half) * VEC * 256 + lane;
+    for (int half = 2; half >= 1; half >>= 1) {
+      if (wave >= half && wave < 2 * half) {
+        f32x4* to = lds + (wave - half) * VEC * 256 + lane;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e)
+        for (int e = 0; e < VEC; ++e)
 #pragma unroll
-        for (int v = 0; v < 4; ++v)
-          to[(e * 4 + v) * 64] = f32x4{acc[e][4 * v], acc[e][4 * v + 1], acc[e][4 * v + 2], acc[e][4 * v + 3]};
+          for (int v = 0; v < 4; ++v)
+            to[(e * 4 + v) * 64] =
+                f32x4{acc[f][e][4 * v], acc[f][e][4 * v + 1], acc[f][e][4 * v + 2], acc[f][e][4 * v + 3]};
+      }
+      __syncthreads();
+      if (wave < half) {
+        const f32x4* from = lds + wave * VEC * 256 + lane;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const f32x4 o = from[(e * 4 + v) * 64];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[f][e][4 * v + i] += o[i];
+          }
+      }
+      __syncthreads();
     }
-    __syncthreads();
-    if (wave < half) {
-      const f32x4* from = lds + wave * VEC * 256 + lane;
+    if (wave != 0 || !in) continue;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e)
+    for (int g = 0; g < 16; ++g) {
+      const int64_t r = 32 * f + 8 * (g >> 2) + 4 * h + (g & 3);
+      if (r >= rows) continue;
+      float v[VEC];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const f32x4 o = from[(e * 4 + v) * 64];
+      for (int e = 0; e < VEC; ++e) v[e] = acc[f][e][g];
+      if (splits > 1) {
+        float* to = part + (split * rows + r) * cols + col;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[e][4 * v + i] += o[i];
-        }
-    }
-    __syncthreads();
-  }
-  if (wave != 0 || !in) return;
-#pragma unroll
-  for (int g = 0; g < 16; ++g) {
-    const int64_t r = 8 * (g >> 2) + 4 * h + (g & 3);
-    if (r >= rows) continue;
-    float v[VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) v[e] = acc[e][g];
-    if (splits > 1) {
-      float* to = part + (split * rows + r) * cols + col;
-#pragma unroll
-      for (int e = 0; e < VEC; e += 4) *(ADA_GLOBAL f32x4*)(to + e) = f32x4{v[e], v[e + 1], v[e + 2], v[e + 3]};
-    } else {
-      store_vec<T>(y + r * ld_y + col, v);
+        for (int e = 0; e < VEC; e += 4) *(ADA_GLOBAL f32x4*)(to + e) = f32x4{v[e], v[e + 1], v[e + 2], v[e + 3]};
+      } else {
+        store_vec<T>(y + r * ld_y + col, v);
+      }
     }
   }
 }
 
 // dx and dW, or one of them, in one grid: the one reads while the other writes.
 template <typename T, int ROWS>
-__global__ void __launch_bounds__(256, 2) few_rows_grad_kernel(GemmPair pair) {
+__global__ void __launch_bounds__(256, ROWS > 32 ? 1 : 2) few_rows_grad_kernel(GemmPair pair) {
   __shared__ f32x4 lds[2 * FewGrad<T>::VEC * 256];
   const int second = static_cast<int>(blockIdx.x) >= pair.first;
   const GemmParams& a = pair.a[second];
   const int block = static_cast<int>(blockIdx.x) - (second ? pair.first : 0);
   if (a.form == kDx)
-    few_rows_dx<T>(a, block, lds);
+    few_rows_dx<T, (ROWS + 31) / 32>(a, block, lds);
   else
     few_rows_dw<T, ROWS>(a, block);
 }
 
-bool few_rows_grad(int64_t rows) { return rows <= 32; }
+// Sizes that take it.  Small matrices are ahead on the tiles (both gradients, tiles against this:
+// bf16 32 x 1024 x 1024 10.9 and 11.2 us, 32 x 512 x 8192 17.8 and 14.0; fp32 32 x 1024 x 1024 13.5
+// and 14.7, 32 x 4096 x 512 19.5 and 15.0).  Two blocks of rows leave one wave on a SIMD, which
+// pays for large ones in bf16 (64 x 4096 x 4096 37.2 and 37.5, 64 x 11008 x 4096 84 and 58), and
+// not in fp32, where the matrix pipes bind (64 x 4096 x 4096 69 and 69, 48 x 4096 x 512 21.6 and 21.9).
+bool few_rows_grad(int64_t rows, int64_t weight_bytes, int esz) {
+  return rows <= 32 ? weight_bytes > (int64_t(4) << 20)
+                    : rows <= 64 && esz == 2 && weight_bytes > (int64_t(32) << 20);
+}
 
-// Into how many parts dx's contraction is split over workgroups.
+// Into how many parts dx's contraction is split over workgroups: one workgroup per CU, and four
+// steps or more a wave.
 int few_rows_dx_splits(int64_t cols, int64_t depth, int esz) {
   const int64_t strips = (cols * esz + 511) / 512, steps = (depth * esz + 31) / 32;
   int64_t splits = 256 / strips;
@@ -1572,6 +1613,7 @@ hipError_t launch_linear_t(const LinearParams& p, void* ws, hipStream_t s) {
 // parts of split contractions.
 struct GradPlan {
   int64_t dz, sums, part[2], total;
+  bool few;
   PairPlan pair;  // dx, dW: the same whichever of the two is asked for, and so are their sums
 };
 
@@ -1586,7 +1628,8 @@ GradPlan plan_grad(int64_t rows, int64_t n, int64_t k, int act, int gated, int e
   g.dz = take(gated || act != ADA_ACT_NONE ? rows * parts * n * esz : 0);
   g.sums = take((rows + kSide - 1) / kSide * parts * n * 4);
   const Product dx{rows, k, parts * n, esz}, dw{parts * n, k, rows, esz};
-  if (few_rows_grad(rows))
+  g.few = few_rows_grad(rows, parts * n * k * esz, esz);
+  if (g.few)
     g.pair = {true, {{0, few_rows_dx_splits(k, parts * n, esz), 1.f}, {0, 1, 0.f}}};
   else
     g.pair = plan_pair(dx, dw);
@@ -1685,11 +1728,14 @@ hipError_t launch_linear_grad_t(const LinearGradParams& p, void* ws, hipStream_t
       d->depth = p.rows;
     }
   }
-  if (count > 0 && few_rows_grad(p.rows)) {
-    if (p.rows <= 16)
+  if (count > 0 && g.few) {
+    if (p.rows <= 16) {
       ADA_TRY((launch_few_rows_grad<T, 16>(a, count, s)));
-    else
+    } else if (p.rows <= 32) {
       ADA_TRY((launch_few_rows_grad<T, 32>(a, count, s)));
+    } else if constexpr (sizeof(T) == 2) {
+      ADA_TRY((launch_few_rows_grad<T, 64>(a, count, s)));
+    }
   } else if (count == 2 && g.pair.together) {
     ADA_TRY((launch_products<T, false, true>(tile[0], a, 2, s)));
   } else {
