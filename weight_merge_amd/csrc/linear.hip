@@ -321,7 +321,7 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 q, u32x4 p, f32x16 acc) {
 // k lies at v ^ spread(k), so that the two halves of a wave, eight k apart, read different banks.
 //
 // The large tiles are bound by the matrix pipes at the clock that their power allows (256 x 256
-// at 4096 x 8192 x 28672: 1.40 ms, 1370 TFLOP/s, pipes 84% busy; with its copies taken out, 1640).
+// at 4096 x 8192 x 28672: 1.40 ms, 1375 TFLOP/s, pipes 84% busy; with its copies taken out, 1640).
 // One wave per SIMD with 128 x 128 sums in its accumulation registers reads two thirds of the LDS
 // bytes of two waves with 128 x 64 each (1280 TFLOP/s).  128 bytes of k a row, because 64-byte
 // segments cost the caches a third of their rate (1130 TFLOP/s).  The smaller tiles, for fewer
@@ -1572,8 +1572,8 @@ struct SlopeParams {
 };
 
 // dz = dy act'(z), or dg = dy u act'(g), du = dy act(g), and the tile's column sums, in one pass
-// over dy and the saved pre-activations: bound by memory (gated, 4096 x 11008: 450 MB in 86 us,
-// 5.2 TB/s).
+// over dy and the saved pre-activations: bound by memory (gated, 4096 x 11008: 450 MB in 75 us,
+// 6.0 TB/s).
 template <typename T, bool GATED>
 __global__ void __launch_bounds__(256) slope_kernel(SlopeParams a) {
   constexpr int VEC = 16 / sizeof(T), PER = kSide / VEC, RSTEP = 256 / PER;
