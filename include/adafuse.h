@@ -263,6 +263,9 @@ int ada_lora_batch(const ada_lora_proj* projs, int32_t n_proj, int32_t nb, int32
 /*
  * Activations of the linear and gated products.  GELU is the error-function form
  * z Phi(z); GELU_TANH its tanh approximation 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))).
+ * At +inf each is +inf; at -inf RELU is 0, NONE -inf, and the others the formula's
+ * -inf * 0 = NaN.  Slopes take their limits there, 1 and 0.  NaN stays NaN, but for RELU's
+ * slope, which is 1 where z > 0 and else 0.
  */
 typedef enum {
   ADA_ACT_NONE = 0,

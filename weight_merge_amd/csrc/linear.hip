@@ -73,6 +73,9 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
 }
 
 // ---- activations: value and slope in fp32 --------------------------------------------
+// At +inf the values are +inf; at -inf they are the formula's -inf * 0 = NaN (relu 0).  The
+// slopes take their limits, 1 and 0: far out, where the part that falls off is 0, its factor z
+// may be infinite and is left out.  NaN stays NaN (relu's slope is a comparison).
 // Everything from one exponential and one reciprocal, each within a unit in the last place, as
 // the instructions give them: in the epilogue of a short contraction the activation is a large
 // part of the time (1838 x 14248 x 192: gelu 56 us, with erfcf 86; silu 44, with expf and a
@@ -118,8 +121,8 @@ __device__ __forceinline__ float act_value(float z, int act) {
     case ADA_ACT_RELU: return z < 0.f ? 0.f : z;  // NaN stays NaN
     case ADA_ACT_SILU: return z * logistic(z, e);
     case ADA_ACT_GELU: {
-      const float tail = z * normal_tail(z, e);
-      return z < 0.f ? tail : z - tail;
+      const float tail = normal_tail(z, e);  // 0 far out: z - z tail is z there, infinite ones too
+      return z < 0.f ? z * tail : tail == 0.f ? z : z - z * tail;
     }
     case ADA_ACT_GELU_TANH: return z * logistic(twice_inner(z), e);
     default: return z;
@@ -147,12 +150,12 @@ __device__ __forceinline__ float act_slope(float z, int act) {
   switch (act) {
     case ADA_ACT_RELU: return z > 0.f ? 1.f : 0.f;
     case ADA_ACT_SILU: {
-      const float s = logistic(z, e);  // 1 - s is e s
-      return s == 0.f ? 0.f : s * (1.f + z * (e * s));
+      const float s = logistic(z, e), fall = e * s;  // 1 - s
+      return s == 0.f ? 0.f : fall == 0.f ? s : s * (1.f + z * fall);
     }
     case ADA_ACT_GELU: {
       const float tail = normal_tail(z, e);
-      return (z < 0.f ? tail : 1.f - tail) + z * kInvSqrt2Pi * e;
+      return (z < 0.f ? tail : 1.f - tail) + (e == 0.f ? 0.f : z * kInvSqrt2Pi * e);
     }
     case ADA_ACT_GELU_TANH: {
       const float s = logistic(twice_inner(z), e);
