@@ -1029,7 +1029,7 @@ hipError_t launch_few_rows(const GemmParams& a, hipStream_t s) {
 // one wave per W row (gated: per pair), lanes along it with 16-byte loads, U vectors of each row
 // in flight before any is used, x from the caches.  Eight waves hold eight consecutive columns,
 // which the epilogue takes together.  Past the row's end a lane re-reads its first vector and
-// multiplies it by a zero x.
+// drops the product (a zero x would make an infinite weight there NaN).
 template <typename T>
 __device__ __forceinline__ float dot16(u32x4 w, u32x4 x, float acc) {
 #pragma unroll
@@ -1069,9 +1069,12 @@ __global__ void __launch_bounds__(512) one_row_kernel(GemmParams a) {
     __builtin_amdgcn_sched_barrier(0);  // every load before the first use
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const u32x4 d = v0 + 64 * u + lane < nvec ? xv[u] : u32x4{0, 0, 0, 0};
+      const bool in = v0 + 64 * u + lane < nvec;
 #pragma unroll
-      for (int h = 0; h < NQ; ++h) acc[h] = dot16<T>(wv[h][u], d, acc[h]);
+      for (int h = 0; h < NQ; ++h) {
+        const float sum = dot16<T>(wv[h][u], xv[u], acc[h]);
+        acc[h] = in ? sum : acc[h];
+      }
     }
   }
 #pragma unroll
