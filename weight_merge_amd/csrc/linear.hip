@@ -76,10 +76,13 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
 // At +inf the values are +inf; at -inf they are the formula's -inf * 0 = NaN (relu 0).  The
 // slopes take their limits, 1 and 0: far out, where the part that falls off is 0, its factor z
 // may be infinite and is left out.  NaN stays NaN (relu's slope is a comparison).
-// Everything from one exponential and one reciprocal, each within a unit in the last place, as
-// the instructions give them: in the epilogue of a short contraction the activation is a large
-// part of the time (1838 x 14248 x 192: gelu 56 us, with erfcf 86; silu 44, with expf and a
-// division 62; none 38).  They stay within a few 2^-24 (1 + |z|) of the functions.
+// Outputs stored in bf16 take everything from one exponential and one reciprocal, as the
+// instructions give them: in the epilogue of a short contraction the activation is a large part
+// of the time (1838 x 14248 x 192: gelu 56 us, with erfcf 86; silu 44, with expf and a division
+// 62; none 38).  The exponent's rounding makes their tails up to (|z| + 8) 2^-23 (silu) or
+// (z^2 + 20) 2^-23 (gelu) of the value off, a small part of bf16's half step of 2^-8 wherever the
+// value is not 0.  Outputs stored in fp32 (T = float) are owed those bits: expf, a division, and
+// the exponent of gelu's tail with its rounding made good.
 constexpr float kLog2E = 1.44269504088896340f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kSqrt2OverPi = 0.79788456080286536f;
@@ -91,9 +94,19 @@ __device__ __forceinline__ float rcp_fast(float v) { return __builtin_amdgcn_rcp
 // Phi(-|z|) for the normal distribution's Phi, and e = exp(-z^2 / 2), from
 // Phi(-|z|) = erfc(|z| / sqrt 2) / 2 = e t P(t), t = 1 / (1 + 0.38 |z| / sqrt 2): P is fitted to
 // exp(x^2) erfc(x) / (2 t), x up to 14, within 3e-8 of it.  No cancellation for z << 0.
+template <typename T>
 __device__ __forceinline__ float normal_tail(float z, float& e) {
-  e = exp2_fast(-0.5f * kLog2E * z * z);
-  const float t = rcp_fast(1.f + 0.26870057685088807f * fabsf(z));
+  const float d = 1.f + 0.26870057685088807f * fabsf(z);
+  float t;
+  if constexpr (sizeof(T) == 4) {
+    const float zz = z * z;
+    e = expf(-0.5f * zz);
+    if (e > 0.f) e = fmaf(e, -0.5f * fmaf(z, z, -zz), e);  // what z * z was rounded by
+    t = 1.f / d;
+  } else {
+    e = exp2_fast(-0.5f * kLog2E * z * z);
+    t = rcp_fast(d);
+  }
   float q = 0.029212618f;
   q = q * t - 0.12993799f;
   q = q * t + 0.17968433f;
@@ -107,7 +120,12 @@ __device__ __forceinline__ float normal_tail(float z, float& e) {
 }
 
 // 1 / (1 + e), e = exp(-z).
+template <typename T>
 __device__ __forceinline__ float logistic(float z, float& e) {
+  if constexpr (sizeof(T) == 4) {
+    e = expf(-z);
+    return 1.f / (1.f + e);
+  }
   e = exp2_fast(-kLog2E * z);
   return rcp_fast(1.f + e);
 }
@@ -115,25 +133,27 @@ __device__ __forceinline__ float logistic(float z, float& e) {
 // What gelu_tanh's tanh is taken of, twice: (1 + tanh v) / 2 = logistic(2 v).
 __device__ __forceinline__ float twice_inner(float z) { return 2.f * kSqrt2OverPi * (z + kCubic * z * z * z); }
 
+template <typename T>
 __device__ __forceinline__ float act_value(float z, int act) {
   float e;
   switch (act) {
     case ADA_ACT_RELU: return z < 0.f ? 0.f : z;  // NaN stays NaN
-    case ADA_ACT_SILU: return z * logistic(z, e);
+    case ADA_ACT_SILU: return z * logistic<T>(z, e);
     case ADA_ACT_GELU: {
-      const float tail = normal_tail(z, e);  // 0 far out: z - z tail is z there, infinite ones too
+      const float tail = normal_tail<T>(z, e);  // 0 far out: z - z tail is z there, infinite ones too
       return z < 0.f ? z * tail : tail == 0.f ? z : z - z * tail;
     }
-    case ADA_ACT_GELU_TANH: return z * logistic(twice_inner(z), e);
+    case ADA_ACT_GELU_TANH: return z * logistic<T>(twice_inner(z), e);
     default: return z;
   }
 }
 
 // One choice of the activation for eight values.
+template <typename T>
 __device__ __forceinline__ void act_values(float (&z)[8], int act) {
 #define ADA_EACH(a)                                         \
   case a:                                                   \
-    _Pragma("unroll") for (int e = 0; e < 8; ++e) z[e] = act_value(z[e], a); \
+    _Pragma("unroll") for (int e = 0; e < 8; ++e) z[e] = act_value<T>(z[e], a); \
     break;
   switch (act) {
     ADA_EACH(ADA_ACT_RELU)
@@ -145,20 +165,21 @@ __device__ __forceinline__ void act_values(float (&z)[8], int act) {
 #undef ADA_EACH
 }
 
+template <typename T>
 __device__ __forceinline__ float act_slope(float z, int act) {
   float e;
   switch (act) {
     case ADA_ACT_RELU: return z > 0.f ? 1.f : 0.f;
     case ADA_ACT_SILU: {
-      const float s = logistic(z, e), fall = e * s;  // 1 - s
+      const float s = logistic<T>(z, e), fall = e * s;  // 1 - s
       return s == 0.f ? 0.f : fall == 0.f ? s : s * (1.f + z * fall);
     }
     case ADA_ACT_GELU: {
-      const float tail = normal_tail(z, e);
+      const float tail = normal_tail<T>(z, e);
       return (z < 0.f ? tail : 1.f - tail) + (e == 0.f ? 0.f : z * kInvSqrt2Pi * e);
     }
     case ADA_ACT_GELU_TANH: {
-      const float s = logistic(twice_inner(z), e);
+      const float s = logistic<T>(twice_inner(z), e);
       const float fall = e * s * s;  // s (1 - s): 0 far out, where z * z may be infinite
       return s == 0.f ? 0.f : s + (fall > 0.f ? 2.f * kSqrt2OverPi * z * fall * (1.f + 3.f * kCubic * z * z) : 0.f);
     }
@@ -259,7 +280,7 @@ struct Epilogue {
       }
       if (pre[h] != nullptr) store8<STREAM>(pre[h] + m * ld_pre[h] + n, z[h]);
     }
-    act_values(z[0], act);
+    act_values<T>(z[0], act);
     if constexpr (GATED) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) z[0][e] *= z[1][e];
@@ -1602,10 +1623,10 @@ __global__ void __launch_bounds__(256) slope_kernel(SlopeParams a) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const float dv = to_f32<T>(d.e[e]), zv = to_f32<T>(z.e[e]);
-        float g = dv * act_slope(zv, a.act);
+        float g = dv * act_slope<T>(zv, a.act);
         if constexpr (GATED) {
           g *= to_f32<T>(u.e[e]);
-          const float w = dv * act_value(zv, a.act);
+          const float w = dv * act_value<T>(zv, a.act);
           sum[1][e] += w;
           out[1].e[e] = from_f32<T>(w);
         }
