@@ -405,10 +405,20 @@ def _current(dev: int):
         raise ValueError(f"tensors are on cuda:{dev}, but cuda:{torch.cuda.current_device()} is current")
 
 
-def _on(stream):
-    """Makes the call's stream the current one, so that what the call allocates is made ready,
-    and taken back, in that stream's order."""
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+def _on(stream, call, *args):
+    """The call with its stream as the current one, so that what it allocates is made ready, and
+    taken back, in that stream's order.  The tensors passed to it are marked as used there: the
+    allocator then gives out their memory, if the caller drops them, only behind this work.
+    (A foreign stream may be gone when the allocator asks it, so for those the caller keeps them.)"""
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(s):
+        out = call(*args)
+    if not isinstance(s, torch.cuda.ExternalStream):
+        for a in args:
+            for t in a if isinstance(a, (tuple, list)) else (a,):
+                if isinstance(t, torch.Tensor) and t.is_cuda:
+                    t.record_stream(s)
+    return out
 
 
 def _raw_stream(dev: int) -> int:
@@ -463,10 +473,14 @@ def ada_linear(x: torch.Tensor, w: torch.Tensor, bias=None, residual=None, act: 
     matrix may be strided); `pre`, if given, receives x w^T + bias for the backward pass.
 
     act: "none", "relu", "silu", "gelu" (error function) or "gelu_tanh".  y may be the
-    residual itself.  A workspace and a y not passed are allocated on the call's stream."""
+    residual itself.  A workspace and a y not passed are allocated on the call's stream.
+
+    `stream` (here and in the calls like this one): a torch.cuda.Stream, or the handle of one,
+    else the current stream.  Work queued elsewhere before the call is not waited for.  Tensors
+    passed with a torch.cuda.Stream may be dropped at once; with a handle or an ExternalStream
+    keep those that belong to another stream until the work is done."""
     if stream is not None:
-        with _on(stream):
-            return ada_linear(x, w, bias, residual, act, y, pre, workspace)
+        return _on(stream, ada_linear, x, w, bias, residual, act, y, pre, workspace)
     rows, d_out, d_in = _sizes(x, w)
     code, dc, dt, dev = _act(act), _dtype(x), x.dtype, x.get_device()
     px, ldx = _mat(x, rows, d_in, dt, dev, "x")
@@ -493,8 +507,8 @@ def ada_linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, pre=
     sum of dz over rows; None for what is neither passed nor wanted.  `pre` is what
     ada_linear saved (not needed for act "none")."""
     if stream is not None:
-        with _on(stream):
-            return ada_linear_backward(dy, x, w, pre, act, dx, dw, dbias, want_dx, want_dw, want_dbias, workspace)
+        return _on(stream, ada_linear_backward, dy, x, w, pre, act, dx, dw, dbias, want_dx, want_dw, want_dbias,
+                   workspace)
     rows, d_out, d_in = _sizes(x, w)
     code, dc, dt, dev = _act(act), _dtype(x), x.dtype, x.get_device()
     if code == 0:
@@ -530,8 +544,7 @@ def ada_glu(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, bias_gate
     """y = act(g) u with g = x w_gate^T + bias_gate and u = x w_up^T + bias_up, in one pass;
     `pre`, if given, is a pair (g, u) of matrices to receive them for the backward pass."""
     if stream is not None:
-        with _on(stream):
-            return ada_glu(x, w_gate, w_up, bias_gate, bias_up, act, y, pre, workspace)
+        return _on(stream, ada_glu, x, w_gate, w_up, bias_gate, bias_up, act, y, pre, workspace)
     rows, d_out, d_in = _sizes(x, w_gate)
     code, dc, dt, dev = _act(act), _dtype(x), x.dtype, x.get_device()
     px, ldx = _mat(x, rows, d_in, dt, dev, "x")
@@ -562,9 +575,8 @@ def ada_glu_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_
     dg = dy u act'(g), du = dy act(g), dx = dg w_gate + du w_up, dw = d^T x, dbias the sums
     over rows; None for what is neither passed nor wanted."""
     if stream is not None:
-        with _on(stream):
-            return ada_glu_backward(dy, x, w_gate, w_up, gate_pre, up_pre, act, dx, dw_gate, dw_up, dbias_gate,
-                                    dbias_up, want_dx, want_dw, want_dbias, workspace)
+        return _on(stream, ada_glu_backward, dy, x, w_gate, w_up, gate_pre, up_pre, act, dx, dw_gate, dw_up,
+                   dbias_gate, dbias_up, want_dx, want_dw, want_dbias, workspace)
     rows, d_out, d_in = _sizes(x, w_gate)
     code, dc, dt, dev = _act(act), _dtype(x), x.dtype, x.get_device()
     if gate_pre is None or up_pre is None:
