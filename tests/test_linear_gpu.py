@@ -397,6 +397,7 @@ def test_large_gradients(shape, dtype):
 
 
 # every tile at both of its kinds of rounds, every few-rows block, split contractions, ragged ends
+# (of some products each: test_linear_plan.py has every form of every product, and counts them)
 VARIANTS = [(17, 1000, 4096), (33, 1000, 4096), (48, 8200, 264), (49, 8200, 264), (64, 4096, 1000),
             (250, 1000, 4104), (509, 4104, 520), (1000, 1032, 2056), (1021, 4104, 264), (2047, 4096, 264)]
 

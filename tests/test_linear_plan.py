@@ -1,0 +1,102 @@
+"""Every kernel form that the planner of the linear and gated products can choose, held against
+the fp64 oracle on the GPU; and, on the CPU, that the shapes here are all of them.
+
+The shapes are ragged (rows odd, dimensions off every tile), and where a contraction is tiled a
+workgroup has 10 steps of it at least, so that its ring of operands goes round.
+"""
+import random
+
+import pytest
+
+import linear_plans as P
+from test_linear_gpu import check_glu, check_glu_backward, check_linear, check_linear_backward
+
+# (call, type): shapes (rows, d_out, d_in)
+SHAPES = {
+    ("linear", "fp32"): [
+        (1, 24, 24), (3, 24, 4112), (3, 4128, 24), (15, 88, 152), (17, 32, 4152), (17, 4336, 24), (27, 104, 72),
+        (35, 24, 4056), (35, 4320, 32), (45, 112, 40), (49, 40, 312), (53, 24, 5800), (341, 17208, 312),
+        (525, 3704, 1272), (643, 1496, 304), (663, 720, 1008), (941, 2200, 312), (985, 2072, 1048),
+        (1091, 904, 1016), (1741, 2312, 1440), (1931, 3104, 304), (5611, 2416, 296)],
+    ("linear", "bf16"): [
+        (1, 24, 24), (3, 24, 8864), (3, 4128, 24), (15, 88, 152), (17, 24, 8616), (17, 4336, 24), (27, 104, 72),
+        (35, 24, 9192), (35, 4320, 32), (45, 112, 40), (49, 24, 616), (49, 32, 10512), (283, 17832, 584),
+        (335, 5896, 6168), (577, 1632, 3960), (725, 464, 4504), (1163, 3336, 7456), (1657, 2440, 600),
+        (1685, 1192, 584), (1723, 608, 584), (2101, 3984, 592), (2807, 648, 5840)],
+    ("glu", "fp32"): [
+        (1, 24, 24), (3, 24, 4112), (3, 4128, 24), (15, 88, 152), (17, 32, 4152), (17, 4336, 24), (27, 104, 72),
+        (35, 24, 4056), (35, 4320, 32), (45, 112, 40), (49, 40, 312), (53, 24, 5800), (291, 816, 952),
+        (387, 1160, 304), (593, 3376, 1488), (643, 1496, 304), (817, 1376, 1048), (903, 584, 936),
+        (1041, 3576, 360), (1091, 904, 1016), (3355, 1832, 352), (3485, 840, 296)],
+    ("glu", "bf16"): [
+        (1, 24, 24), (3, 24, 8864), (3, 4128, 24), (15, 88, 152), (17, 24, 8616), (17, 4336, 24), (27, 104, 72),
+        (35, 24, 9192), (35, 4320, 32), (45, 112, 40), (49, 24, 616), (49, 32, 10512), (263, 3552, 5536),
+        (385, 392, 4024), (449, 1032, 600), (649, 1560, 5816), (863, 584, 3800), (1087, 3424, 584),
+        (1093, 2016, 7096), (1685, 1192, 584), (1723, 608, 584), (3343, 1224, 584)],
+    ("linear_backward", "fp32"): [
+        (1, 160, 6584), (1, 520, 2024), (17, 216, 5208), (17, 288, 3656), (297, 296, 1624), (311, 304, 24),
+        (321, 352, 3688), (353, 2920, 1200), (437, 408, 14752), (453, 480, 6160), (525, 496, 1928),
+        (999, 648, 152), (1259, 1776, 664), (1283, 664, 720), (1733, 952, 136), (2751, 328, 1240),
+        (5073, 2576, 488)],
+    ("linear_backward", "bf16"): [
+        (1, 360, 5864), (1, 1712, 1232), (17, 1256, 1696), (21, 312, 6888), (33, 408, 14544), (33, 17584, 536),
+        (33, 18896, 928), (35, 13776, 664), (37, 9960, 360), (65, 7504, 2712), (77, 656, 8968), (91, 4448, 344),
+        (593, 616, 24), (631, 648, 856), (647, 592, 3376), (653, 88, 8504), (691, 584, 7960), (959, 592, 1312),
+        (1889, 1240, 88), (2805, 40, 7656), (3089, 24, 864), (3781, 24, 2616), (4149, 24, 3368), (5089, 72, 536)],
+    ("glu_backward", "fp32"): [
+        (1, 40, 13160), (1, 168, 3144), (17, 96, 5784), (17, 288, 1832), (299, 152, 48), (309, 152, 3336),
+        (315, 152, 10536), (385, 168, 1328), (415, 1512, 1144), (479, 240, 12968), (561, 328, 1696),
+        (1057, 536, 216), (1097, 624, 432), (1327, 352, 72), (1375, 2568, 200), (2975, 248, 1176),
+        (3219, 1632, 664)],
+    ("glu_backward", "bf16"): [
+        (1, 160, 6584), (1, 520, 2024), (17, 216, 5208), (17, 288, 3656), (35, 1888, 4472), (35, 3720, 928),
+        (35, 8400, 552), (37, 7080, 656), (39, 6248, 288), (75, 2256, 328), (87, 312, 9440), (581, 296, 24),
+        (637, 304, 776), (665, 40, 8288), (665, 400, 2704), (671, 304, 6544), (683, 312, 1568), (1909, 616, 88),
+        (2453, 24, 3728), (3781, 24, 2616), (4017, 5208, 136), (4513, 48, 328), (5431, 40, 552)],
+}
+CHECKS = {"linear": check_linear, "glu": check_glu, "linear_backward": check_linear_backward,
+          "glu_backward": check_glu_backward}
+CALLS = [(call, dtype, s) for (call, dtype), shapes in SHAPES.items() for s in shapes]
+
+
+def variants(so, call, dtype, shape, deep):
+    f = P.gradient_variants if call.endswith("backward") else P.forward_variants
+    return f(so, *shape, call.startswith("glu"), dtype, deep)
+
+
+@pytest.fixture(scope="module")
+def planner(tmp_path_factory):
+    return P.compile_planner(str(tmp_path_factory.mktemp("planner")))
+
+
+def test_the_shapes_reach_every_form(planner):
+    """Whatever 40000 drawn shapes reach, over all sizes up to far past every threshold, the
+    shapes of this file reach too."""
+    rng = random.Random(20)
+
+    def spread(lo, hi):
+        return int(round(lo * (hi / lo) ** rng.random()))
+
+    reached = set()
+    for _ in range(40000):
+        shape = (spread(1, 16384), 8 * spread(1, 4096), 8 * spread(1, 4096))
+        for call in CHECKS:
+            for dtype in ("fp32", "bf16"):
+                reached |= variants(planner, call, dtype, shape, False)
+    covered = set().union(*(variants(planner, *c, True) for c in CALLS))
+    assert reached <= covered, sorted(map(str, reached - covered))
+    # the forms that there are: one row; few rows in 1 to 3 blocks with two waves, or more and
+    # whole or split; six tiles whole or split; few-rows gradients; one grid or two
+    tiles = {v[2:4] for v in covered if len(v) == 5 and isinstance(v[2], int)}
+    assert tiles == {(256, 256), (256, 128), (128, 256), (128, 128), (64, 128), (64, 64)}
+    for dtype in ("fp32", "bf16"):
+        for name in ("linear", "glu", "dx", "dw", "glu dx", "glu dw"):
+            for t in tiles:
+                for cut in ("whole", "split"):
+                    assert (dtype, name, *t, cut) in covered, (dtype, name, t, cut)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("call, dtype, shape", CALLS, ids=lambda v: "x".join(map(str, v)) if isinstance(v, tuple) else v)
+def test_form(call, dtype, shape):
+    CHECKS[call](*shape, dtype, "silu", seed=sum(shape))
