@@ -100,3 +100,22 @@ def test_the_shapes_reach_every_form(planner):
 @pytest.mark.parametrize("call, dtype, shape", CALLS, ids=lambda v: "x".join(map(str, v)) if isinstance(v, tuple) else v)
 def test_form(call, dtype, shape):
     CHECKS[call](*shape, dtype, "silu", seed=sum(shape))
+
+
+# Gated gradients of 33 to 64 rows: the second block of 32 rows partly filled, the seam between the
+# two weights inside it, d_out off the waves' rows.
+TWO_BLOCKS = [(49, 648, 13064), (63, 2056, 4168), (34, 8536, 1000)]
+
+
+def test_two_blocks_of_rows_stay_on_their_kernel(planner):
+    for shape in TWO_BLOCKS:
+        assert ("bf16", "glu dw", "few-rows gradients", 64, "whole") in P.gradient_variants(planner, *shape, True, "bf16")
+    # 2 x 640 x 13064 is not large enough for it
+    assert ("bf16", "glu dw", "few-rows gradients", 64, "whole") not in P.gradient_variants(planner, 49, 640, 13064, True,
+                                                                                            "bf16")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", TWO_BLOCKS, ids=lambda s: "x".join(map(str, s)))
+def test_gated_gradients_of_two_blocks_of_rows(shape):
+    check_glu_backward(*shape, "bf16", "gelu", pad=8, seed=71)
