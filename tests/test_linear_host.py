@@ -244,3 +244,35 @@ def test_none_backward_ignores_pre():
     with pytest.raises(ValueError, match="on the device"):
         A.ada_linear_backward(cpu(4, 32), cpu(4, 64), cpu(32, 64), pre=cpu(1, 1), act="none")
     assert ADA_ACT_NONE == 0 and ADA_ACT_GELU == 3 and ctypes.sizeof(AdaLinearArgs) == 104
+
+
+EXTREMES = [(1 << 22, 8, 8), (8, 1 << 22, 8), (8, 8, 1 << 22), (1, 1 << 22, 1 << 13), (1 << 22, 1 << 13, 1 << 13),
+            (1 << 13, 1 << 22, 1 << 13), (1 << 13, 1 << 13, 1 << 22), (1 << 17, 1 << 18, 1 << 17), ((1 << 22) - 1, 8184, 8184),
+            (33, (1 << 22) - 8, 8), (48, 8192, 1 << 22), (32, 1 << 22, 8192), (64, 1 << 22, 8192), (1 << 22, 8, 8192)]
+
+
+@pytest.mark.parametrize("rows, n, k", EXTREMES)
+def test_workspaces_at_the_largest_sizes(rows, n, k):
+    """The plan of the largest rows, dimensions and matrices that are admitted: found, and no larger
+    than dz, its column sums and the parts of splits into 128 at most."""
+    lib = _lib.load()
+    for dt, e in ((ADA_F32, 4), (ADA_BF16, 2)):
+        for gated in (1, 2):
+            names = ("linear", "glu")[gated - 1]
+            forward = getattr(lib, f"ada_{names}_workspace")(rows, n, k, dt)
+            assert 0 <= forward <= 16 * 4 * rows * n * gated
+            for act in (ADA_ACT_NONE, ADA_ACT_GELU):
+                b = getattr(lib, f"ada_{names}_backward_workspace")(rows, n, k, act, dt)
+                dz = rows * n * gated * e if gated == 2 or act != ADA_ACT_NONE else 0
+                assert dz <= b <= dz + (rows // 64 + 1) * n * gated * 4 + 128 * 4 * (rows + gated * n) * k + 1024
+
+
+@pytest.mark.parametrize("rows, n, k", [((1 << 22) + 1, 8, 8), (1, (1 << 22) + 8, 8), (1, 8, (1 << 22) + 8),
+                                        (1 << 22, 8200, 8), (1 << 22, 8, 8200), (1, 1 << 22, 8200)])
+def test_larger_sizes_are_refused(rows, n, k):
+    lib = _lib.load()
+    for dt in (ADA_F32, ADA_BF16):
+        assert lib.ada_linear_workspace(rows, n, k, dt) == ADA_ESHAPE
+        assert lib.ada_glu_workspace(rows, n, k, dt) == ADA_ESHAPE
+        assert lib.ada_linear_backward_workspace(rows, n, k, ADA_ACT_NONE, dt) == ADA_ESHAPE
+        assert lib.ada_glu_backward_workspace(rows, n, k, ADA_ACT_SILU, dt) == ADA_ESHAPE
