@@ -28,7 +28,7 @@ extern "C" {
 void forward(int64_t rows, int64_t n, int64_t k, int gated, int esz, int32_t* out) {
   const Plan p = plan_forward(rows, n, k, gated, esz);
   out[0] = kTileRows[p.tile], out[1] = kTileCols[p.tile], out[2] = p.splits;
-  out[3] = rows == 1 ? 1 : few_rows_sizes(rows, n) ? 2 : 0;
+  out[3] = rows == 1 ? 1 : few_rows_sizes(rows, n, k, gated, esz) ? 2 : 0;
   out[4] = few_rows_two_waves(n, k, gated, static_cast<int>((rows + 15) / 16), esz);
 }
 // {few-rows kernel, together, and for dx and dw: tile rows, tile columns, splits}

@@ -119,3 +119,38 @@ def test_two_blocks_of_rows_stay_on_their_kernel(planner):
 @pytest.mark.parametrize("shape", TWO_BLOCKS, ids=lambda s: "x".join(map(str, s)))
 def test_gated_gradients_of_two_blocks_of_rows(shape):
     check_glu_backward(*shape, "bf16", "gelu", pad=8, seed=71)
+
+
+# us on one MI355X of the few-rows kernel and of the tiles, where they are apart
+TIMES = [("bf16", "linear", (16, 4096, 4096), 8.8, 13.4), ("bf16", "linear", (16, 11008, 4096), 18.7, 21.8),
+         ("bf16", "linear", (24, 4096, 11008), 20.4, 26.9), ("bf16", "linear", (24, 4096, 4096), 9.7, 13.7),
+         ("bf16", "linear", (32, 8192, 1024), 6.8, 9.1), ("bf16", "linear", (32, 5120, 8192), 28.9, 24.3),
+         ("bf16", "linear", (32, 16384, 4096), 35.5, 26.8), ("bf16", "linear", (32, 28672, 8192), 103.6, 90.3),
+         ("bf16", "linear", (30, 14176, 4096), 30.6, 25.6), ("bf16", "linear", (48, 4096, 4096), 12.1, 14.4),
+         ("bf16", "linear", (48, 8192, 1024), 7.7, 9.4), ("bf16", "linear", (48, 8192, 8192), 39.9, 33.1),
+         ("bf16", "linear", (48, 5120, 5560), 35.4, 24.0), ("bf16", "linear", (48, 11008, 4096), 32.3, 24.2),
+         ("bf16", "glu", (24, 4096, 4096), 14.2, 21.0), ("bf16", "glu", (30, 8192, 4096), 24.7, 36.9),
+         ("bf16", "glu", (32, 11008, 1024), 15.1, 13.6), ("bf16", "glu", (48, 4096, 8192), 30.0, 34.4),
+         ("bf16", "glu", (48, 2048, 7168), 22.9, 19.8), ("bf16", "glu", (48, 5120, 8192), 46.4, 39.3),
+         ("bf16", "glu", (48, 11008, 4096), 43.3, 38.7), ("fp32", "linear", (32, 11008, 4096), 48.5, 78.9),
+         ("fp32", "linear", (48, 8192, 1024), 13.9, 19.1), ("fp32", "linear", (48, 11008, 1024), 24.9, 22.9),
+         ("fp32", "glu", (32, 8192, 8192), 93.3, 164.4), ("fp32", "glu", (48, 11008, 4096), 100.6, 132.0),
+         ("fp32", "glu", (48, 28672, 2048), 126.6, 156.7)]
+
+
+def test_the_rule_for_few_rows_takes_the_faster_kernel(planner):
+    for dtype, call, shape, few, tiles in TIMES:
+        (form,) = variants(planner, call, dtype, shape, False)
+        assert (form[2] == "few rows") == (few < tiles), (dtype, call, shape, form)
+
+
+def test_the_rule_for_two_waves_takes_the_faster_one(planner):
+    """... and of the few-rows kernel with two waves a workgroup, and with more."""
+    for dtype, call, shape, two, more in [
+            ("bf16", "linear", (8, 11008, 1024), 6.6, 10.2), ("bf16", "linear", (8, 14176, 6144), 33.0, 37.3),
+            ("bf16", "linear", (8, 8192, 8192), 29.2, 25.7), ("bf16", "linear", (32, 8192, 1024), 6.8, 8.6),
+            ("bf16", "glu", (16, 28672, 2048), 40.2, 48.8), ("bf16", "glu", (16, 8192, 8192), 48.9, 45.1),
+            ("bf16", "glu", (30, 8192, 4096), 24.7, 27.3), ("fp32", "linear", (16, 14176, 2048), 23.6, 30.2),
+            ("fp32", "linear", (24, 8192, 8192), 72.9, 55.8), ("fp32", "glu", (48, 28672, 2048), 126.6, 136.6)]:
+        (form,) = variants(planner, call, dtype, shape, False)
+        assert form[2] == "few rows" and (form[4] == 2) == (two < more), (dtype, call, shape, form)

@@ -999,8 +999,8 @@ __global__ void __launch_bounds__(64 * NW) few_rows_kernel(GemmParams a) {
 }
 
 // ... and whose operands lie within the 32-bit offsets of its buffer copies.
-bool few_rows(const GemmParams& a, int gated, int esz) {
-  if (!few_rows_sizes(a.rows, a.cols)) return false;
+bool few_rows(const GemmParams& a, bool gated, int esz) {
+  if (!few_rows_sizes(a.rows, a.cols, a.depth, gated, esz)) return false;
   for (int h = 0; h < (gated ? 3 : 2); ++h)
     if ((15 * (h == 0 ? a.p : a.q[h - 1]).ld + a.depth) * esz >= (int64_t(1) << 31)) return false;
   return true;

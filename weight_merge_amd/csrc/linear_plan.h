@@ -10,11 +10,29 @@ namespace ada {
 namespace {
 
 // ---- few rows ------------------------------------------------------------------------
-// Sizes that take the few-rows kernel.  Up to 32 rows it is ahead of the tiles everywhere (24 x
-// 4096 x 11008: 22.2 against 26.9 us); with a third block of x next to W only while the
-// workgroups fit twice on the card (48 x 4096 x 4096: 11.8 against 15.0 us, 48 x 11008 x 4096:
-// 31.5 against 26.8 us).
-inline bool few_rows_sizes(int64_t rows, int64_t cols) { return rows <= 32 || (rows <= 48 && cols <= 8192); }
+// Sizes that take the few-rows kernel, timed against the tiles at 2400 pairs of columns and depths
+// (1024 to 32768 columns, 1 to 64 KB of depth), 2 to 48 rows, both types, gated and not; the rule
+// is within 4% of the faster of the two in the mean of every kind, within 13% at nine of ten.
+//   to 16 rows: it is ahead throughout, or level (8 x 4096 x 4096: 7.9 against 13.4 us, 16 x 28672
+//     x 2048: 25.2 and 25.1)
+//   17 to 32 rows: x's second block leaves room for one workgroup on a CU.  In fp32, whose matrix
+//     instructions bind the tiles, it is still ahead (32 x 11008 x 4096: 48.5 against 78.9).  In
+//     bf16 while the workgroups are one round (24 x 4096 x 4096: 9.7 against 13.7), or two with
+//     rows short enough for two waves each (32 x 8192 x 1024: 6.8 against 9.1; gated 30 x 8192 x
+//     4096: 24.7 against 36.9); not where there are more (32 x 16384 x 4096: 35.9 against 26.8;
+//     gated 32 x 11008 x 1024: 15.1 against 13.6) or two of longer rows (32 x 5120 x 5560: 32
+//     against 22)
+//   33 to 48 rows: short rows in one round or two (48 x 4096 x 4096: 12.0 against 14.4; 48 x 8192 x
+//     1024: 7.6 against 9.4; but 48 x 8192 x 8192: 40 against 33), longer ones for a gated pair
+//     whose round nearly fills the CUs (48 x 4096 x 8192: 30 against 34, but 48 x 2048 x 7168: 23
+//     against 20), fp32 pairs always (48 x 11008 x 4096: 101 against 130)
+inline bool few_rows_sizes(int64_t rows, int64_t cols, int64_t depth, bool gated, int esz) {
+  if (rows <= 16 || rows > 48) return rows <= 16;
+  if (esz == 4 && (gated || rows <= 32)) return true;
+  const int64_t bytes = depth * esz;
+  if (rows <= 32) return cols <= 4096 || (cols <= 8192 && (gated ? bytes < 16384 : bytes <= 8192));
+  return (cols <= 8192 && bytes <= 8192) || (gated && cols > 2048 && cols <= 4096 && bytes <= 16384);
+}
 
 // Into how many parts the contraction is split over workgroups: where the columns leave most CUs
 // idle and k is long (14 x 216 x 13456: 12.0 against 19.7 us; fp32 12 x 1016 x 28552: 33 against
@@ -27,10 +45,14 @@ inline int few_rows_splits(int64_t cols, int64_t depth, int esz) {
 }
 
 // Two waves a workgroup, and several workgroups on a CU, where there are more of them than CUs
-// and k is short (8 x 11008 x 1024: 6.8 against 10.5 us, 8 x 11008 x 4096: 17.5 against 20.6 us);
-// else as many waves as have room for their rings (16 x 4096 x 4096: 9.4 against 10.9 us).
+// and k is short; else as many waves as have room for their rings (16 x 4096 x 4096: 9.4 against
+// 10.9 us).  To 16 rows, and for gated pairs, two waves are ahead below 16 KB of depth (8 x 11008 x
+// 1024: 6.6 against 10.2 us, 8 x 14176 x 6144: 33 against 37, gated 16 x 28672 x 2048: 40 against
+// 49) and behind from there on (8 x 8192 x 8192: 29 against 26, gated 16 x 8192 x 8192: 49 against
+// 45); with x's second block beside one W to 8 KB (32 x 8192 x 1024: 6.8 against 8.6, fp32 24 x
+// 8192 x 8192: 73 against 56).
 inline bool few_rows_two_waves(int64_t cols, int64_t depth, bool gated, int blocks_of_rows, int esz) {
-  return cols > 256 * 16 && depth * esz <= (gated && blocks_of_rows > 1 ? 16 : 32) * 256;
+  return cols > 256 * 16 && (blocks_of_rows > 1 && !gated ? depth * esz <= 8192 : depth * esz < 16384);
 }
 
 // ---- tiles ---------------------------------------------------------------------------
@@ -140,7 +162,8 @@ inline int64_t part_bytes(const Product& p, int splits) { return splits > 1 ? sp
 // rows too far apart for it.
 inline Plan plan_forward(int64_t rows, int64_t cols, int64_t depth, int gated, int esz) {
   Plan p = plan_product({rows, gated ? 2 * cols : cols, depth, esz});
-  if (rows == 1 || few_rows_sizes(rows, cols)) p = {kTiles - 1, rows == 1 ? 1 : few_rows_splits(cols, depth, esz), 0.f};
+  if (rows == 1 || few_rows_sizes(rows, cols, depth, gated, esz))
+    p = {kTiles - 1, rows == 1 ? 1 : few_rows_splits(cols, depth, esz), 0.f};
   return p;
 }
 
