@@ -141,8 +141,8 @@ __device__ __forceinline__ float act_value(float z, int act) {
     case ADA_ACT_RELU: return z < 0.f ? 0.f : z;  // NaN stays NaN
     case ADA_ACT_SILU: return z * logistic<T>(z, e);
     case ADA_ACT_GELU: {
-      const float tail = normal_tail<T>(z, e);  // 0 far out: z - z tail is z there, infinite ones too
-      return z < 0.f ? z * tail : tail == 0.f ? z : z - z * tail;
+      const float tail = normal_tail<T>(z, e);  // 0 from 15 on, so an infinite z need not meet it
+      return z < 0.f ? z * tail : z - fminf(z, 16.f) * tail;
     }
     case ADA_ACT_GELU_TANH: return z * logistic<T>(twice_inner(z), e);
     default: return z;
