@@ -107,3 +107,34 @@ def test_inputs_dropped_behind_the_call(dtype):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, ref))
         del others
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", (20, 250))
+def test_captured_with_the_stream_given(rows):
+    """A capture whose calls name its stream, with tensors made and dropped inside it."""
+    n, k = 1000, 4104
+    x, w, u = (H.normal(i, s, 0.05, "bf16").to("cuda") for i, s in enumerate(((rows, k), (n, k), (n, k))))
+    side = torch.cuda.Stream()
+
+    def step(s):
+        h = A.ada_glu(x, w, u, stream=s)  # its workspace, and h below, go back to the pool here
+        y = A.ada_linear(h * 2, w[:, :n].contiguous(), residual=h, act="gelu", stream=s)
+        return [y, *A.ada_linear_backward(y, x, w, stream=s)[:2]]
+
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        step(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = step(side)
+    for rep in range(4):
+        x.copy_(H.normal(10 + rep, (rows, k), 0.05, "bf16"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            ref = step(side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, ref)), rep
