@@ -292,7 +292,9 @@ typedef enum {
  *     their row strides are equal.  Overlaps return ADA_EINVAL.
  *   - Sums and activations are fp32; each result is rounded to the storage type once.  The
  *     backward calls round dz (dg, du) to the storage type once more, as an operand of the
- *     matrix instructions (no effect in fp32); dbias sums the unrounded dz.
+ *     matrix instructions: in bf16 dx and dw are within about 2.35e-3 of the exact ones (2-norm),
+ *     where the rounding of the results alone leaves 1.66e-3; nothing in fp32, for callers who
+ *     are owed more.  dbias sums the unrounded dz.
  *   - `workspace`: caller-owned device memory, 16-byte aligned, of at least as many bytes as
  *     the call's _workspace function returns (0: may be NULL).  Its contents need not be
  *     set and mean nothing afterwards.  Calls that overlap in time need workspaces of

@@ -12,7 +12,7 @@ namespace {
 // ---- few rows ------------------------------------------------------------------------
 // Sizes that take the few-rows kernel, timed against the tiles at 2400 pairs of columns and depths
 // (1024 to 32768 columns, 1 to 64 KB of depth), 2 to 48 rows, both types, gated and not; the rule
-// is within 4% of the faster of the two in the mean of every kind, within 13% at nine of ten.
+// is within 4% of the faster of the two in the mean of every kind, within 15% at nine of ten.
 //   to 16 rows: it is ahead throughout, or level (8 x 4096 x 4096: 7.9 against 13.4 us, 16 x 28672
 //     x 2048: 25.2 and 25.1)
 //   17 to 32 rows: x's second block leaves room for one workgroup on a CU.  In fp32, whose matrix
@@ -168,11 +168,13 @@ inline Plan plan_forward(int64_t rows, int64_t cols, int64_t depth, int gated, i
 }
 
 // ---- backward passes -------------------------------------------------------------------
-// Sizes that take it.  Small matrices are ahead on the tiles (both gradients, tiles against this:
+// Sizes that take the few-rows gradients.  Small matrices are ahead on the tiles (both gradients, tiles against this:
 // bf16 32 x 1024 x 1024 10.9 and 11.2 us, 32 x 512 x 8192 17.8 and 14.0; fp32 32 x 1024 x 1024 13.5
 // and 14.7, 32 x 4096 x 512 19.5 and 15.0).  Two blocks of rows leave one wave on a SIMD, which
 // pays for large ones in bf16 (64 x 4096 x 4096 37.2 and 37.5, 64 x 11008 x 4096 84 and 58), and
 // not in fp32, where the matrix pipes bind (64 x 4096 x 4096 69 and 69, 48 x 4096 x 512 21.6 and 21.9).
+// At 720 more pairs of columns and depths (1 MB to 1 GB of weights, gated and not) it is within 2% of
+// the faster of the two in the mean of every kind, within 10% at nine of ten.
 inline bool few_rows_grad(int64_t rows, int64_t weight_bytes, int esz) {
   return rows <= 32 ? weight_bytes > (int64_t(4) << 20)
                     : rows <= 64 && esz == 2 && weight_bytes > (int64_t(32) << 20);
