@@ -18,8 +18,8 @@
  *   - Every tensor pointer is a DEVICE pointer unless stated otherwise, 16-byte
  *     aligned, row-major, owned by the caller.  The library never allocates or
  *     frees caller memory, and the hot calls (pregate, merge, unmerge, switch,
- *     decode_gemv, decode_gemv_layer, lora_apply, lora_layer, lora_batch, linear, glu
- *     and their backward calls) allocate nothing at all.
+ *     decode_gemv, decode_gemv_layer, lora_apply, lora_layer, lora_batch, linear, glu,
+ *     norm, dropout, route and their backward calls) allocate nothing at all.
  *   - `stream` is a hipStream_t passed as void* (NULL = the default stream).  All
  *     calls are asynchronous on that stream and return once the work is enqueued.
  *   - Return value: ADA_OK (0) or a negative ada_status.  All argument checks run
@@ -415,6 +415,185 @@ int ada_glu_backward(const ada_glu_grad_args* args, int32_t act, int32_t dtype, 
                      int64_t workspace_bytes, void* stream);
 int64_t ada_glu_backward_workspace(int64_t rows, int32_t d_out, int32_t d_in, int32_t act,
                                    int32_t dtype);
+
+/*
+ * What stands between the projections: norms, dropout, and the router's choice for many rows.
+ *   - Matrices as for the linear products: row-major, a row stride ld in elements (at least the
+ *     row's length, at most 2^36), pointers and row strides 16-byte aligned, at most 2^35
+ *     elements, 0 <= rows <= 2^22 (with rows = 0 the matrices may be NULL); columns are a
+ *     multiple of 8.  Vectors of fp32 or int32 are contiguous and 4-byte aligned.
+ *   - Statistics, sums, gates and losses are fp32 (or wider); each result is rounded to the
+ *     storage type once.  No atomics: equal calls give equal bits, and a gradient's do not depend
+ *     on which others are asked for.
+ *   - An output may not overlap an input or another output (ADA_EINVAL), but for the outputs that
+ *     may be an input itself (same pointer and row stride), named at each call.
+ */
+
+/*
+ * Dropout from a counter-based generator: no mask is stored, it is made again wherever (seed,
+ * offset) and the matrix's sizes are the same, whatever its row stride.  The generator is Philox4x32-10 with
+ * the counter (g, offset) and the key seed, 64 bits each: its four words, low half first, are the
+ * eight 16-bit numbers of elements 8 g .. 8 g + 7 in row-major order (row * d + column).  An
+ * element is kept where its number is at least t = 65536 p rounded to nearest-even, and then
+ * multiplied by 65536 / (65536 - t): p counts as the nearest multiple of 2^-16.  A dropped element
+ * is 0, also where it was infinite or NaN.  p = 1 drops everything.
+ */
+typedef struct {
+  double p;               /* 0 <= p <= 1                                                    */
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t* state;  /* NULL, or device memory (8-byte aligned) of two numbers: the seed, */
+                          /* instead of `seed`, and a start that `offset` is added to. Read    */
+                          /* when the kernel runs, so a captured graph draws anew when they    */
+                          /* are changed between replays.                                      */
+} ada_drop;
+
+typedef struct {
+  const void* x;         /* [rows][d]                                    */
+  const void* residual;  /* NULL or [rows][d]                            */
+  void* y;               /* [rows][d]; may be x or residual              */
+  int64_t ld_x;
+  int64_t ld_res;
+  int64_t ld_y;
+  int64_t rows;
+  int32_t d;
+  ada_drop drop;
+} ada_dropout_args;
+
+/* y = residual + dropout(x). */
+int ada_dropout(const ada_dropout_args* args, int32_t dtype, void* stream);
+
+typedef struct {
+  const void* dy;  /* [rows][d]                */
+  void* dx;        /* [rows][d]; may be dy     */
+  int64_t ld_dy;
+  int64_t ld_dx;
+  int64_t rows;
+  int32_t d;
+  ada_drop drop;   /* as in the forward call   */
+} ada_dropout_grad_args;
+
+/* dx = dropout(dy).  The gradient of the residual is dy. */
+int ada_dropout_backward(const ada_dropout_grad_args* args, int32_t dtype, void* stream);
+
+typedef enum { ADA_NORM_LAYER = 0, ADA_NORM_RMS = 1 } ada_norm_kind;
+
+typedef struct {
+  const void* x;         /* [rows][d]                                                   */
+  const void* residual;  /* NULL or [rows][d]                                           */
+  const void* weight;    /* NULL (ones) or [d]                                          */
+  const void* bias;      /* NULL or [d]                                                 */
+  void* y;               /* [rows][d]; may be x or residual                             */
+  void* hidden;          /* NULL or [rows][d]: h, the residual stream and what the      */
+                         /* backward pass reads; may be x or residual (not y)           */
+  float* mean;           /* NULL or [rows]; not written for ADA_NORM_RMS                */
+  float* rstd;           /* NULL or [rows]                                              */
+  int64_t ld_x;
+  int64_t ld_res;
+  int64_t ld_y;
+  int64_t ld_hidden;
+  int64_t rows;
+  int32_t d;             /* at most 32768                                               */
+  int32_t kind;          /* ada_norm_kind                                               */
+  float eps;             /* not negative                                                */
+  ada_drop drop;         /* on x, before the residual is added; p = 0: none             */
+} ada_norm_args;
+
+/*
+ * h = residual + dropout(x);  per row: mean of h, rstd = 1 / sqrt(mean of (h - mean)^2 + eps),
+ * y = (h - mean) rstd weight + bias.  ADA_NORM_RMS: the same with 0 for the mean.  The norm reads
+ * h before it is rounded to the storage type.
+ */
+int ada_norm(const ada_norm_args* args, int32_t dtype, void* stream);
+
+typedef struct {
+  const void* dy;       /* [rows][d] gradient of y                                              */
+  const void* hidden;   /* [rows][d] h (x itself where there was neither residual nor dropout)  */
+  const void* dhidden;  /* NULL or [rows][d]: the gradient that reaches h past the norm         */
+  const void* weight;   /* NULL (ones) or [d]                                                   */
+  const float* mean;    /* [rows] as ada_norm wrote them; not read for ADA_NORM_RMS             */
+  const float* rstd;    /* [rows]                                                               */
+  void* dx;             /* NULL or [rows][d]: behind the dropout; may be dy or dhidden          */
+  void* dresidual;      /* NULL or [rows][d]: gradient of h; may be dy or dhidden (not dx)      */
+  void* dweight;        /* NULL or [d]                                                          */
+  void* dbias;          /* NULL or [d]                                                          */
+  int64_t ld_dy;
+  int64_t ld_hidden;
+  int64_t ld_dhidden;
+  int64_t ld_dx;
+  int64_t ld_dresidual;
+  int64_t rows;
+  int32_t d;
+  int32_t kind;
+  ada_drop drop;        /* as in the forward call                                               */
+} ada_norm_grad_args;
+
+/*
+ * xhat = (h - mean) rstd, t = dy weight;  dresidual = dhidden + rstd (t - mean(t) - xhat mean(t xhat))
+ * (ADA_NORM_RMS: without mean(t)), dx = dropout(dresidual), dweight and dbias the sums of dy xhat
+ * and dy over rows; at least one of the four is asked for.  Without dropout dx is the residual's
+ * gradient as well.  The gradients are overwritten, not added to.
+ */
+int ada_norm_backward(const ada_norm_grad_args* args, int32_t dtype, void* workspace, int64_t workspace_bytes,
+                      void* stream);
+/* Bytes of workspace (as for the linear products); negative status on bad sizes. */
+int64_t ada_norm_backward_workspace(int64_t rows, int32_t d, int32_t dtype);
+
+typedef struct {
+  const void* logits;    /* [rows][E]: any row stride of at least E, aligned to the type only   */
+  const uint8_t* valid;  /* NULL or [rows]: 0 for rows that do not count (padding)              */
+  int32_t* idx;          /* [rows][k]                                                           */
+  float* gate;           /* [rows][k]                                                           */
+  int32_t* counts;       /* [E]: rows that picked each expert; NULL, with the next three: no balance */
+  float* prob;           /* [E]: mean probability                                               */
+  float* loss;           /* [1]                                                                 */
+  int32_t* used;         /* [1]: n, the rows that count                                         */
+  int64_t ld_logits;
+  int64_t rows;
+  int32_t E;
+  int32_t k;
+  int32_t renorm;        /* as in ada_pregate                                                   */
+} ada_route_args;
+
+/*
+ * ada_pregate's choice for many rows, from the logits of a router product (ada_linear), and what
+ * the router is trained on.  Per row: the k largest logits in descending order, equal ones lower
+ * index first, and their gates: the softmax over the picked logits (renorm = 1) or the full softmax
+ * at them (0).  A logit of -inf closes its expert to the row: it is never picked.  A row counts if
+ * its flag is not 0 and an expert is open to it; other rows, and slots for which no open expert is
+ * left, get index -1 and gate 0 (the merge skips both).  Balance: loss = E sum_e (counts_e /
+ * (k n)) prob_e, with the means over the n rows that count (1 where the load is even); 0 with n = 0.
+ * A NaN logit counts as the largest, and where a row that counts holds a NaN or +inf its gates, prob and loss are
+ * NaN; the indices stay in range.
+ */
+int ada_route(const ada_route_args* args, int32_t dtype, void* workspace, int64_t workspace_bytes, void* stream);
+/* Bytes of workspace; negative status on bad sizes. */
+int64_t ada_route_workspace(int64_t rows, int32_t E);
+
+typedef struct {
+  const void* logits;     /* [rows][E]                                                            */
+  const int32_t* idx;     /* [rows][k] as ada_route wrote it, and the next three                  */
+  const float* gate;      /* [rows][k]; read for dgate with renorm                                */
+  const int32_t* counts;  /* [E]; read for dloss                                                  */
+  const int32_t* used;    /* [1]; read for dloss                                                  */
+  const float* dgate;     /* NULL or [rows][k]: gradient of the gates                             */
+  const float* dloss;     /* NULL or [1]: gradient of the loss; at least one of the two is given  */
+  void* dlogits;          /* [rows][E]                                                            */
+  int64_t ld_logits;
+  int64_t ld_dlogits;
+  int64_t rows;
+  int32_t E;
+  int32_t k;
+  int32_t renorm;
+} ada_route_grad_args;
+
+/*
+ * With p = softmax(logits) and dp_e = dloss E counts_e / (k n^2), to which dgate is added at the
+ * picked experts without renorm: dlogits = p (dp - sum p dp), plus gate (dgate - sum gate dgate)
+ * at the picked with renorm.  The counts are constants.  Rows that did not count (idx -1 in
+ * their first slot) get zeros; an index outside [0, E) is passed over.
+ */
+int ada_route_backward(const ada_route_grad_args* args, int32_t dtype, void* stream);
 
 /* Static text for a status code (never NULL). */
 const char* ada_status_string(int status);

@@ -7,8 +7,11 @@ and streams only.
 from .api import (  # noqa: F401
     AdaError,
     AdaModel,
+    Routing,
     ada_decode_gemv,
     ada_decode_gemv_layer,
+    ada_dropout,
+    ada_dropout_backward,
     ada_glu,
     ada_glu_backward,
     ada_linear,
@@ -17,7 +20,11 @@ from .api import (  # noqa: F401
     ada_lora_batch,
     ada_lora_layer,
     ada_merge,
+    ada_norm,
+    ada_norm_backward,
     ada_pregate,
+    ada_route,
+    ada_route_backward,
     ada_switch,
     ada_unmerge,
 )

@@ -9,10 +9,12 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libadafuse.
 ADA_OK, ADA_EINVAL, ADA_ESHAPE, ADA_EDTYPE, ADA_EALIGN, ADA_EHIP, ADA_ENOMEM = 0, -1, -2, -3, -4, -5, -6
 ADA_F32, ADA_BF16 = 0, 1
 ADA_ACT_NONE, ADA_ACT_RELU, ADA_ACT_SILU, ADA_ACT_GELU, ADA_ACT_GELU_TANH = 0, 1, 2, 3, 4
+ADA_NORM_LAYER, ADA_NORM_RMS = 0, 1
 
 c_void_p = ctypes.c_void_p
 c_int32 = ctypes.c_int32
 c_int64 = ctypes.c_int64
+c_uint64 = ctypes.c_uint64
 c_float = ctypes.c_float
 
 
@@ -84,6 +86,58 @@ class AdaGluGradArgs(ctypes.Structure):
     )
 
 
+class AdaDrop(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("seed", c_uint64), ("offset", c_uint64), ("state", c_void_p)]
+
+
+class AdaDropoutArgs(ctypes.Structure):
+    _fields_ = (
+        [(n, c_void_p) for n in ("x", "residual", "y")]
+        + [(n, c_int64) for n in ("ld_x", "ld_res", "ld_y", "rows")]
+        + [("d", c_int32), ("drop", AdaDrop)]
+    )
+
+
+class AdaDropoutGradArgs(ctypes.Structure):
+    _fields_ = (
+        [(n, c_void_p) for n in ("dy", "dx")]
+        + [(n, c_int64) for n in ("ld_dy", "ld_dx", "rows")]
+        + [("d", c_int32), ("drop", AdaDrop)]
+    )
+
+
+class AdaNormArgs(ctypes.Structure):
+    _fields_ = (
+        [(n, c_void_p) for n in ("x", "residual", "weight", "bias", "y", "hidden", "mean", "rstd")]
+        + [(n, c_int64) for n in ("ld_x", "ld_res", "ld_y", "ld_hidden", "rows")]
+        + [("d", c_int32), ("kind", c_int32), ("eps", c_float), ("drop", AdaDrop)]
+    )
+
+
+class AdaNormGradArgs(ctypes.Structure):
+    _fields_ = (
+        [(n, c_void_p) for n in ("dy", "hidden", "dhidden", "weight", "mean", "rstd", "dx", "dresidual", "dweight", "dbias")]
+        + [(n, c_int64) for n in ("ld_dy", "ld_hidden", "ld_dhidden", "ld_dx", "ld_dresidual", "rows")]
+        + [("d", c_int32), ("kind", c_int32), ("drop", AdaDrop)]
+    )
+
+
+class AdaRouteArgs(ctypes.Structure):
+    _fields_ = (
+        [(n, c_void_p) for n in ("logits", "valid", "idx", "gate", "counts", "prob", "loss", "used")]
+        + [(n, c_int64) for n in ("ld_logits", "rows")]
+        + [(n, c_int32) for n in ("E", "k", "renorm")]
+    )
+
+
+class AdaRouteGradArgs(ctypes.Structure):
+    _fields_ = (
+        [(n, c_void_p) for n in ("logits", "idx", "gate", "counts", "used", "dgate", "dloss", "dlogits")]
+        + [(n, c_int64) for n in ("ld_logits", "ld_dlogits", "rows")]
+        + [(n, c_int32) for n in ("E", "k", "renorm")]
+    )
+
+
 _SIGNATURES = {
     "ada_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "ada_model_create": (ctypes.c_int, [ctypes.POINTER(AdaProj), c_int32, c_int32, c_int32, c_int32,
@@ -118,6 +172,14 @@ _SIGNATURES = {
     "ada_glu_workspace": (c_int64, [c_int64, c_int32, c_int32, c_int32]),
     "ada_glu_backward": (ctypes.c_int, [ctypes.POINTER(AdaGluGradArgs), c_int32, c_int32, c_void_p, c_int64, c_void_p]),
     "ada_glu_backward_workspace": (c_int64, [c_int64, c_int32, c_int32, c_int32, c_int32]),
+    "ada_dropout": (ctypes.c_int, [ctypes.POINTER(AdaDropoutArgs), c_int32, c_void_p]),
+    "ada_dropout_backward": (ctypes.c_int, [ctypes.POINTER(AdaDropoutGradArgs), c_int32, c_void_p]),
+    "ada_norm": (ctypes.c_int, [ctypes.POINTER(AdaNormArgs), c_int32, c_void_p]),
+    "ada_norm_backward": (ctypes.c_int, [ctypes.POINTER(AdaNormGradArgs), c_int32, c_void_p, c_int64, c_void_p]),
+    "ada_norm_backward_workspace": (c_int64, [c_int64, c_int32, c_int32]),
+    "ada_route": (ctypes.c_int, [ctypes.POINTER(AdaRouteArgs), c_int32, c_void_p, c_int64, c_void_p]),
+    "ada_route_workspace": (c_int64, [c_int64, c_int32]),
+    "ada_route_backward": (ctypes.c_int, [ctypes.POINTER(AdaRouteGradArgs), c_int32, c_void_p]),
 }
 
 _lib = None

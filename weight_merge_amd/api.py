@@ -9,12 +9,14 @@ from __future__ import annotations
 
 import ctypes
 import functools
+from typing import NamedTuple
 
 import torch
 
 from . import _lib
-from ._lib import (ADA_BF16, ADA_F32, AdaGemvProj, AdaGluArgs, AdaGluGradArgs, AdaLinearArgs, AdaLinearGradArgs,
-                   AdaLoraProj, AdaProj)
+from ._lib import (ADA_BF16, ADA_F32, AdaDrop, AdaDropoutArgs, AdaDropoutGradArgs, AdaGemvProj, AdaGluArgs,
+                   AdaGluGradArgs, AdaLinearArgs, AdaLinearGradArgs, AdaLoraProj, AdaNormArgs, AdaNormGradArgs, AdaProj,
+                   AdaRouteArgs, AdaRouteGradArgs)
 
 _DT = {torch.float32: ADA_F32, torch.bfloat16: ADA_BF16}
 
@@ -614,3 +616,278 @@ def ada_glu_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_
                           lddg, lddu, rows, d_out, d_in)
     _check(_lib.load().ada_glu_backward(args, code, dc, ws, nbytes, _raw_stream(dev)), "ada_glu_backward")
     return dx, dw_gate, dw_up, dbias_gate, dbias_up
+
+
+# ---- norms, dropout, and the router for many rows ------------------------------------
+_NORMS = {"layer": 0, "rms": 1}
+_M64 = (1 << 64) - 1
+
+
+def _kind(kind: str) -> int:
+    try:
+        return _NORMS[kind]
+    except KeyError:
+        raise ValueError(f"unknown norm {kind!r}; expected one of {', '.join(_NORMS)}") from None
+
+
+def _drop(p: float, seed, offset: int, dev: int) -> AdaDrop:
+    """The C call's dropout; a seed that is a tensor is the generator's state on the device."""
+    if not isinstance(seed, torch.Tensor):
+        return AdaDrop(p, seed & _M64, offset & _M64, None)
+    if seed.dtype is not torch.int64 or seed.shape != (2,) or seed.stride(0) != 1:
+        raise TypeError("a seed on the device must be int64 [2]: the seed and the offset's start")
+    if seed.get_device() != dev:
+        raise ValueError(f"seed is on {seed.device}, not with the other tensors")
+    return AdaDrop(p, 0, offset & _M64, seed.data_ptr())
+
+
+def _matrix(x: torch.Tensor, name: str):
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be [rows, d]")
+    return x.shape
+
+
+def ada_dropout(x: torch.Tensor, p: float, seed, offset: int = 0, residual=None, y=None, stream=None):
+    """y = residual + dropout(x) for x [rows, d]: an element is zero with probability p (to the nearest 2^-16),
+    else divided by 1 - p.  y may be x or the residual itself.
+
+    The mask is a function of (seed, offset) and the element's place, and is not stored: give the
+    backward pass the same numbers, and every call of a step an offset of its own.  `seed` may be
+    an int64 [2] tensor on the device, (seed, start of the offset): a captured call then draws
+    anew whenever that tensor changes.  `stream` as in ada_linear."""
+    if stream is not None:
+        return _on(stream, ada_dropout, x, p, seed, offset, residual, y)
+    rows, d = _matrix(x, "x")
+    dc, dt, dev = _dtype(x), x.dtype, x.get_device()
+    px, ldx = _mat(x, rows, d, dt, dev, "x")
+    pr, ldr = _mat(residual, rows, d, dt, dev, "residual")
+    if y is not None:
+        py, ldy = _mat(y, rows, d, dt, dev, "y")
+    drop = _drop(p, seed, offset, dev)
+    _current(dev)
+    if y is None:
+        y = torch.empty((rows, d), dtype=dt, device=x.device)
+        py, ldy = y.data_ptr(), d
+    args = AdaDropoutArgs(px, pr, py, ldx, ldr, ldy, rows, d, drop)
+    _check(_lib.load().ada_dropout(args, dc, _raw_stream(dev)), "ada_dropout")
+    return y
+
+
+def ada_dropout_backward(dy: torch.Tensor, p: float, seed, offset: int = 0, dx=None, stream=None):
+    """dx of ada_dropout with the same p, seed and offset (dx may be dy itself); the gradient of
+    the residual is dy."""
+    if stream is not None:
+        return _on(stream, ada_dropout_backward, dy, p, seed, offset, dx)
+    rows, d = _matrix(dy, "dy")
+    dc, dt, dev = _dtype(dy), dy.dtype, dy.get_device()
+    pdy, lddy = _mat(dy, rows, d, dt, dev, "dy")
+    if dx is not None:
+        pdx, lddx = _mat(dx, rows, d, dt, dev, "dx")
+    drop = _drop(p, seed, offset, dev)
+    _current(dev)
+    if dx is None:
+        dx = torch.empty((rows, d), dtype=dt, device=dy.device)
+        pdx, lddx = dx.data_ptr(), d
+    args = AdaDropoutGradArgs(pdy, pdx, lddy, lddx, rows, d, drop)
+    _check(_lib.load().ada_dropout_backward(args, dc, _raw_stream(dev)), "ada_dropout_backward")
+    return dx
+
+
+def ada_norm(x: torch.Tensor, weight=None, bias=None, residual=None, kind: str = "layer", eps: float = 1e-5,
+             p: float = 0.0, seed=0, offset: int = 0, y=None, hidden=None, stats=None, stream=None):
+    """y = (h - mean) rstd weight + bias over each row of h = residual + dropout(x), for x [rows, d]
+    with d at most 32768; kind "rms" has no mean.  rstd = 1 / sqrt(mean of (h - mean)^2 + eps).
+
+    `hidden` receives h, the new residual stream; `stats` is a pair (mean, rstd) of fp32 [rows]
+    vectors to receive them (either may be None), both for the backward pass.  y and hidden may be
+    x or the residual itself.  p, seed and offset as in ada_dropout, `stream` as in ada_linear."""
+    if stream is not None:
+        return _on(stream, ada_norm, x, weight, bias, residual, kind, eps, p, seed, offset, y, hidden, stats)
+    rows, d = _matrix(x, "x")
+    code, dc, dt, dev = _kind(kind), _dtype(x), x.dtype, x.get_device()
+    px, ldx = _mat(x, rows, d, dt, dev, "x")
+    pr, ldr = _mat(residual, rows, d, dt, dev, "residual")
+    pw = _vec(weight, d, dt, dev, "weight")
+    pb = _vec(bias, d, dt, dev, "bias")
+    ph, ldh = _mat(hidden, rows, d, dt, dev, "hidden")
+    mean, rstd = stats if stats is not None else (None, None)
+    pm = _vec(mean, rows, torch.float32, dev, "mean")
+    ps = _vec(rstd, rows, torch.float32, dev, "rstd")
+    if y is not None:
+        py, ldy = _mat(y, rows, d, dt, dev, "y")
+    drop = _drop(p, seed, offset, dev)
+    _current(dev)
+    if y is None:
+        y = torch.empty((rows, d), dtype=dt, device=x.device)
+        py, ldy = y.data_ptr(), d
+    args = AdaNormArgs(px, pr, pw, pb, py, ph, pm, ps, ldx, ldr, ldy, ldh, rows, d, code, eps, drop)
+    _check(_lib.load().ada_norm(args, dc, _raw_stream(dev)), "ada_norm")
+    return y
+
+
+def norm_backward_workspace_bytes(rows: int, d: int, dtype: torch.dtype) -> int:
+    """Bytes of workspace ada_norm_backward needs at these sizes."""
+    return _workspace_bytes("ada_norm_backward_workspace", rows, d, _DT[dtype])
+
+
+def ada_norm_backward(dy: torch.Tensor, hidden: torch.Tensor, stats, weight=None, dhidden=None, kind: str = "layer",
+                      p: float = 0.0, seed=0, offset: int = 0, dx=None, dresidual=None, dweight=None, dbias=None,
+                      want_dx: bool = True, want_dresidual: bool = False, want_dweight: bool = True,
+                      want_dbias: bool = False, workspace=None, stream=None):
+    """(dx, dresidual, dweight, dbias) of ada_norm, given h and (mean, rstd) as it saved them (h is x
+    where there was neither residual nor dropout) and `dhidden`, the gradient that reaches h past
+    the norm; None for what is neither passed nor wanted.
+
+    dresidual is the gradient of h, dx that behind the dropout: without dropout dx is both.  dx and
+    dresidual may be dy or dhidden itself."""
+    if stream is not None:
+        return _on(stream, ada_norm_backward, dy, hidden, stats, weight, dhidden, kind, p, seed, offset, dx, dresidual,
+                   dweight, dbias, want_dx, want_dresidual, want_dweight, want_dbias, workspace)
+    rows, d = _matrix(dy, "dy")
+    code, dc, dt, dev = _kind(kind), _dtype(dy), dy.dtype, dy.get_device()
+    mean, rstd = stats
+    if rstd is None or (mean is None and code == 0):
+        raise ValueError("stats must hold what ada_norm saved: rstd, and mean unless the norm is rms")
+    pdy, lddy = _mat(dy, rows, d, dt, dev, "dy")
+    ph, ldh = _mat(hidden, rows, d, dt, dev, "hidden")
+    pdh, lddh = _mat(dhidden, rows, d, dt, dev, "dhidden")
+    pw = _vec(weight, d, dt, dev, "weight")
+    pm = _vec(mean, rows, torch.float32, dev, "mean")
+    ps = _vec(rstd, rows, torch.float32, dev, "rstd")
+    pdx, lddx = _mat(dx, rows, d, dt, dev, "dx")
+    pdr, lddr = _mat(dresidual, rows, d, dt, dev, "dresidual")
+    pdw = _vec(dweight, d, dt, dev, "dweight")
+    pdb = _vec(dbias, d, dt, dev, "dbias")
+    drop = _drop(p, seed, offset, dev)
+    _current(dev)
+    if dx is None and want_dx:
+        dx = torch.empty((rows, d), dtype=dt, device=dy.device)
+        pdx, lddx = dx.data_ptr(), d
+    if dresidual is None and want_dresidual:
+        dresidual = torch.empty((rows, d), dtype=dt, device=dy.device)
+        pdr, lddr = dresidual.data_ptr(), d
+    if dweight is None and want_dweight:
+        dweight = torch.empty(d, dtype=dt, device=dy.device)
+        pdw = dweight.data_ptr()
+    if dbias is None and want_dbias:
+        dbias = torch.empty(d, dtype=dt, device=dy.device)
+        pdb = dbias.data_ptr()
+    ws, nbytes, _keep = _workspace(_workspace_bytes("ada_norm_backward_workspace", rows, d, dc), workspace, dev)
+    args = AdaNormGradArgs(pdy, ph, pdh, pw, pm, ps, pdx, pdr, pdw, pdb, lddy, ldh, lddh, lddx, lddr, rows, d, code,
+                           drop)
+    _check(_lib.load().ada_norm_backward(args, dc, ws, nbytes, _raw_stream(dev)), "ada_norm_backward")
+    return dx, dresidual, dweight, dbias
+
+
+class Routing(NamedTuple):
+    """What ada_route writes.  The last four are None where no balance was asked for."""
+
+    idx: torch.Tensor      # int32 [rows, k], -1 where nothing was picked
+    gate: torch.Tensor     # fp32 [rows, k]
+    counts: torch.Tensor   # int32 [E]: rows that picked each expert
+    prob: torch.Tensor     # fp32 [E]: mean probability of each
+    loss: torch.Tensor     # fp32 [1]: the balance loss
+    used: torch.Tensor     # int32 [1]: the rows that count
+
+
+def _logits(t: torch.Tensor, rows: int, E: int, dt, dev: int, name: str):
+    """Pointer and row stride of [rows, E] logits, which may begin anywhere."""
+    p, ld = _mat(t, rows, E, dt, dev, name)
+    return p, max(ld, E)
+
+
+def _table(t: torch.Tensor, shape, dt, dev: int, name: str):
+    """Pointer of a contiguous table."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype is not dt or t.get_device() != dev:
+        _refuse(t, shape, dt, dev, name)
+    _contig(t, name)
+    return t.data_ptr()
+
+
+def route_workspace_bytes(rows: int, E: int) -> int:
+    """Bytes of workspace ada_route needs at these sizes (none without a balance)."""
+    return _workspace_bytes("ada_route_workspace", rows, E)
+
+
+def ada_route(logits: torch.Tensor, k: int, renorm: bool = True, valid=None, balance: bool = True, out=None,
+              workspace=None, stream=None) -> Routing:
+    """ada_pregate's choice for every row of logits [rows, E], and the balance the router is
+    trained on: how many rows picked each expert, the mean probability of each, and
+    loss = E sum_e (counts_e / (k n)) prob_e over the n rows that count.
+
+    A logit of -inf closes its expert to the row.  `valid` (bool or uint8 [rows]) marks the rows that
+    count; the others, rows with every expert closed, and slots without an open expert left get
+    index -1 and gate 0.  `out` is a Routing (or six tensors) to write to; `stream` as in ada_linear."""
+    if stream is not None:
+        return _on(stream, ada_route, logits, k, renorm, valid, balance, out, workspace)
+    rows, E = _matrix(logits, "logits")
+    dc, dev = _dtype(logits), logits.get_device()
+    pl, ld = _logits(logits, rows, E, logits.dtype, dev, "logits")
+    pv = None
+    if valid is not None:
+        if valid.dtype not in (torch.bool, torch.uint8):
+            raise TypeError(f"valid must be bool or uint8, got {valid.dtype}")
+        pv = _vec(valid, rows, valid.dtype, dev, "valid")
+    i32, f32 = torch.int32, torch.float32
+    if out is None:
+        _current(dev)
+        one = logits.device
+        out = Routing(torch.empty((rows, k), dtype=i32, device=one), torch.empty((rows, k), dtype=f32, device=one),
+                      *((torch.empty(E, dtype=i32, device=one), torch.empty(E, dtype=f32, device=one),
+                         torch.empty(1, dtype=f32, device=one), torch.empty(1, dtype=i32, device=one))
+                        if balance else (None,) * 4))
+    else:
+        out = Routing(*out)
+    pi = _table(out.idx, (rows, k), i32, dev, "idx")
+    pg = _table(out.gate, (rows, k), f32, dev, "gate")
+    pc = pp = po = pu = None
+    if balance:
+        pc = _vec(out.counts, E, i32, dev, "counts")
+        pp = _vec(out.prob, E, f32, dev, "prob")
+        po = _vec(out.loss, 1, f32, dev, "loss")
+        pu = _vec(out.used, 1, i32, dev, "used")
+    _current(dev)
+    ws, nbytes, _keep = _workspace(_workspace_bytes("ada_route_workspace", rows, E) if balance else 0, workspace, dev)
+    args = AdaRouteArgs(pl, pv, pi, pg, pc, pp, po, pu, ld, rows, E, k, bool(renorm))
+    _check(_lib.load().ada_route(args, dc, ws, nbytes, _raw_stream(dev)), "ada_route")
+    return out
+
+
+def ada_route_backward(logits: torch.Tensor, out, dgate=None, dloss=None, renorm: bool = True, dlogits=None,
+                       stream=None):
+    """dlogits of ada_route, given its logits and what it wrote: `dgate` (fp32 [rows, k]) is the
+    gradient of the gates, `dloss` (fp32 [1]) that of the loss; either may be None.  The counts
+    are constants."""
+    if stream is not None:
+        return _on(stream, ada_route_backward, logits, out, dgate, dloss, renorm, dlogits)
+    rows, E = _matrix(logits, "logits")
+    dc, dt, dev = _dtype(logits), logits.dtype, logits.get_device()
+    idx, gate, counts, _, _, used = out
+    i32, f32 = torch.int32, torch.float32
+    if idx.dim() != 2:
+        raise ValueError("idx must be [rows, k]")
+    k = idx.shape[1]
+    if dgate is None and dloss is None:
+        raise ValueError("dgate or dloss is needed")
+    pl, ld = _logits(logits, rows, E, dt, dev, "logits")
+    pi = _table(idx, (rows, k), i32, dev, "idx")
+    pg = _table(gate, (rows, k), f32, dev, "gate")
+    pdg = _table(dgate, (rows, k), f32, dev, "dgate")
+    pc = pu = pdl = None
+    if dloss is not None:
+        if counts is None or used is None:
+            raise ValueError("the loss was not computed: ada_route was called without balance")
+        pc = _vec(counts, E, i32, dev, "counts")
+        pu = _vec(used, 1, i32, dev, "used")
+        pdl = _vec(dloss, 1, f32, dev, "dloss")
+    if dlogits is not None:
+        po, ldo = _logits(dlogits, rows, E, dt, dev, "dlogits")
+    _current(dev)
+    if dlogits is None:
+        dlogits = torch.empty((rows, E), dtype=dt, device=logits.device)
+        po, ldo = dlogits.data_ptr(), E
+    args = AdaRouteGradArgs(pl, pi, pg, pc, pu, pdg, pdl, po, ld, ldo, rows, E, k, bool(renorm))
+    _check(_lib.load().ada_route_backward(args, dc, _raw_stream(dev)), "ada_route_backward")
+    return dlogits

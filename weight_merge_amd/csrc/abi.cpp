@@ -6,11 +6,15 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
+#include <initializer_list>
 #include <new>
+#include <utility>
 #include <vector>
 
 #include "launch.h"
+#include "layer.h"
 #include "linear.h"
 
 #ifndef ADA_LONG_TILE_GROUP
@@ -257,6 +261,60 @@ int check_workspace(const void* ws, int64_t have, int64_t need, const MatArg* m,
   for (int i = 0; i < n; ++i)
     if (overlaps(w, m[i], esz)) return ADA_EINVAL;
   return ADA_OK;
+}
+
+// ---- argument checks of the norms, dropout and the router -----------------------------
+// Arguments of several element sizes are compared in bytes: a MatArg with its columns and row
+// stride in bytes.
+MatArg bytes_of(const void* p, int64_t rows, int64_t cols, int64_t ld, int esz, bool out) {
+  return MatArg{p, cols == 0 ? 0 : rows, cols * esz, ld * esz, out};
+}
+MatArg bytes_of(const void* p, int64_t n, int esz, bool out) { return bytes_of(p, 1, n, n, esz, out); }
+
+int check_matrix(const void* p, int64_t cols, int64_t ld, int esz) {
+  if (p == nullptr) return ADA_OK;
+  if (!aligned16(p)) return ADA_EALIGN;
+  if (ld < cols || ld > kMaxLd) return ADA_ESHAPE;
+  return (ld * esz) % 16 == 0 ? ADA_OK : ADA_EALIGN;
+}
+
+// Whether an output overlaps any other argument; the pairs in `same` may be one matrix.
+bool bytes_overlap(const MatArg* m, int n, std::initializer_list<std::pair<int, int>> same) {
+  for (int i = 0; i < n; ++i)
+    for (int j = i + 1; j < n; ++j) {
+      if (!m[i].out && !m[j].out) continue;
+      bool one = false;
+      for (const auto& q : same) one = one || (q.first == i && q.second == j);
+      if (one && m[i].p == m[j].p && m[i].ld == m[j].ld) continue;
+      if (overlaps(m[i], m[j], 1)) return true;
+    }
+  return false;
+}
+
+int check_layer_sizes(int64_t rows, int32_t d, int32_t most, int32_t dtype) {
+  if (!dtype_ok(dtype)) return ADA_EDTYPE;
+  if (rows < 0 || rows > kMaxDim || !dim_ok(d) || d > most || rows * d > kMaxMat) return ADA_ESHAPE;
+  return ADA_OK;
+}
+
+int check_drop(const ada_drop& q, ada::DropParams& d) {
+  if (!(q.p >= 0.0 && q.p <= 1.0)) return ADA_EINVAL;
+  if ((reinterpret_cast<uintptr_t>(q.state) & 7u) != 0) return ADA_EALIGN;
+  d.least = static_cast<uint32_t>(std::nearbyint(65536.0 * q.p));
+  d.scale = d.least < 65536u ? 65536.f / static_cast<float>(65536u - d.least) : 0.f;
+  d.seed = q.seed;
+  d.offset = q.offset;
+  d.state = q.state;
+  return ADA_OK;
+}
+
+int check_route_sizes(int64_t rows, int32_t E) {
+  return rows < 0 || rows > kMaxDim || E < 1 || E > ada::kMaxExperts ? ADA_ESHAPE : ADA_OK;
+}
+
+int check_logits(const void* p, int32_t E, int64_t ld, int esz) {
+  if (reinterpret_cast<uintptr_t>(p) % esz != 0) return ADA_EALIGN;
+  return p != nullptr && (ld < E || ld > kMaxLd) ? ADA_ESHAPE : ADA_OK;
 }
 
 }  // namespace
@@ -751,6 +809,225 @@ int ada_glu_backward(const ada_glu_grad_args* q, int32_t act, int32_t dtype, voi
   p.act = act;
   p.gated = 1;
   const hipError_t e = ada::launch_linear_grad(p, dtype, workspace, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? ADA_OK : ADA_EHIP;
+}
+
+int ada_dropout(const ada_dropout_args* q, int32_t dtype, void* stream) {
+  if (q == nullptr) return ADA_EINVAL;
+  if (int st = check_layer_sizes(q->rows, q->d, kMaxDim, dtype); st != ADA_OK) return st;
+  if (q->rows > 0 && (q->x == nullptr || q->y == nullptr)) return ADA_EINVAL;
+  const int esz = dtype == ADA_BF16 ? 2 : 4;
+  ada::DropoutParams p{};
+  if (int st = check_drop(q->drop, p.drop); st != ADA_OK) return st;
+  if (int st = check_matrix(q->x, q->d, q->ld_x, esz); st != ADA_OK) return st;
+  if (int st = check_matrix(q->residual, q->d, q->ld_res, esz); st != ADA_OK) return st;
+  if (int st = check_matrix(q->y, q->d, q->ld_y, esz); st != ADA_OK) return st;
+  const MatArg m[] = {bytes_of(q->x, q->rows, q->d, q->ld_x, esz, false),
+                      bytes_of(q->residual, q->rows, q->d, q->ld_res, esz, false),
+                      bytes_of(q->y, q->rows, q->d, q->ld_y, esz, true), bytes_of(q->drop.state, 2, 8, false)};
+  if (bytes_overlap(m, 4, {{0, 2}, {1, 2}})) return ADA_EINVAL;
+  p.x = {q->x, q->ld_x};
+  p.res = {q->residual, q->ld_res};
+  p.y = {q->y, q->ld_y};
+  p.rows = q->rows;
+  p.d = q->d;
+  const hipError_t e = ada::launch_dropout(p, dtype, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? ADA_OK : ADA_EHIP;
+}
+
+int ada_dropout_backward(const ada_dropout_grad_args* q, int32_t dtype, void* stream) {
+  if (q == nullptr) return ADA_EINVAL;
+  const ada_dropout_args f{q->dy, nullptr, q->dx, q->ld_dy, 0, q->ld_dx, q->rows, q->d, q->drop};
+  return ada_dropout(&f, dtype, stream);
+}
+
+int ada_norm(const ada_norm_args* q, int32_t dtype, void* stream) {
+  if (q == nullptr || (q->kind != ADA_NORM_LAYER && q->kind != ADA_NORM_RMS) || !(q->eps >= 0.f)) return ADA_EINVAL;
+  if (int st = check_layer_sizes(q->rows, q->d, ada::kMaxNorm, dtype); st != ADA_OK) return st;
+  if (q->rows > 0 && (q->x == nullptr || q->y == nullptr)) return ADA_EINVAL;
+  const int esz = dtype == ADA_BF16 ? 2 : 4;
+  const int64_t rows = q->rows, d = q->d;
+  ada::NormParams p{};
+  if (int st = check_drop(q->drop, p.drop); st != ADA_OK) return st;
+  float* mean = q->kind == ADA_NORM_RMS ? nullptr : q->mean;
+  if (!aligned4(mean) || !aligned4(q->rstd) || !aligned16(q->weight) || !aligned16(q->bias)) return ADA_EALIGN;
+  if (int st = check_matrix(q->x, d, q->ld_x, esz); st != ADA_OK) return st;
+  if (int st = check_matrix(q->residual, d, q->ld_res, esz); st != ADA_OK) return st;
+  if (int st = check_matrix(q->y, d, q->ld_y, esz); st != ADA_OK) return st;
+  if (int st = check_matrix(q->hidden, d, q->ld_hidden, esz); st != ADA_OK) return st;
+  const MatArg m[] = {bytes_of(q->x, rows, d, q->ld_x, esz, false),
+                      bytes_of(q->residual, rows, d, q->ld_res, esz, false),
+                      bytes_of(q->y, rows, d, q->ld_y, esz, true),
+                      bytes_of(q->hidden, rows, d, q->ld_hidden, esz, true),
+                      bytes_of(q->weight, d, esz, false),
+                      bytes_of(q->bias, d, esz, false),
+                      bytes_of(mean, rows, 4, true),
+                      bytes_of(q->rstd, rows, 4, true),
+                      bytes_of(q->drop.state, 2, 8, false)};
+  if (bytes_overlap(m, 9, {{0, 2}, {1, 2}, {0, 3}, {1, 3}})) return ADA_EINVAL;
+  p.x = {q->x, q->ld_x};
+  p.res = {q->residual, q->ld_res};
+  p.w = q->weight;
+  p.b = q->bias;
+  p.y = {q->y, q->ld_y};
+  p.hidden = {q->hidden, q->ld_hidden};
+  p.mean = mean;
+  p.rstd = q->rstd;
+  p.rows = rows;
+  p.d = q->d;
+  p.rms = q->kind == ADA_NORM_RMS;
+  p.eps = q->eps;
+  const hipError_t e = ada::launch_norm(p, dtype, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? ADA_OK : ADA_EHIP;
+}
+
+int64_t ada_norm_backward_workspace(int64_t rows, int32_t d, int32_t dtype) {
+  if (int st = check_layer_sizes(rows, d, ada::kMaxNorm, dtype); st != ADA_OK) return st;
+  return ada::norm_grad_workspace(rows, d, dtype);
+}
+
+int ada_norm_backward(const ada_norm_grad_args* q, int32_t dtype, void* workspace, int64_t workspace_bytes,
+                      void* stream) {
+  if (q == nullptr || (q->kind != ADA_NORM_LAYER && q->kind != ADA_NORM_RMS)) return ADA_EINVAL;
+  if (int st = check_layer_sizes(q->rows, q->d, ada::kMaxNorm, dtype); st != ADA_OK) return st;
+  const int64_t rows = q->rows, d = q->d;
+  const float* mean = q->kind == ADA_NORM_RMS ? nullptr : q->mean;
+  if (rows > 0 && (q->dy == nullptr || q->hidden == nullptr || q->rstd == nullptr ||
+                   (q->kind == ADA_NORM_LAYER && mean == nullptr) ||
+                   (q->dx == nullptr && q->dresidual == nullptr && q->dweight == nullptr && q->dbias == nullptr)))
+    return ADA_EINVAL;
+  const int esz = dtype == ADA_BF16 ? 2 : 4;
+  ada::NormGradParams p{};
+  if (int st = check_drop(q->drop, p.drop); st != ADA_OK) return st;
+  if (!aligned4(mean) || !aligned4(q->rstd) || !aligned16(q->weight) || !aligned16(q->dweight) ||
+      !aligned16(q->dbias))
+    return ADA_EALIGN;
+  if (int st = check_matrix(q->dy, d, q->ld_dy, esz); st != ADA_OK) return st;
+  if (int st = check_matrix(q->hidden, d, q->ld_hidden, esz); st != ADA_OK) return st;
+  if (int st = check_matrix(q->dhidden, d, q->ld_dhidden, esz); st != ADA_OK) return st;
+  if (int st = check_matrix(q->dx, d, q->ld_dx, esz); st != ADA_OK) return st;
+  if (int st = check_matrix(q->dresidual, d, q->ld_dresidual, esz); st != ADA_OK) return st;
+  const MatArg m[] = {bytes_of(q->dy, rows, d, q->ld_dy, esz, false),
+                      bytes_of(q->dhidden, rows, d, q->ld_dhidden, esz, false),
+                      bytes_of(q->dx, rows, d, q->ld_dx, esz, true),
+                      bytes_of(q->dresidual, rows, d, q->ld_dresidual, esz, true),
+                      bytes_of(q->hidden, rows, d, q->ld_hidden, esz, false),
+                      bytes_of(q->weight, d, esz, false),
+                      bytes_of(mean, rows, 4, false),
+                      bytes_of(q->rstd, rows, 4, false),
+                      bytes_of(q->dweight, d, esz, true),
+                      bytes_of(q->dbias, d, esz, true),
+                      bytes_of(q->drop.state, 2, 8, false)};
+  if (bytes_overlap(m, 11, {{0, 2}, {1, 2}, {0, 3}, {1, 3}})) return ADA_EINVAL;
+  const int64_t need = ada::norm_grad_workspace(rows, q->d, dtype);
+  if (int st = check_workspace(workspace, workspace_bytes, need, m, 11, 1); st != ADA_OK) return st;
+  p.dy = {q->dy, q->ld_dy};
+  p.hidden = {q->hidden, q->ld_hidden};
+  p.dhidden = {q->dhidden, q->ld_dhidden};
+  p.w = q->weight;
+  p.mean = mean;
+  p.rstd = q->rstd;
+  p.dx = {q->dx, q->ld_dx};
+  p.dres = {q->dresidual, q->ld_dresidual};
+  p.dw = q->dweight;
+  p.db = q->dbias;
+  p.rows = rows;
+  p.d = q->d;
+  const hipError_t e = ada::launch_norm_grad(p, dtype, workspace, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? ADA_OK : ADA_EHIP;
+}
+
+int64_t ada_route_workspace(int64_t rows, int32_t E) {
+  if (int st = check_route_sizes(rows, E); st != ADA_OK) return st;
+  return ada::route_workspace(rows, E);
+}
+
+int ada_route(const ada_route_args* q, int32_t dtype, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (q == nullptr || (q->renorm != 0 && q->renorm != 1)) return ADA_EINVAL;
+  if (!dtype_ok(dtype)) return ADA_EDTYPE;
+  if (int st = check_route_sizes(q->rows, q->E); st != ADA_OK) return st;
+  if (q->k < 1 || q->k > q->E) return ADA_ESHAPE;
+  if (q->rows > 0 && (q->logits == nullptr || q->idx == nullptr || q->gate == nullptr)) return ADA_EINVAL;
+  const bool balance = q->counts != nullptr;
+  if (balance != (q->prob != nullptr) || balance != (q->loss != nullptr) || balance != (q->used != nullptr))
+    return ADA_EINVAL;
+  const int esz = dtype == ADA_BF16 ? 2 : 4;
+  if (int st = check_logits(q->logits, q->E, q->ld_logits, esz); st != ADA_OK) return st;
+  if (!aligned4(q->idx) || !aligned4(q->gate) || !aligned4(q->counts) || !aligned4(q->prob) || !aligned4(q->loss) ||
+      !aligned4(q->used))
+    return ADA_EALIGN;
+  const int64_t picks = q->rows * q->k;
+  const MatArg m[] = {bytes_of(q->logits, q->rows, q->E, q->ld_logits, esz, false),
+                      bytes_of(q->valid, q->rows, 1, false),
+                      bytes_of(q->idx, picks, 4, true),
+                      bytes_of(q->gate, picks, 4, true),
+                      bytes_of(q->counts, q->E, 4, true),
+                      bytes_of(q->prob, q->E, 4, true),
+                      bytes_of(q->loss, 1, 4, true),
+                      bytes_of(q->used, 1, 4, true)};
+  if (bytes_overlap(m, 8, {})) return ADA_EINVAL;
+  const int64_t need = balance ? ada::route_workspace(q->rows, q->E) : 0;
+  if (int st = check_workspace(workspace, workspace_bytes, need, m, 8, 1); st != ADA_OK) return st;
+  ada::RouteParams p{};
+  p.logits = {q->logits, q->ld_logits};
+  p.valid = q->valid;
+  p.idx = q->idx;
+  p.gate = q->gate;
+  p.counts = q->counts;
+  p.prob = q->prob;
+  p.loss = q->loss;
+  p.used = q->used;
+  p.rows = q->rows;
+  p.E = q->E;
+  p.k = q->k;
+  p.renorm = q->renorm;
+  const hipError_t e = ada::launch_route(p, dtype, workspace, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? ADA_OK : ADA_EHIP;
+}
+
+int ada_route_backward(const ada_route_grad_args* q, int32_t dtype, void* stream) {
+  if (q == nullptr || (q->renorm != 0 && q->renorm != 1)) return ADA_EINVAL;
+  if (!dtype_ok(dtype)) return ADA_EDTYPE;
+  if (int st = check_route_sizes(q->rows, q->E); st != ADA_OK) return st;
+  if (q->k < 1 || q->k > q->E) return ADA_ESHAPE;
+  const float* gate = q->dgate != nullptr && q->renorm == 1 ? q->gate : nullptr;
+  const int32_t* counts = q->dloss != nullptr ? q->counts : nullptr;
+  const int32_t* used = q->dloss != nullptr ? q->used : nullptr;
+  if (q->rows > 0 && (q->logits == nullptr || q->idx == nullptr || q->dlogits == nullptr ||
+                      (q->dgate == nullptr && q->dloss == nullptr) ||
+                      (q->dgate != nullptr && q->renorm == 1 && gate == nullptr) ||
+                      (q->dloss != nullptr && (counts == nullptr || used == nullptr))))
+    return ADA_EINVAL;
+  const int esz = dtype == ADA_BF16 ? 2 : 4;
+  if (int st = check_logits(q->logits, q->E, q->ld_logits, esz); st != ADA_OK) return st;
+  if (int st = check_logits(q->dlogits, q->E, q->ld_dlogits, esz); st != ADA_OK) return st;
+  if (!aligned4(q->idx) || !aligned4(gate) || !aligned4(counts) || !aligned4(used) || !aligned4(q->dgate) ||
+      !aligned4(q->dloss))
+    return ADA_EALIGN;
+  const int64_t picks = q->rows * q->k;
+  const MatArg m[] = {bytes_of(q->logits, q->rows, q->E, q->ld_logits, esz, false),
+                      bytes_of(q->idx, picks, 4, false),
+                      bytes_of(gate, picks, 4, false),
+                      bytes_of(counts, q->E, 4, false),
+                      bytes_of(used, 1, 4, false),
+                      bytes_of(q->dgate, picks, 4, false),
+                      bytes_of(q->dloss, 1, 4, false),
+                      bytes_of(q->dlogits, q->rows, q->E, q->ld_dlogits, esz, true)};
+  if (bytes_overlap(m, 8, {})) return ADA_EINVAL;
+  ada::RouteGradParams p{};
+  p.logits = {q->logits, q->ld_logits};
+  p.idx = q->idx;
+  p.gate = gate;
+  p.counts = counts;
+  p.used = used;
+  p.dgate = q->dgate;
+  p.dloss = q->dloss;
+  p.dlogits = {q->dlogits, q->ld_dlogits};
+  p.rows = q->rows;
+  p.E = q->E;
+  p.k = q->k;
+  p.renorm = q->renorm;
+  const hipError_t e = ada::launch_route_grad(p, dtype, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? ADA_OK : ADA_EHIP;
 }
 

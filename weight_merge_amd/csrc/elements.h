@@ -1,0 +1,138 @@
+// Device code shared by the norms, dropout and the router: eight consecutive elements as one
+// unit of work, the counter-based generator, and sums over lanes.
+#pragma once
+
+#include "layer.h"
+
+namespace ada {
+namespace {
+
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+
+// ---- eight consecutive elements, 16-byte aligned ---------------------------------------
+template <typename T>
+struct Eight {
+  u32x4 v[sizeof(T) / 2];  // bf16: one vector, fp32: two
+};
+
+template <typename T>
+__device__ __forceinline__ Eight<T> load_eight(const T* p) {
+  Eight<T> e;
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(T) / 2; ++i) e.v[i] = reinterpret_cast<const u32x4*>(p)[i];
+  return e;
+}
+
+template <typename T>
+__device__ __forceinline__ void zero_eight(Eight<T>& e) {
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(T) / 2; ++i) e.v[i] = u32x4{0, 0, 0, 0};
+}
+
+__device__ __forceinline__ void unpack(const Eight<float>& e, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(e.v[i >> 2][i & 3]);
+}
+__device__ __forceinline__ void unpack(const Eight<uint16_t>& e, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(e.v[0][i] << 16);
+    f[2 * i + 1] = __uint_as_float(e.v[0][i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ Eight<float> pack(const float (&f)[8], float) {
+  Eight<float> e;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e.v[i >> 2][i & 3] = __float_as_uint(f[i]);
+  return e;
+}
+__device__ __forceinline__ Eight<uint16_t> pack(const float (&f)[8], uint16_t) {  // to nearest-even
+  Eight<uint16_t> e;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = __builtin_bit_cast(uint16_t, static_cast<__bf16>(f[2 * i]));
+    const uint32_t hi = __builtin_bit_cast(uint16_t, static_cast<__bf16>(f[2 * i + 1]));
+    e.v[0][i] = lo | hi << 16;
+  }
+  return e;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_eight(T* p, const float (&f)[8]) {
+  const Eight<T> e = pack(f, T());
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(T) / 2; ++i) reinterpret_cast<u32x4*>(p)[i] = e.v[i];
+}
+
+// ---- dropout ---------------------------------------------------------------------------
+// Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3",
+// 2011).  Counter (g, 0, offset), key = seed: the four words are the eight 16-bit numbers of
+// elements 8 g .. 8 g + 7, low half first.  16 bits an element rather than 32 halve the
+// generator's products, which would otherwise bound the pass (20 of 32 x 32 bits at a quarter
+// of the rate of other instructions for every block of eight instead of four elements); p is
+// then a multiple of 2^-16 and the scale is exactly that multiple's.
+struct DropKey {
+  uint32_t k0, k1, o0, o1;
+};
+__device__ __forceinline__ DropKey drop_key(const DropParams& d) {
+  uint64_t seed = d.seed, offset = d.offset;
+  if (d.state != nullptr) {
+    seed = d.state[0];
+    offset += d.state[1];
+  }
+  return {uint32_t(seed), uint32_t(seed >> 32), uint32_t(offset), uint32_t(offset >> 32)};
+}
+
+__device__ __forceinline__ u32x4 philox(uint32_t g, const DropKey& key) {
+  uint32_t c0 = g, c1 = 0, c2 = key.o0, c3 = key.o1, k0 = key.k0, k1 = key.k1;
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint64_t a = uint64_t(c0) * 0xD2511F53u, b = uint64_t(c2) * 0xCD9E8D57u;
+    c0 = uint32_t(b >> 32) ^ c1 ^ k0;
+    c1 = uint32_t(b);
+    c2 = uint32_t(a >> 32) ^ c3 ^ k1;
+    c3 = uint32_t(a);
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return u32x4{c0, c1, c2, c3};
+}
+
+// Block g of eight elements: kept ones times the scale, dropped ones zero whatever they were.
+__device__ __forceinline__ void drop_eight(float (&f)[8], uint32_t g, const DropKey& key, uint32_t least,
+                                           float scale) {
+  const u32x4 w = philox(g, key);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = (w[i] & 0xffffu) >= least ? f[2 * i] * scale : 0.f;
+    f[2 * i + 1] = (w[i] >> 16) >= least ? f[2 * i + 1] * scale : 0.f;
+  }
+}
+
+// ---- sums over lanes -------------------------------------------------------------------
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_or_zero(float v) {
+  return __uint_as_float(__builtin_amdgcn_update_dpp(0, int(__float_as_uint(v)), CTRL, ROWS, 0xf, true));
+}
+
+// Sum over the wave's 64 lanes, on every lane: within rows of 16 lanes by shifts, then each
+// row's last lane into the next row and the half's into the other half (DPP: no LDS traffic).
+__device__ __forceinline__ float wave_total(float v) {
+  v += dpp_or_zero<0x111, 0xf>(v);  // row_shr:1
+  v += dpp_or_zero<0x112, 0xf>(v);  // row_shr:2
+  v += dpp_or_zero<0x114, 0xf>(v);  // row_shr:4
+  v += dpp_or_zero<0x118, 0xf>(v);  // row_shr:8
+  v += dpp_or_zero<0x142, 0xa>(v);  // row_bcast:15 into rows 1 and 3
+  v += dpp_or_zero<0x143, 0xc>(v);  // row_bcast:31 into rows 2 and 3
+  return __uint_as_float(__builtin_amdgcn_readlane(int(__float_as_uint(v)), 63));
+}
+
+// Sum over groups of `lanes` lanes (a power of two up to 32), on each of them.
+__device__ __forceinline__ float group_total(float v, int lanes) {
+  for (int m = 1; m < lanes; m <<= 1) v += __shfl_xor(v, m, 64);
+  return v;
+}
+
+}  // namespace
+}  // namespace ada
