@@ -250,6 +250,10 @@ def test_python_refusals():
         A.ada_dropout(x, 0.1, torch.zeros(2))
     with pytest.raises(TypeError, match="seed on the device"):
         A.ada_dropout(x, 0.1, torch.zeros(3, dtype=torch.int64))
+    with pytest.raises(ValueError, match="needs a seed"):
+        A.ada_norm(x, w, p=0.1)
+    with pytest.raises(ValueError, match="needs a seed"):
+        A.ada_dropout(x, float("nan"), None)
     with pytest.raises(ValueError, match="stats must hold"):
         A.ada_norm_backward(x, x, (None, torch.zeros(4)), w)
     z, out = torch.zeros(4, 6), (torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2), None, None, None, None)

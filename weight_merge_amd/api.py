@@ -621,6 +621,7 @@ def ada_glu_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_
 # ---- norms, dropout, and the router for many rows ------------------------------------
 _NORMS = {"layer": 0, "rms": 1}
 _M64 = (1 << 64) - 1
+_NO_DROP = AdaDrop()  # p = 0
 
 
 def _kind(kind: str) -> int:
@@ -632,6 +633,10 @@ def _kind(kind: str) -> int:
 
 def _drop(p: float, seed, offset: int, dev: int) -> AdaDrop:
     """The C call's dropout; a seed that is a tensor is the generator's state on the device."""
+    if seed is None:
+        if p != 0:
+            raise ValueError("dropout needs a seed")
+        return _NO_DROP
     if not isinstance(seed, torch.Tensor):
         return AdaDrop(p, seed & _M64, offset & _M64, None)
     if seed.dtype is not torch.int64 or seed.shape != (2,) or seed.stride(0) != 1:
@@ -694,7 +699,7 @@ def ada_dropout_backward(dy: torch.Tensor, p: float, seed, offset: int = 0, dx=N
 
 
 def ada_norm(x: torch.Tensor, weight=None, bias=None, residual=None, kind: str = "layer", eps: float = 1e-5,
-             p: float = 0.0, seed=0, offset: int = 0, y=None, hidden=None, stats=None, stream=None):
+             p: float = 0.0, seed=None, offset: int = 0, y=None, hidden=None, stats=None, stream=None):
     """y = (h - mean) rstd weight + bias over each row of h = residual + dropout(x), for x [rows, d]
     with d at most 32768; kind "rms" has no mean.  rstd = 1 / sqrt(mean of (h - mean)^2 + eps).
 
@@ -731,7 +736,7 @@ def norm_backward_workspace_bytes(rows: int, d: int, dtype: torch.dtype) -> int:
 
 
 def ada_norm_backward(dy: torch.Tensor, hidden: torch.Tensor, stats, weight=None, dhidden=None, kind: str = "layer",
-                      p: float = 0.0, seed=0, offset: int = 0, dx=None, dresidual=None, dweight=None, dbias=None,
+                      p: float = 0.0, seed=None, offset: int = 0, dx=None, dresidual=None, dweight=None, dbias=None,
                       want_dx: bool = True, want_dresidual: bool = False, want_dweight: bool = True,
                       want_dbias: bool = False, workspace=None, stream=None):
     """(dx, dresidual, dweight, dbias) of ada_norm, given h and (mean, rstd) as it saved them (h is x

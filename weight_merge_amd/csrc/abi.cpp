@@ -883,7 +883,7 @@ int ada_norm(const ada_norm_args* q, int32_t dtype, void* stream) {
 
 int64_t ada_norm_backward_workspace(int64_t rows, int32_t d, int32_t dtype) {
   if (int st = check_layer_sizes(rows, d, ada::kMaxNorm, dtype); st != ADA_OK) return st;
-  return ada::norm_grad_workspace(rows, d, dtype);
+  return ada::norm_grad_workspace(rows, d);
 }
 
 int ada_norm_backward(const ada_norm_grad_args* q, int32_t dtype, void* workspace, int64_t workspace_bytes,
@@ -919,7 +919,7 @@ int ada_norm_backward(const ada_norm_grad_args* q, int32_t dtype, void* workspac
                       bytes_of(q->dbias, d, esz, true),
                       bytes_of(q->drop.state, 2, 8, false)};
   if (bytes_overlap(m, 11, {{0, 2}, {1, 2}, {0, 3}, {1, 3}})) return ADA_EINVAL;
-  const int64_t need = ada::norm_grad_workspace(rows, q->d, dtype);
+  const int64_t need = ada::norm_grad_workspace(rows, q->d);
   if (int st = check_workspace(workspace, workspace_bytes, need, m, 11, 1); st != ADA_OK) return st;
   p.dy = {q->dy, q->ld_dy};
   p.hidden = {q->hidden, q->ld_hidden};

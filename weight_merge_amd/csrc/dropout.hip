@@ -42,8 +42,8 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(DropoutParams p, uint
   for (int u = 0; u < kBlocks; ++u) {
     const uint64_t g = g0 + u * kThreads;
     if (g >= blocks) continue;
-    in[u] = load_eight(x + block_at<DENSE>(g, per_row, inv, p.x.ld));
-    if constexpr (RES) add[u] = load_eight(res + block_at<DENSE>(g, per_row, inv, p.res.ld));
+    in[u] = load_eight<true>(x + block_at<DENSE>(g, per_row, inv, p.x.ld));
+    if constexpr (RES) add[u] = load_eight<true>(res + block_at<DENSE>(g, per_row, inv, p.res.ld));
   }
 #pragma unroll
   for (int u = 0; u < kBlocks; ++u) {
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(DropoutParams p, uint
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] += r[i];
     }
-    store_eight(y + block_at<DENSE>(g, per_row, inv, p.y.ld), f);
+    store_eight<true>(y + block_at<DENSE>(g, per_row, inv, p.y.ld), f);
   }
 }
 

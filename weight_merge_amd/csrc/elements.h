@@ -8,6 +8,7 @@ namespace ada {
 namespace {
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // ---- eight consecutive elements, 16-byte aligned ---------------------------------------
 template <typename T>
@@ -15,11 +16,20 @@ struct Eight {
   u32x4 v[sizeof(T) / 2];  // bf16: one vector, fp32: two
 };
 
-template <typename T>
+// STREAM: past the caches' ordinary policy, for matrices that are touched once.  Only in bf16, where
+// a wave's vectors cover whole lines: in fp32 a lane's two vectors are one instruction each, and
+// either fills half of every line it touches.
+template <bool STREAM = false, typename T>
 __device__ __forceinline__ Eight<T> load_eight(const T* p) {
   Eight<T> e;
 #pragma unroll
-  for (unsigned i = 0; i < sizeof(T) / 2; ++i) e.v[i] = reinterpret_cast<const u32x4*>(p)[i];
+  for (unsigned i = 0; i < sizeof(T) / 2; ++i) {
+    const u32x4* v = reinterpret_cast<const u32x4*>(p) + i;
+    if constexpr (STREAM && sizeof(T) == 2)
+      e.v[i] = __builtin_nontemporal_load(v);
+    else
+      e.v[i] = *v;
+  }
   return e;
 }
 
@@ -58,11 +68,17 @@ __device__ __forceinline__ Eight<uint16_t> pack(const float (&f)[8], uint16_t) {
   return e;
 }
 
-template <typename T>
+template <bool STREAM = false, typename T>
 __device__ __forceinline__ void store_eight(T* p, const float (&f)[8]) {
   const Eight<T> e = pack(f, T());
 #pragma unroll
-  for (unsigned i = 0; i < sizeof(T) / 2; ++i) reinterpret_cast<u32x4*>(p)[i] = e.v[i];
+  for (unsigned i = 0; i < sizeof(T) / 2; ++i) {
+    u32x4* v = reinterpret_cast<u32x4*>(p) + i;
+    if constexpr (STREAM && sizeof(T) == 2)
+      __builtin_nontemporal_store(e.v[i], v);
+    else
+      *v = e.v[i];
+  }
 }
 
 // ---- dropout ---------------------------------------------------------------------------
@@ -84,14 +100,19 @@ __device__ __forceinline__ DropKey drop_key(const DropParams& d) {
   return {uint32_t(seed), uint32_t(seed >> 32), uint32_t(offset), uint32_t(offset >> 32)};
 }
 
+// One instruction; the compiler makes two of it where a key is uniform.
+__device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) {
+  return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96);
+}
+
 __device__ __forceinline__ u32x4 philox(uint32_t g, const DropKey& key) {
   uint32_t c0 = g, c1 = 0, c2 = key.o0, c3 = key.o1, k0 = key.k0, k1 = key.k1;
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
     const uint64_t a = uint64_t(c0) * 0xD2511F53u, b = uint64_t(c2) * 0xCD9E8D57u;
-    c0 = uint32_t(b >> 32) ^ c1 ^ k0;
+    c0 = xor3(uint32_t(b >> 32), c1, k0);
     c1 = uint32_t(b);
-    c2 = uint32_t(a >> 32) ^ c3 ^ k1;
+    c2 = xor3(uint32_t(a >> 32), c3, k1);
     c3 = uint32_t(a);
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;
@@ -126,6 +147,15 @@ __device__ __forceinline__ float wave_total(float v) {
   v += dpp_or_zero<0x142, 0xa>(v);  // row_bcast:15 into rows 1 and 3
   v += dpp_or_zero<0x143, 0xc>(v);  // row_bcast:31 into rows 2 and 3
   return __uint_as_float(__builtin_amdgcn_readlane(int(__float_as_uint(v)), 63));
+}
+
+// Sum over 16 neighbouring lanes that hold the same in every row of 16, on every lane.
+__device__ __forceinline__ float row16_total(float v) {
+  v += dpp_or_zero<0x111, 0xf>(v);
+  v += dpp_or_zero<0x112, 0xf>(v);
+  v += dpp_or_zero<0x114, 0xf>(v);
+  v += dpp_or_zero<0x118, 0xf>(v);
+  return __uint_as_float(__builtin_amdgcn_readlane(int(__float_as_uint(v)), 15));
 }
 
 // Sum over groups of `lanes` lanes (a power of two up to 32), on each of them.

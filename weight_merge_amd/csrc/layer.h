@@ -66,7 +66,7 @@ struct NormGradParams {
   int32_t d;
   DropParams drop;
 };
-int64_t norm_grad_workspace(int64_t rows, int32_t d, int dtype);
+int64_t norm_grad_workspace(int64_t rows, int32_t d);
 hipError_t launch_norm_grad(const NormGradParams& p, int dtype, void* ws, hipStream_t s);
 
 struct RouteParams {

@@ -15,6 +15,8 @@ namespace ada {
 namespace {
 
 constexpr int kMaxWaves = 16;
+constexpr int kGradThreads = 1024;  // of a workgroup of norm_grad_kernel, about
+constexpr int kGradBlocks = 256;    // one a CU: twice as many write and join twice the partial sums
 
 // Lanes that share a row: `lanes` below 64 is a power of two, otherwise a multiple of 64.
 struct RowShape {
@@ -36,18 +38,15 @@ __device__ __forceinline__ void row_totals(float (&v)[N], int lanes, float (*slo
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = wave_total(v[i]);
   if constexpr (WIDE) {
-    const int wave = threadIdx.x >> 6, per_row = lanes >> 6, first = wave / per_row * per_row;
+    // at most 16 waves: their sums come back on 16 lanes, which add up as a row of lanes does
+    const int wave = threadIdx.x >> 6, waves = lanes >> 6, first = wave / waves * waves, from = threadIdx.x & 15;
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
       for (int i = 0; i < N; ++i) slot[wave][i] = v[i];
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = 0.f;
-    for (int w = 0; w < per_row; ++w) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] += slot[first + w][i];
-    }
+    for (int i = 0; i < N; ++i) v[i] = row16_total(from < waves ? slot[first + from][i] : 0.f);
   }
 }
 
@@ -56,6 +55,26 @@ __device__ __forceinline__ void row_totals(float (&v)[N], int lanes, float (*slo
 // first sum's mean, and that sum's rounding is taken out of both with the mean of h - m
 // (Chan, Golub, LeVeque, "Algorithms for computing the sample variance", 1983), so rows far from
 // zero keep their accuracy.  y and hidden may be x or the residual: a lane reads what it writes.
+template <typename T, int CH>
+struct NormRow {
+  Eight<T> x[CH], res[CH];
+
+  __device__ __forceinline__ void load(const NormParams& p, int64_t row, int lane, int lanes, int per_row) {
+    const T* px = static_cast<const T*>(p.x.p) + row * p.x.ld;
+    const T* pr = static_cast<const T*>(p.res.p) + row * p.res.ld;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int g = lane + c * lanes;
+      zero_eight(x[c]);
+      zero_eight(res[c]);
+      if (row < p.rows && g < per_row) {
+        x[c] = load_eight<true>(px + g * 8);
+        if (p.res.p != nullptr) res[c] = load_eight<true>(pr + g * 8);
+      }
+    }
+  }
+};
+
 template <typename T, int CH, bool SUB, bool WIDE, bool DROP>
 __global__ void __launch_bounds__(1024) norm_kernel(NormParams p, int lanes) {
   __shared__ float mean_slot[kMaxWaves][1];
@@ -68,37 +87,27 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p, int lanes) {
   DropKey key{};
   if constexpr (DROP) key = drop_key(p.drop);
 
-  for (int64_t row0 = int64_t(blockIdx.x) * groups; row0 < p.rows; row0 += int64_t(gridDim.x) * groups) {
-    const bool live = row0 + group < p.rows;
-    const int64_t row = live ? row0 + group : p.rows - 1;
-    const T* x = static_cast<const T*>(p.x.p) + row * p.x.ld;
-    const T* res = static_cast<const T*>(p.res.p) + row * p.res.ld;
+  NormRow<T, CH> now;
+  const int64_t step = int64_t(gridDim.x) * groups;
+  int64_t row = int64_t(blockIdx.x) * groups + group;
+  now.load(p, row, lane, lanes, per_row);
+  for (int64_t row0 = row - group; row0 < p.rows; row0 += step, row += step) {
     T* y = static_cast<T*>(p.y.p) + row * p.y.ld;
     T* hidden = static_cast<T*>(p.hidden.p) + row * p.hidden.ld;
-    Eight<T> in[CH], add[CH];
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int g = lane + c * lanes;
-      zero_eight(in[c]);
-      zero_eight(add[c]);
-      if (g < per_row) {
-        in[c] = load_eight(x + g * 8);
-        if (p.res.p != nullptr) add[c] = load_eight(res + g * 8);
-      }
-    }
     float h[CH][8], sum[1] = {0.f};
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      float r[8];
-      unpack(in[c], h[c]);
+      unpack(now.x[c], h[c]);
       if constexpr (DROP)
         drop_eight(h[c], uint32_t(row * per_row + lane + c * lanes), key, p.drop.least, p.drop.scale);
-      unpack(add[c], r);
+      if (p.res.p != nullptr) {
+        float r[8];
+        unpack(now.res[c], r);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (p.res.p != nullptr) h[c][i] += r[i];
-        sum[0] += h[c][i];
+        for (int i = 0; i < 8; ++i) h[c][i] += r[i];
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[0] += h[c][i];
     }
     float mean = 0.f, rest = 0.f;
     if (!p.rms) {
@@ -125,203 +134,314 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p, int lanes) {
       square = square < 0.f ? 0.f : square;  // NaN stays
     }
     const float rstd = 1.f / sqrtf(square + p.eps);
-    if (live) {
+    if (row < p.rows) {
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int g = lane + c * lanes;
         if (g >= per_row) continue;
-        if (p.hidden.p != nullptr) store_eight(hidden + g * 8, h[c]);
-        float wv[8], bv[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          wv[i] = 1.f;
-          bv[i] = 0.f;
-        }
-        if (w != nullptr) unpack(load_eight(w + g * 8), wv);
-        if (b != nullptr) unpack(load_eight(b + g * 8), bv);
+        if (p.hidden.p != nullptr) store_eight<true>(hidden + g * 8, h[c]);
         float out[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) out[i] = fmaf((h[c][i] - mean - rest) * rstd, wv[i], bv[i]);
-        store_eight(y + g * 8, out);
+        for (int i = 0; i < 8; ++i) out[i] = (h[c][i] - mean - rest) * rstd;
+        if (w != nullptr) {
+          float v[8];
+          unpack(load_eight(w + g * 8), v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) out[i] *= v[i];
+        }
+        if (b != nullptr) {
+          float v[8];
+          unpack(load_eight(b + g * 8), v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) out[i] += v[i];
+        }
+        store_eight<true>(y + g * 8, out);
       }
       if (lane == 0) {
         if (p.mean != nullptr) p.mean[row] = mean + rest;
         if (p.rstd != nullptr) p.rstd[row] = rstd;
       }
     }
+    now.load(p, row + step, lane, lanes, per_row);
   }
 }
 
 // ---- backward --------------------------------------------------------------------------
-// A workgroup takes every gridDim.x-th set of rows, keeps dw and db of a lane's columns in
-// registers over all of them, and writes them once: part[0][block][d] and part[1][block][d], which
-// norm_join_kernel sums in a fixed order.  The next row's loads are in flight while this one is
-// summed where registers allow it (CH sizeof(T) <= 4); rows of more than 16384 fp32 elements are
-// read again behind their sums instead of being held.  dx and dres may be dy or dhidden.
+// Eight columns of a row's operands.
+template <typename T>
+struct GradBlock {
+  Eight<T> dy, h, add;
+
+  __device__ __forceinline__ void load(const NormGradParams& p, int64_t row, int g, bool live) {
+    zero_eight(dy);
+    zero_eight(h);
+    zero_eight(add);
+    if (!live) return;
+    dy = load_eight<true>(static_cast<const T*>(p.dy.p) + row * p.dy.ld + g * 8);
+    h = load_eight<true>(static_cast<const T*>(p.hidden.p) + row * p.hidden.ld + g * 8);
+    if (p.dhidden.p != nullptr)
+      add = load_eight<true>(static_cast<const T*>(p.dhidden.p) + row * p.dhidden.ld + g * 8);
+  }
+};
+
+// A lane's part of a row; a row past the end adds zeros.
 template <typename T, int CH>
 struct GradRow {
-  Eight<T> dy[CH], h[CH], add[CH];
+  GradBlock<T> c[CH];
   float mean, rstd;
 
   __device__ __forceinline__ void load(const NormGradParams& p, int64_t row, int lane, int lanes, int per_row) {
     const bool live = row < p.rows;
-    const T* pdy = static_cast<const T*>(p.dy.p) + row * p.dy.ld;
-    const T* ph = static_cast<const T*>(p.hidden.p) + row * p.hidden.ld;
-    const T* pd = static_cast<const T*>(p.dhidden.p) + row * p.dhidden.ld;
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int g = lane + c * lanes;
-      zero_eight(dy[c]);
-      zero_eight(h[c]);
-      zero_eight(add[c]);
-      if (live && g < per_row) {
-        dy[c] = load_eight(pdy + g * 8);
-        h[c] = load_eight(ph + g * 8);
-        if (p.dhidden.p != nullptr) add[c] = load_eight(pd + g * 8);
-      }
-    }
+    for (int i = 0; i < CH; ++i) c[i].load(p, row, lane + i * lanes, live && lane + i * lanes < per_row);
     mean = live && p.mean != nullptr ? p.mean[row] : 0.f;
-    rstd = live ? p.rstd[row] : 0.f;  // a row past the end adds zeros
+    rstd = live ? p.rstd[row] : 0.f;
+  }
+
+  // The eight values of dh from block i, given the means of t and of t xhat.
+  __device__ __forceinline__ void gradient(int i, const float (&w)[8], float c1, float c2, float (&dh)[8]) const {
+    float dy[8], add[8];
+    unpack(c[i].dy, dy);
+    unpack(c[i].h, dh);
+    unpack(c[i].add, add);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float xhat = (dh[e] - mean) * rstd;
+      dh[e] = fmaf(rstd, dy[e] * w[e] - c1 - xhat * c2, add[e]);
+    }
   }
 };
 
-template <typename T, int CH, bool SUB, bool WIDE, bool DROP>
+// What a row's gradient goes to; dx and dres may be dy or dhidden: a lane has read what it writes.
+template <typename T, bool DROP>
+__device__ __forceinline__ void store_gradient(const NormGradParams& p, int64_t row, int g, const DropKey& key,
+                                               float (&dh)[8]) {
+  if (p.dres.p != nullptr) store_eight<true>(static_cast<T*>(p.dres.p) + row * p.dres.ld + g * 8, dh);
+  if (p.dx.p == nullptr) return;
+  if constexpr (DROP) drop_eight(dh, uint32_t(row * (p.d >> 3) + g), key, p.drop.least, p.drop.scale);
+  store_eight<true>(static_cast<T*>(p.dx.p) + row * p.dx.ld + g * 8, dh);
+}
+
+template <typename T>
+__device__ __forceinline__ void load_weight(const void* w, int g, bool live, float (&f)[8]) {
+  if (w != nullptr && live) {
+    unpack(load_eight(static_cast<const T*>(w) + g * 8), f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = 1.f;
+  }
+}
+
+// Rows and columns in one pass, for many rows of up to 8192 columns.  A workgroup takes every
+// gridDim.x-th set of rows, keeps the sums dw and db of a lane's eight columns in registers over all
+// of them, and writes them once: part[0][block][d] and part[1][block][d], which norm_join_kernel
+// adds up in a fixed order.  The next row's loads are in flight while this one is summed.
+template <typename T, bool SUB, bool WIDE, bool DROP>
 __global__ void __launch_bounds__(1024) norm_grad_kernel(NormGradParams p, int lanes, float* part) {
-  constexpr bool AHEAD = CH * sizeof(T) <= 4, AGAIN = CH * sizeof(T) > 8;
   __shared__ float slot[2][kMaxWaves][2];
-  extern __shared__ float meet[];  // [threads][8] where several groups of a workgroup meet
+  __shared__ f32x4 meet[2 * kGradThreads];  // where the groups of a workgroup meet
   const int group = threadIdx.x / lanes, lane = threadIdx.x - group * lanes, groups = blockDim.x / lanes;
   const int per_row = p.d >> 3;
   const float over = 1.f / float(p.d);
+  const bool inside = lane < per_row;
   DropKey key{};
   if constexpr (DROP) key = drop_key(p.drop);
+  float dw[8] = {}, db[8] = {};
+  Eight<T> weight;  // unpacked anew for each row: held as floats the loads ahead waited for it
+  zero_eight(weight);
+  if (p.w != nullptr && inside) weight = load_eight(static_cast<const T*>(p.w) + lane * 8);
 
-  Eight<T> wraw[CH];
+  const auto take = [&](const GradRow<T, 1>& now, int64_t row, float (*totals)[2]) {
+    float sums[2] = {0.f, 0.f}, dy[8], h[8], w[8];
+    unpack(weight, w);
+    if (p.w == nullptr) {
 #pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    zero_eight(wraw[c]);
-    if (p.w != nullptr && lane + c * lanes < per_row)
-      wraw[c] = load_eight(static_cast<const T*>(p.w) + (lane + c * lanes) * 8);
-  }
-  float dw[CH][8], db[CH][8];
+      for (int i = 0; i < 8; ++i) w[i] = 1.f;
+    }
+    unpack(now.c[0].dy, dy);
+    unpack(now.c[0].h, h);
 #pragma unroll
-  for (int c = 0; c < CH; ++c)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) dw[c][i] = db[c][i] = 0.f;
-
-  GradRow<T, CH> now, next;
+    for (int i = 0; i < 8; ++i) {
+      const float t = dy[i] * w[i], xhat = (h[i] - now.mean) * now.rstd;
+      sums[0] += t;
+      sums[1] = fmaf(t, xhat, sums[1]);
+      dw[i] = fmaf(dy[i], xhat, dw[i]);
+      db[i] += dy[i];
+    }
+    row_totals<2, SUB, WIDE>(sums, lanes, totals);
+    if (row < p.rows && inside) {
+      now.gradient(0, w, p.mean != nullptr ? sums[0] * over : 0.f, sums[1] * over, h);
+      store_gradient<T, DROP>(p, row, lane, key, h);
+    }
+  };
+  GradRow<T, 1> now, next;
   const int64_t step = int64_t(gridDim.x) * groups;
   int64_t row = int64_t(blockIdx.x) * groups + group;
   now.load(p, row, lane, lanes, per_row);
   int turn = 0;
   for (int64_t row0 = row - group; row0 < p.rows; row0 += step, row += step, turn ^= 1) {
-    if constexpr (AHEAD) next.load(p, row + step, lane, lanes, per_row);
-    float sums[2] = {0.f, 0.f};
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      float dy[8], h[8], w[8];
-      unpack(now.dy[c], dy);
-      unpack(now.h[c], h);
-      unpack(wraw[c], w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float t = p.w != nullptr ? dy[i] * w[i] : dy[i], xhat = (h[i] - now.mean) * now.rstd;
-        sums[0] += t;
-        sums[1] = fmaf(t, xhat, sums[1]);
-        dw[c][i] = fmaf(dy[i], xhat, dw[c][i]);
-        db[c][i] += dy[i];
-      }
-    }
-    row_totals<2, SUB, WIDE>(sums, lanes, slot[turn]);
-    const float c1 = p.mean != nullptr ? sums[0] * over : 0.f, c2 = sums[1] * over;
-    if (row < p.rows && (p.dx.p != nullptr || p.dres.p != nullptr)) {
-      T* dx = static_cast<T*>(p.dx.p) + row * p.dx.ld;
-      T* dres = static_cast<T*>(p.dres.p) + row * p.dres.ld;
-      if constexpr (AGAIN) {
-        asm volatile("" ::: "memory");
-        now.load(p, row, lane, lanes, per_row);
-      }
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int g = lane + c * lanes;
-        if (g >= per_row) continue;
-        float dy[8], h[8], w[8], add[8];
-        unpack(now.dy[c], dy);
-        unpack(now.h[c], h);
-        unpack(wraw[c], w);
-        unpack(now.add[c], add);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float t = p.w != nullptr ? dy[i] * w[i] : dy[i], xhat = (h[i] - now.mean) * now.rstd;
-          h[i] = fmaf(now.rstd, t - c1 - xhat * c2, add[i]);
-        }
-        if (p.dres.p != nullptr) store_eight(dres + g * 8, h);
-        if (p.dx.p != nullptr) {
-          if constexpr (DROP) drop_eight(h, uint32_t(row * per_row + g), key, p.drop.least, p.drop.scale);
-          store_eight(dx + g * 8, h);
-        }
-      }
-    }
-    if constexpr (AHEAD)
-      now = next;
-    else
-      now.load(p, row + step, lane, lanes, per_row);
+    next.load(p, row + step, lane, lanes, per_row);
+    take(now, row, slot[turn]);
+    now = next;
   }
 
-  // the groups' sums meet in LDS, a block of eight columns at a time, and go to part
   for (int which = 0; which < 2; ++which) {
     if ((which == 0 ? p.dw : p.db) == nullptr) continue;
-    float* to = part + (int64_t(which) * gridDim.x + blockIdx.x) * p.d;
+    float v[8];
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      float v[8];
+    for (int i = 0; i < 8; ++i) v[i] = which == 0 ? dw[i] : db[i];
+    if (groups > 1) {
+      __syncthreads();
+      meet[threadIdx.x] = f32x4{v[0], v[1], v[2], v[3]};
+      meet[blockDim.x + threadIdx.x] = f32x4{v[4], v[5], v[6], v[7]};
+      __syncthreads();
+      if (group == 0) {
+        for (int q = 1; q < groups; ++q) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = which == 0 ? dw[c][i] : db[c][i];
-      if (groups > 1) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) meet[i * blockDim.x + threadIdx.x] = v[i];
-        __syncthreads();
-        if (group == 0) {
-          for (int q = 1; q < groups; ++q)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += meet[i * blockDim.x + q * lanes + lane];
+          for (int i = 0; i < 8; ++i) v[i] += meet[(i >> 2) * blockDim.x + q * lanes + lane][i & 3];
         }
       }
-      const int g = lane + c * lanes;
-      if (group == 0 && g < per_row) store_eight(to + g * 8, v);
     }
+    if (group == 0 && inside) store_eight(part + (int64_t(which) * gridDim.x + blockIdx.x) * p.d + lane * 8, v);
   }
 }
 
-// dw (blockIdx.y = 0) and db (1) from `parts` rows of d sums each: 64 columns a workgroup, four a
-// lane, the rows dealt to 16 sets of lanes whose sums meet in LDS.
-constexpr int kJoinSets = 16;
+// Rows and columns apart, in one grid: dw and db need no sums over a row, since mean and rstd are
+// given.  The first `stripes` workgroups sum 64 columns each over all rows, eight columns a lane, the
+// rows dealt to sets of eight lanes; the others take a set of rows each.  dy and h are read twice,
+// but there are no partial sums to write and join, so few rows need one launch; and a row is only
+// held until it is summed, so wide ones fit the registers.
+constexpr int kStripe = 64;
+template <typename T, int CH, bool SUB, bool WIDE, bool DROP>
+__global__ void __launch_bounds__(1024) norm_apart_kernel(NormGradParams p, int lanes, int stripes) {
+  const int per_row = p.d >> 3;
+  if (int(blockIdx.x) < stripes) {
+    __shared__ f32x4 meet[kMaxWaves][8][4];
+    const int quad = threadIdx.x & 7, sets = blockDim.x >> 3, g = blockIdx.x * 8 + quad;
+    const bool inside = g < per_row;
+    const T* dyp = static_cast<const T*>(p.dy.p) + g * 8;
+    const T* hp = static_cast<const T*>(p.hidden.p) + g * 8;
+    f32x4 sum[4] = {};  // dw, dw, db, db
+    constexpr int U = 4;
+    for (int64_t row0 = threadIdx.x >> 3; row0 < p.rows; row0 += int64_t(sets) * U) {
+      Eight<T> a[U], b[U];
+      float mean[U], rstd[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t row = row0 + int64_t(u) * sets;
+        zero_eight(a[u]);
+        zero_eight(b[u]);
+        mean[u] = rstd[u] = 0.f;
+        if (row < p.rows && inside) {
+          a[u] = load_eight(dyp + row * p.dy.ld);
+          b[u] = load_eight(hp + row * p.hidden.ld);
+          if (p.mean != nullptr) mean[u] = p.mean[row];
+          rstd[u] = p.rstd[row];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float dy[8], h[8];
+        unpack(a[u], dy);
+        unpack(b[u], h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          sum[i >> 2][i & 3] = fmaf(dy[i], (h[i] - mean[u]) * rstd[u], sum[i >> 2][i & 3]);
+          sum[2 + (i >> 2)][i & 3] += dy[i];
+        }
+      }
+    }
+    // the eight sets of a wave, then the waves
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        for (int m = 8; m < 64; m <<= 1) sum[j][e] += __shfl_xor(sum[j][e], m, 64);
+      }
+      if ((threadIdx.x & 63) < 8) meet[threadIdx.x >> 6][quad][j] = sum[j];
+    }
+    __syncthreads();
+    if (threadIdx.x < 8 && inside) {
+      for (unsigned v = 1; v < blockDim.x >> 6; ++v) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[j] += meet[v][quad][j];
+      }
+      float f[8];
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = sum[2 * which + (i >> 2)][i & 3];
+        T* to = static_cast<T*>(which == 0 ? p.dw : p.db);
+        if (to != nullptr) store_eight(to + g * 8, f);
+      }
+    }
+    return;
+  }
+  __shared__ float slot[kMaxWaves][2];
+  const int group = threadIdx.x / lanes, lane = threadIdx.x - group * lanes, groups = blockDim.x / lanes;
+  const float over = 1.f / float(p.d);
+  DropKey key{};
+  if constexpr (DROP) key = drop_key(p.drop);
+  const int64_t row = int64_t(blockIdx.x - stripes) * groups + group;
+  GradRow<T, CH> now;
+  now.load(p, row, lane, lanes, per_row);
+  float sums[2] = {0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int g = lane + c * lanes;
+    float dy[8], h[8], w[8];
+    unpack(now.c[c].dy, dy);
+    unpack(now.c[c].h, h);
+    load_weight<T>(p.w, g, g < per_row, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float t = dy[i] * w[i];
+      sums[0] += t;
+      sums[1] = fmaf(t, (h[i] - now.mean) * now.rstd, sums[1]);
+    }
+  }
+  row_totals<2, SUB, WIDE>(sums, lanes, slot);
+  if (row >= p.rows) return;
+  const float c1 = p.mean != nullptr ? sums[0] * over : 0.f, c2 = sums[1] * over;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int g = lane + c * lanes;
+    if (g >= per_row) continue;
+    float w[8], dh[8];
+    load_weight<T>(p.w, g, true, w);
+    now.gradient(c, w, c1, c2, dh);
+    store_gradient<T, DROP>(p, row, g, key, dh);
+  }
+}
+
+// dw (blockIdx.y = 0) and db (1) from `parts` (at most kGradBlocks) rows of d sums each: 32 columns a
+// workgroup (one line of each row), four a lane, the rows dealt to 32 sets of lanes, all of a lane's
+// loads in flight at once; the sets meet in LDS.
+constexpr int kJoinSets = 32;
 template <typename T>
 __global__ void __launch_bounds__(256) norm_join_kernel(const float* part, int parts, int d, T* dw, T* db) {
-  __shared__ float meet[kJoinSets][64];
+  constexpr int EACH = (kGradBlocks + kJoinSets - 1) / kJoinSets;
+  __shared__ f32x4 meet[kJoinSets][8];
   T* out = blockIdx.y == 0 ? dw : db;
   if (out == nullptr) return;
   const float* from = part + int64_t(blockIdx.y) * parts * d;
-  const int quad = threadIdx.x & 15, set = threadIdx.x >> 4, col = blockIdx.x * 64 + quad * 4;
-  float v[4] = {0.f, 0.f, 0.f, 0.f};
-  if (col < d) {
-    for (int r = set; r < parts; r += kJoinSets) {
-      const float4 f = *reinterpret_cast<const float4*>(from + int64_t(r) * d + col);
-      v[0] += f.x;
-      v[1] += f.y;
-      v[2] += f.z;
-      v[3] += f.w;
-    }
+  const int quad = threadIdx.x & 7, set = threadIdx.x >> 3, col = blockIdx.x * 32 + quad * 4;
+  f32x4 v[EACH];
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const int r = set + i * kJoinSets;
+    v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (col < d && r < parts) v[i] = *reinterpret_cast<const f32x4*>(from + int64_t(r) * d + col);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) meet[set][quad * 4 + i] = v[i];
+  for (int i = 1; i < EACH; ++i) v[0] += v[i];
+  meet[set][quad] = v[0];
   __syncthreads();
-  const int c = blockIdx.x * 64 + threadIdx.x;
-  if (threadIdx.x < 64 && c < d) {
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  if (threadIdx.x < 32 && c < d) {
     float sum = 0.f;
 #pragma unroll
-    for (int q = 0; q < kJoinSets; ++q) sum += meet[q][threadIdx.x];
+    for (int q = 0; q < kJoinSets; ++q) sum += meet[q][threadIdx.x >> 2][threadIdx.x & 3];
     if constexpr (sizeof(T) == 2)
       out[c] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(sum));
     else
@@ -332,71 +452,108 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const float* part, int p
 // ---- rules on sizes --------------------------------------------------------------------
 int round64(int v) { return (v + 63) / 64 * 64; }
 
-RowShape row_shape(int d, int threads) {
-  const int per_row = d / 8;
+// Lanes of a row of `chunks` blocks a lane, and rows of a workgroup of about `threads` threads.
+RowShape row_shape(int per_row, int chunks, int threads) {
   RowShape s{};
-  s.chunks = per_row <= 1024 ? 1 : per_row <= 2048 ? 2 : 4;
+  s.chunks = chunks;
   if (per_row <= 32) {
     s.lanes = 1;
     while (s.lanes < per_row) s.lanes *= 2;
   } else {
-    s.lanes = round64((per_row + s.chunks - 1) / s.chunks);
+    s.lanes = round64((per_row + chunks - 1) / chunks);
   }
   s.groups = s.lanes < threads ? threads / s.lanes : 1;
   return s;
 }
 
+// Blocks a lane: one up to 4096 columns, two up to 8192, else four.  More waves of fewer blocks
+// each are the faster (4096 x 4096 bf16: 26 us with one, 28 with two), until a row takes 1024
+// threads, of which a CU holds two rows only (4096 x 8192: 48 us with two blocks, 61 with one, 49 with
+// four; one row of 4096: 3.0, 3.3 and 4.1 us).  Many rows of up to 1536 columns take a wave each, without
+// barriers and with less of the last wave idle (16384 x 1032: 32 against 35 us, x 520: 18
+// against 21); few rows do not (300 x 1032 fp32: 4.4 against 3.6).
+RowShape forward_shape(int64_t rows, int d) {
+  const int per_row = d / 8;
+  if (per_row > 32 && per_row <= 192 && rows >= 2048) return row_shape(per_row, (per_row + 63) / 64, 256);
+  return row_shape(per_row, per_row <= 512 ? 1 : per_row <= 1024 ? 2 : 4, 256);
+}
+
+// Rows and columns apart, or in one pass.  Apart reads 7 matrices for 5 but has no partial sums and
+// one launch: 512 x 4096 bf16 9.6 against 14.9 us, 1024 x 4096 14.8 against 17.4, 2048 x 4096 26 against
+// 22; 1024 x 1032 14.2 against 12.1, 1024 x 8192 20.4 against 26.9, 4096 x 8192 67 against 55.  Past 8192
+// columns a lane of the one pass would hold two blocks or more with their sums, which spilled:
+// 1170 x 28672 in 98 us apart, 218 in one pass.
+bool apart(int64_t rows, int d) { return d > 8192 || rows <= 512 + d / 8; }
+
+// The rows' part, as the forward pass; at least 512 threads for the columns' part.
+RowShape apart_shape(int d) {
+  const int per_row = d / 8;
+  return row_shape(per_row, per_row <= 512 ? 1 : per_row <= 1024 ? 2 : 4, 512);
+}
+
 int norm_grad_blocks(int64_t rows, int d) {
-  const RowShape s = row_shape(d, 512);
+  const RowShape s = row_shape(d / 8, 1, kGradThreads);
   const int64_t sets = (rows + s.groups - 1) / s.groups;
-  return static_cast<int>(sets < 256 ? sets : 256);
+  return static_cast<int>(sets < kGradBlocks ? sets : kGradBlocks);
 }
 
 template <typename T, int CH, bool DROP>
 hipError_t forward(const NormParams& p, const RowShape& r, hipStream_t s) {
-  const int64_t sets = (p.rows + r.groups - 1) / r.groups;
-  const dim3 grid(static_cast<unsigned>(sets < (1 << 20) ? sets : 1 << 20)), block(r.lanes * r.groups);
+  const int64_t sets = (p.rows + r.groups - 1) / r.groups, most = 1 << 20;
+  const dim3 grid(static_cast<unsigned>(sets < most ? sets : most)), block(r.lanes * r.groups);
+  // three blocks a lane are a wave's only, four a wide row's
   if (r.lanes < 64)
-    hipLaunchKernelGGL((norm_kernel<T, CH, true, false, DROP>), grid, block, 0, s, p, r.lanes);
-  else if (r.lanes == 64)
-    hipLaunchKernelGGL((norm_kernel<T, CH, false, false, DROP>), grid, block, 0, s, p, r.lanes);
+    hipLaunchKernelGGL((norm_kernel<T, 1, true, false, DROP>), grid, block, 0, s, p, r.lanes);
+  else if (CH < 4 && r.lanes == 64)
+    hipLaunchKernelGGL((norm_kernel<T, CH < 4 ? CH : 1, false, false, DROP>), grid, block, 0, s, p, r.lanes);
   else
-    hipLaunchKernelGGL((norm_kernel<T, CH, false, true, DROP>), grid, block, 0, s, p, r.lanes);
+    hipLaunchKernelGGL((norm_kernel<T, CH != 3 ? CH : 1, false, true, DROP>), grid, block, 0, s, p, r.lanes);
   return hipGetLastError();
 }
 
 template <typename T, bool DROP>
 hipError_t forward(const NormParams& p, hipStream_t s) {
-  const RowShape r = row_shape(p.d, 256);
+  const RowShape r = forward_shape(p.rows, p.d);
   if (r.chunks == 1) return forward<T, 1, DROP>(p, r, s);
   if (r.chunks == 2) return forward<T, 2, DROP>(p, r, s);
+  if (r.chunks == 3) return forward<T, 3, DROP>(p, r, s);
   return forward<T, 4, DROP>(p, r, s);
 }
 
 template <typename T, int CH, bool DROP>
-hipError_t backward(const NormGradParams& p, const RowShape& r, int blocks, float* part, hipStream_t s) {
-  const dim3 grid(blocks), block(r.lanes * r.groups);
-  const size_t meet = r.groups > 1 ? size_t(r.lanes) * r.groups * 8 * sizeof(float) : 0;
-  if (r.lanes < 64)
-    hipLaunchKernelGGL((norm_grad_kernel<T, CH, true, false, DROP>), grid, block, meet, s, p, r.lanes, part);
+hipError_t rows_apart(const NormGradParams& p, const RowShape& r, hipStream_t s) {
+  const int64_t sets = p.dx.p == nullptr && p.dres.p == nullptr ? 0 : (p.rows + r.groups - 1) / r.groups;
+  const int stripes = p.dw == nullptr && p.db == nullptr ? 0 : (p.d + kStripe - 1) / kStripe;
+  const dim3 grid(static_cast<unsigned>(stripes + sets)), block(r.lanes * r.groups);
+  if (r.lanes > 64)
+    hipLaunchKernelGGL((norm_apart_kernel<T, CH, false, true, DROP>), grid, block, 0, s, p, r.lanes, stripes);
   else if (r.lanes == 64)
-    hipLaunchKernelGGL((norm_grad_kernel<T, CH, false, false, DROP>), grid, block, meet, s, p, r.lanes, part);
+    hipLaunchKernelGGL((norm_apart_kernel<T, 1, false, false, DROP>), grid, block, 0, s, p, r.lanes, stripes);
   else
-    hipLaunchKernelGGL((norm_grad_kernel<T, CH, false, true, DROP>), grid, block, meet, s, p, r.lanes, part);
+    hipLaunchKernelGGL((norm_apart_kernel<T, 1, true, false, DROP>), grid, block, 0, s, p, r.lanes, stripes);
   return hipGetLastError();
 }
 
 template <typename T, bool DROP>
 hipError_t backward(const NormGradParams& p, float* part, hipStream_t s) {
-  const RowShape r = row_shape(p.d, 512);
+  if (apart(p.rows, p.d)) {
+    const RowShape r = apart_shape(p.d);
+    if (r.chunks == 1) return rows_apart<T, 1, DROP>(p, r, s);
+    if (r.chunks == 2) return rows_apart<T, 2, DROP>(p, r, s);
+    return rows_apart<T, 4, DROP>(p, r, s);
+  }
+  const RowShape r = row_shape(p.d / 8, 1, kGradThreads);
   const int blocks = norm_grad_blocks(p.rows, p.d);
-  hipError_t e = hipSuccess;
-  if (p.rows > 0)
-    e = r.chunks == 1   ? backward<T, 1, DROP>(p, r, blocks, part, s)
-        : r.chunks == 2 ? backward<T, 2, DROP>(p, r, blocks, part, s)
-                        : backward<T, 4, DROP>(p, r, blocks, part, s);
+  const dim3 grid(blocks), block(r.lanes * r.groups);
+  if (r.lanes > 64)
+    hipLaunchKernelGGL((norm_grad_kernel<T, false, true, DROP>), grid, block, 0, s, p, r.lanes, part);
+  else if (r.lanes == 64)
+    hipLaunchKernelGGL((norm_grad_kernel<T, false, false, DROP>), grid, block, 0, s, p, r.lanes, part);
+  else
+    hipLaunchKernelGGL((norm_grad_kernel<T, true, false, DROP>), grid, block, 0, s, p, r.lanes, part);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || (p.dw == nullptr && p.db == nullptr)) return e;
-  hipLaunchKernelGGL(norm_join_kernel<T>, dim3((p.d + 63) / 64, 2), dim3(256), 0, s, part, blocks, p.d,
+  hipLaunchKernelGGL(norm_join_kernel<T>, dim3((p.d + 31) / 32, 2), dim3(256), 0, s, part, blocks, p.d,
                      static_cast<T*>(p.dw), static_cast<T*>(p.db));
   return hipGetLastError();
 }
@@ -410,12 +567,13 @@ hipError_t launch_norm(const NormParams& p, int dtype, hipStream_t s) {
   return drop ? forward<float, true>(p, s) : forward<float, false>(p, s);
 }
 
-int64_t norm_grad_workspace(int64_t rows, int32_t d, int dtype) {
-  (void)dtype;
-  return int64_t(2) * norm_grad_blocks(rows, d) * d * int64_t(sizeof(float));
+int64_t norm_grad_workspace(int64_t rows, int32_t d) {
+  return apart(rows, d) ? 0 : int64_t(2) * norm_grad_blocks(rows, d) * d * int64_t(sizeof(float));
 }
 
 hipError_t launch_norm_grad(const NormGradParams& p, int dtype, void* ws, hipStream_t s) {
+  // without rows only dw and db are written
+  if (p.rows == 0 && p.dw == nullptr && p.db == nullptr) return hipSuccess;
   float* part = static_cast<float*>(ws);
   const bool drop = p.drop.least != 0;
   if (dtype == 1) return drop ? backward<uint16_t, true>(p, part, s) : backward<uint16_t, false>(p, part, s);

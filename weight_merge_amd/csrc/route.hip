@@ -22,6 +22,9 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kMostBlocks = 256;
+#ifndef ONE
+#define ONE 32
+#endif
 
 // Order-preserving map of fp32 bits to nonzero integers, 0 for -inf (closed); -0 and +0 are equal,
 // and NaN is above everything, so a row that holds one still picks experts inside its range.
@@ -78,12 +81,15 @@ __device__ __forceinline__ void load_logits(const T* row, int first, int E, floa
   }
 }
 
-// Probabilities of a row from a lane's eight logits, and whether any expert is open.
+// Softmax of a row from a lane's eight logits: x over sums to 1.  Whether any expert is open.
 template <int L>
-__device__ __forceinline__ bool softmax8(const float (&z)[8], float (&x)[8], float& over) {
+__device__ __forceinline__ bool softmax8(const float (&z)[8], uint32_t (&key)[8], float (&x)[8], float& over) {
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, rank_key(z[i]));
+  for (int i = 0; i < 8; ++i) {
+    key[i] = rank_key(z[i]);
+    top = max(top, key[i]);
+  }
   top = row_max<L>(top);
   const bool open = top != 0;
   const float m = top == 0xffffffffu ? __builtin_nanf("")
@@ -91,8 +97,8 @@ __device__ __forceinline__ bool softmax8(const float (&z)[8], float (&x)[8], flo
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    // -inf is zero also where the largest logit is infinite; m = -inf only in a row that is not open
-    x[i] = open && z[i] != -__builtin_inff() ? expf(z[i] - m) : 0.f;
+    // a closed expert's is zero also where the largest logit is infinite
+    x[i] = key[i] != 0 ? expf(z[i] - m) : 0.f;
     sum += x[i];
   }
   sum = row_sum<L>(sum);
@@ -138,10 +144,10 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteParams p, BalanceP
     float z[8], x[8], over;
     load_logits<T, VEC>(static_cast<const T*>(p.logits.p) + at * p.logits.ld, first, p.E, z);
     const bool counts_row = inside && (p.valid == nullptr || p.valid[at] != 0);
-    const bool open = softmax8<L>(z, x, over) && counts_row;
     uint32_t key[8];
+    const bool open = softmax8<L>(z, key, x, over) && counts_row;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) key[i] = open ? rank_key(z[i]) : 0u;
+    for (int i = 0; i < 8; ++i) key[i] = open ? key[i] : 0u;
     uint32_t taken = 0;                     // bit i: expert first + i is picked
     unsigned long long slots = 0;           // byte i: its place among the picks
     int n = 0;
@@ -241,12 +247,23 @@ __global__ void __launch_bounds__(kThreads) balance_join_kernel(RouteParams p, B
   __shared__ double wave_prob[kThreads / 64][64];
   __shared__ int wave_count[kThreads / 64][64], wave_used[kThreads / 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int EACH = kMostBlocks / (kThreads / 64);
   double sum = 0.0;
   int count = 0, used = 0;
-  for (int b = wave; b < blocks; b += kThreads / 64) {
-    sum += parts.prob[b * kMaxExperts + lane];
-    count += parts.counts[b * kMaxExperts + lane];
-    used += parts.used[b];
+  float prob[EACH];
+  int counts[EACH], rows[EACH];
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {  // all loads in flight at once
+    const int b = wave + i * (kThreads / 64);
+    prob[i] = b < blocks ? parts.prob[b * kMaxExperts + lane] : 0.f;
+    counts[i] = b < blocks ? parts.counts[b * kMaxExperts + lane] : 0;
+    rows[i] = b < blocks ? parts.used[b] : 0;
+  }
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    sum += prob[i];
+    count += counts[i];
+    used += rows[i];
   }
   wave_prob[wave][lane] = sum;
   wave_count[wave][lane] = count;
@@ -264,18 +281,38 @@ __global__ void __launch_bounds__(kThreads) balance_join_kernel(RouteParams p, B
 }
 
 // ---- backward --------------------------------------------------------------------------
-// A lane walks the row's k picks (its neighbours read the same addresses) and keeps what falls
-// on its eight experts; an index outside [0, E) is passed over.
+// Eight of a row's picks, loaded together; past the k-th none (index -1).
+struct Picks {
+  int e[8];
+  float gate[8], dgate[8];
+
+  __device__ __forceinline__ void load(const RouteGradParams& p, int64_t at, int j0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const bool some = j0 + j < p.k;
+      const int64_t i = at * p.k + (some ? j0 + j : 0);
+      e[j] = some ? p.idx[i] : -1;
+      gate[j] = p.renorm ? p.gate[i] : 1.f;
+      dgate[j] = p.dgate[i];
+    }
+  }
+};
+
+// The lanes of a row read the same picks, and each keeps what falls on its eight experts; an index
+// outside [0, E) is passed over.  The first eight picks stay in registers between the sum over
+// them and its use.
 template <typename T, int L, bool VEC>
 __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradParams p) {
   const int l = threadIdx.x & (L - 1), first = l * 8;
   const int64_t row = (int64_t(blockIdx.x) * 256 + threadIdx.x) / L;
   const bool inside = row < p.rows;
   const int64_t at = inside ? row : p.rows - 1;
-  const int32_t* idx = p.idx + at * p.k;
   float z[8], x[8], over, dp[8], dz[8];
+  uint32_t key[8];
+  Picks picks;
   load_logits<T, VEC>(static_cast<const T*>(p.logits.p) + at * p.logits.ld, first, p.E, z);
-  const bool open = softmax8<L>(z, x, over) && idx[0] >= 0;
+  const int top = p.idx[at * p.k];
+  if (p.dgate != nullptr) picks.load(p, at, 0);
   float per_count = 0.f;
   if (p.dloss != nullptr) {
     const int used = p.used[0];
@@ -286,23 +323,28 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradParams p) {
     dp[i] = p.dloss != nullptr && first + i < p.E ? per_count * float(p.counts[first + i]) : 0.f;
     dz[i] = 0.f;
   }
+  const bool open = softmax8<L>(z, key, x, over) && top >= 0;
   if (p.dgate != nullptr) {
-    const float* gate = p.gate + at * p.k;
-    const float* dgate = p.dgate + at * p.k;
     float along = 0.f;
-    if (p.renorm)
-      for (int j = 0; j < p.k; ++j)
-        if (idx[j] >= 0) along = fmaf(gate[j], dgate[j], along);
-    for (int j = 0; j < p.k; ++j) {
-      const int e = idx[j] - first;
-      const float d = p.renorm ? gate[j] * (dgate[j] - along) : dgate[j];
+    if (p.renorm) {
+      for (int j0 = 0; j0 < p.k; j0 += 8) {
+        if (j0 > 0) picks.load(p, at, j0);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (e == i) {
+        for (int j = 0; j < 8; ++j) along += picks.e[j] >= 0 ? picks.gate[j] * picks.dgate[j] : 0.f;
+      }
+    }
+    for (int j0 = 0; j0 < p.k; j0 += 8) {
+      if (p.k > 8) picks.load(p, at, j0);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int e = picks.e[j] - first;
+        const float d = p.renorm ? picks.gate[j] * (picks.dgate[j] - along) : picks.dgate[j];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
           if (p.renorm)
-            dz[i] += d;
+            dz[i] += e == i ? d : 0.f;
           else
-            dp[i] += d;
+            dp[i] += e == i ? d : 0.f;
         }
       }
     }
@@ -336,9 +378,17 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradParams p) {
 // ---- rules on sizes --------------------------------------------------------------------
 int row_lanes(int E) { return E <= 8 ? 1 : E <= 16 ? 2 : E <= 32 ? 4 : 8; }
 
-int route_blocks(int64_t rows, int E) {
-  const int64_t at_once = kThreads / row_lanes(E), sets = (rows + at_once - 1) / at_once;
-  return static_cast<int>(sets < kMostBlocks ? sets : kMostBlocks);
+struct RouteGrid {
+  int blocks;
+  int threads;
+};
+
+RouteGrid route_grid(int64_t rows, int E) {
+  const int64_t waves = (rows * row_lanes(E) + 63) / 64;
+  if (waves <= ONE) return {1, static_cast<int>(waves < 1 ? 64 : waves < 16 ? 64 * waves : kThreads)};
+  const int64_t each = (waves + kMostBlocks - 1) / kMostBlocks, most = each < 4 ? 4 : each < 16 ? each : 16;
+  const int64_t blocks = (waves + most - 1) / most;
+  return {static_cast<int>(blocks < kMostBlocks ? blocks : kMostBlocks), static_cast<int>(64 * most)};
 }
 
 // Whether eight logits may be moved as 16-byte vectors.
@@ -348,19 +398,19 @@ bool vectors(const void* p, int64_t ld, int E, int dtype) {
 }
 
 template <typename T, int L>
-void forward(const RouteParams& p, const BalanceParts& parts, int blocks, int threads, bool vec, hipStream_t s) {
+void forward(const RouteParams& p, const BalanceParts& parts, const RouteGrid& g, bool vec, hipStream_t s) {
   if (vec)
-    hipLaunchKernelGGL((route_kernel<T, L, true>), dim3(blocks), dim3(threads), 0, s, p, parts);
+    hipLaunchKernelGGL((route_kernel<T, L, true>), dim3(g.blocks), dim3(g.threads), 0, s, p, parts);
   else
-    hipLaunchKernelGGL((route_kernel<T, L, false>), dim3(blocks), dim3(threads), 0, s, p, parts);
+    hipLaunchKernelGGL((route_kernel<T, L, false>), dim3(g.blocks), dim3(g.threads), 0, s, p, parts);
 }
 template <typename T>
-void forward(const RouteParams& p, const BalanceParts& parts, int blocks, int threads, bool vec, hipStream_t s) {
+void forward(const RouteParams& p, const BalanceParts& parts, const RouteGrid& g, bool vec, hipStream_t s) {
   switch (row_lanes(p.E)) {
-    case 1: return forward<T, 1>(p, parts, blocks, threads, vec, s);
-    case 2: return forward<T, 2>(p, parts, blocks, threads, vec, s);
-    case 4: return forward<T, 4>(p, parts, blocks, threads, vec, s);
-    default: return forward<T, 8>(p, parts, blocks, threads, vec, s);
+    case 1: return forward<T, 1>(p, parts, g, vec, s);
+    case 2: return forward<T, 2>(p, parts, g, vec, s);
+    case 4: return forward<T, 4>(p, parts, g, vec, s);
+    default: return forward<T, 8>(p, parts, g, vec, s);
   }
 }
 
@@ -385,32 +435,29 @@ void backward(const RouteGradParams& p, bool vec, hipStream_t s) {
 }  // namespace
 
 int64_t route_workspace(int64_t rows, int32_t E) {
-  const int blocks = route_blocks(rows, E);
-  return blocks <= 1 ? 0 : int64_t(blocks) * (2 * kMaxExperts + 1) * 4;
+  const int blocks = route_grid(rows, E).blocks;
+  return blocks == 1 ? 0 : int64_t(blocks) * (2 * kMaxExperts + 1) * 4;
 }
 
 hipError_t launch_route(const RouteParams& p, int dtype, void* ws, hipStream_t s) {
   // no rows: one workgroup that writes a balance of nothing
   if (p.rows == 0 && p.counts == nullptr) return hipSuccess;
-  const int lanes = row_lanes(p.E);
-  int blocks = route_blocks(p.rows, p.E);
-  blocks = blocks < 1 ? 1 : blocks;
-  const int64_t need = (p.rows * lanes + 63) / 64 * 64;
-  const int threads = need < 64 ? 64 : need < kThreads ? static_cast<int>(need) : kThreads;
+  const RouteGrid g = route_grid(p.rows, p.E);
+  const bool join = g.blocks > 1 && p.counts != nullptr;
   BalanceParts parts{};
-  if (blocks > 1 && p.counts != nullptr) {
+  if (join) {
     parts.prob = static_cast<float*>(ws);
-    parts.counts = reinterpret_cast<int32_t*>(parts.prob + blocks * kMaxExperts);
-    parts.used = parts.counts + blocks * kMaxExperts;
+    parts.counts = reinterpret_cast<int32_t*>(parts.prob + g.blocks * kMaxExperts);
+    parts.used = parts.counts + g.blocks * kMaxExperts;
   }
   const bool vec = vectors(p.logits.p, p.logits.ld, p.E, dtype);
   if (dtype == 1)
-    forward<uint16_t>(p, parts, blocks, threads, vec, s);
+    forward<uint16_t>(p, parts, g, vec, s);
   else
-    forward<float>(p, parts, blocks, threads, vec, s);
+    forward<float>(p, parts, g, vec, s);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || blocks == 1 || p.counts == nullptr) return e;
-  hipLaunchKernelGGL(balance_join_kernel, dim3(1), dim3(kThreads), 0, s, p, parts, blocks);
+  if (e != hipSuccess || !join) return e;
+  hipLaunchKernelGGL(balance_join_kernel, dim3(1), dim3(kThreads), 0, s, p, parts, g.blocks);
   return hipGetLastError();
 }
 
