@@ -380,9 +380,12 @@ def _mat(t, rows: int, cols: int, dt, dev: int, name: str):
     """Pointer and row stride of a [rows, cols] matrix."""
     if t is None:
         return None, 0
-    if t.shape != (rows, cols) or t.dtype is not dt or t.get_device() != dev or t.stride(1) != 1:
+    if t.shape != (rows, cols) or t.dtype is not dt or t.get_device() != dev:
         _refuse(t, (rows, cols), dt, dev, name)
-    return t.data_ptr(), t.stride(0) if rows > 1 else cols
+    ld, one = t.stride()
+    if one != 1:
+        _refuse(t, (rows, cols), dt, dev, name)
+    return t.data_ptr(), ld if rows > 1 else cols
 
 
 def _vec(t, n: int, dt, dev: int, name: str):
@@ -400,10 +403,15 @@ def _sizes(x: torch.Tensor, w: torch.Tensor):
     return x.shape[0], w.shape[0], w.shape[1]
 
 
+# index of the current device (the public call looks whether the runtime is up each time; a device
+# tensor is there already)
+_device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _current(dev: int):
     if dev < 0:
         raise ValueError("tensors must be on the device")
-    if dev != torch.cuda.current_device():
+    if dev != _device_now():
         raise ValueError(f"tensors are on cuda:{dev}, but cuda:{torch.cuda.current_device()} is current")
 
 

@@ -981,6 +981,7 @@ int ada_route(const ada_route_args* q, int32_t dtype, void* workspace, int64_t w
   p.E = q->E;
   p.k = q->k;
   p.renorm = q->renorm;
+  p.per_pick = double(q->E) / double(q->k);
   const hipError_t e = ada::launch_route(p, dtype, workspace, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? ADA_OK : ADA_EHIP;
 }

@@ -82,6 +82,7 @@ struct RouteParams {
   int32_t E;
   int32_t k;
   int32_t renorm;
+  double per_pick;  // E / k, the loss's factor
 };
 int64_t route_workspace(int64_t rows, int32_t E);
 hipError_t launch_route(const RouteParams& p, int dtype, void* ws, hipStream_t s);

@@ -12,9 +12,9 @@
 //
 // A row is shared by 1, 2, 4 or 8 neighbouring lanes, eight experts each, so one 16-byte load a
 // lane (bf16) brings a wave 8 to 64 rows and the softmax needs at most three steps across
-// lanes.  A pick is a maximum over a lane's eight keys, the same steps across lanes, and a
-// ballot that names the first lane that holds it.  Bound by launches and latency at the sizes of a
-// training step (16384 rows of 64 experts are 5 MB).
+// lanes.  A pick is a maximum over a lane's eight keys and the row's lanes, then the lowest index that
+// holds it.  Bound by launches and latency up to some ten thousand rows (16384 rows of 64 experts
+// are 5 MB), by the picks' instructions past that (262144 x 64, eight picks: 40 us for 84 MB).
 #include "elements.h"
 
 namespace ada {
@@ -22,19 +22,24 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kMostBlocks = 256;
-#ifndef ONE
-#define ONE 32
-#endif
 
-// Order-preserving map of fp32 bits to nonzero integers, 0 for -inf (closed); -0 and +0 are equal,
-// and NaN is above everything, so a row that holds one still picks experts inside its range.
+// Order-preserving map of a logit to an integer: -0 and +0 are equal, NaN is above everything (a
+// row that holds one still picks inside its range), and -inf, a closed expert, gives kClosed, next below
+// the lowest finite one.
+constexpr uint32_t kClosed = 0x007fffffu;
 __device__ __forceinline__ uint32_t rank_key(float f) {
-  if (f != f) return 0xffffffffu;
-  if (f == -__builtin_inff()) return 0u;
-  const uint32_t u = f == 0.f ? 0u : __float_as_uint(f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  const uint32_t u = __float_as_uint(f + 0.f);
+  const uint32_t k = u ^ (uint32_t(int(u) >> 31) | 0x80000000u);
+  return f == f ? k : 0xffffffffu;
+}
+__device__ __forceinline__ float value_of_key(uint32_t k) {  // of an open expert; NaN of 0xffffffff
+  return __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xffffffffu));
 }
 
+template <int V>
+struct Int {
+  static constexpr int value = V;
+};
 template <int CTRL>
 __device__ __forceinline__ uint32_t swapped(uint32_t v) {
   return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xf, 0xf, true));
@@ -61,6 +66,27 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v) {
   return v;
 }
 
+template <int L>
+__device__ __forceinline__ uint32_t row_min(uint32_t v) {
+  if constexpr (L > 1) v = min(v, across<1>(v));
+  if constexpr (L > 2) v = min(v, across<2>(v));
+  if constexpr (L > 4) v = min(v, across<4>(v));
+  return v;
+}
+// Sum over the lanes of 16 that hold the same part of their rows, on each of them (rotations by
+// L, 2 L, .. 8 of the row of 16).
+template <int L, typename V>
+__device__ __forceinline__ V same_part_sum(V v) {
+  const auto turned = [](auto ctrl, V a) {
+    return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, a), decltype(ctrl)::value, 0xf, 0xf, true));
+  };
+  if constexpr (L <= 1) v += turned(Int<0x121>(), v);
+  if constexpr (L <= 2) v += turned(Int<0x122>(), v);
+  if constexpr (L <= 4) v += turned(Int<0x124>(), v);
+  v += turned(Int<0x128>(), v);
+  return v;
+}
+
 __device__ __forceinline__ float value_of(float v) { return v; }
 __device__ __forceinline__ float value_of(uint16_t v) { return __uint_as_float(uint32_t(v) << 16); }
 
@@ -81,54 +107,86 @@ __device__ __forceinline__ void load_logits(const T* row, int first, int E, floa
   }
 }
 
-// Softmax of a row from a lane's eight logits: x over sums to 1.  Whether any expert is open.
+// Softmax of a row from a lane's eight logits, x over sums to 1, and their keys; a row that does not
+// count has every expert closed.  Whether any is open.
 template <int L>
-__device__ __forceinline__ bool softmax8(const float (&z)[8], uint32_t (&key)[8], float (&x)[8], float& over) {
+__device__ __forceinline__ bool softmax8(const float (&z)[8], bool counts, uint32_t (&key)[8], float (&x)[8],
+                                         float& m, float& over) {
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    key[i] = rank_key(z[i]);
+    key[i] = counts ? rank_key(z[i]) : 0u;
     top = max(top, key[i]);
   }
   top = row_max<L>(top);
-  const bool open = top != 0;
-  const float m = top == 0xffffffffu ? __builtin_nanf("")
-                                     : __uint_as_float((top & 0x80000000u) ? top & 0x7fffffffu : ~top);
+  m = value_of_key(top);
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     // a closed expert's is zero also where the largest logit is infinite
-    x[i] = key[i] != 0 ? expf(z[i] - m) : 0.f;
+    x[i] = key[i] > kClosed ? expf(z[i] - m) : 0.f;
     sum += x[i];
   }
   sum = row_sum<L>(sum);
-  over = open ? 1.f / sum : 0.f;
-  return open;
+  over = top > kClosed ? 1.f / sum : 0.f;
+  return top > kClosed;
 }
 
 // ---- forward ---------------------------------------------------------------------------
+__device__ __forceinline__ double wave_total(double v) {
+  const auto part = [&](auto ctrl, auto rows) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, int(uint32_t(u)), decltype(ctrl)::value, decltype(rows)::value, 0xf, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, int(u >> 32), decltype(ctrl)::value, decltype(rows)::value, 0xf, true);
+    return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+  };
+  v += part(Int<0x111>(), Int<0xf>());
+  v += part(Int<0x112>(), Int<0xf>());
+  v += part(Int<0x114>(), Int<0xf>());
+  v += part(Int<0x118>(), Int<0xf>());
+  v += part(Int<0x142>(), Int<0xa>());
+  v += part(Int<0x143>(), Int<0xc>());
+  return v;  // on lane 63
+}
+
 // The last step of the balance: counts, mean probabilities and the loss from the sums over every
-// row, expert e on lane e of the first wave.
+// row, expert e on lane e of one wave.
 __device__ __forceinline__ void finish_balance(const RouteParams& p, int lane, int count, double sum, int used) {
-  const double n = used > 0 ? double(used) : 1.0;
+  const double over = used > 0 ? 1.0 / double(used) : 1.0, mean = sum * over;
   if (lane < p.E) {
     p.counts[lane] = count;
-    p.prob[lane] = float(sum / n);
+    p.prob[lane] = float(mean);
   }
-  double part = lane < p.E ? double(count) / (double(p.k) * n) * (sum / n) : 0.0;
-  for (int m = 1; m < 64; m <<= 1) part += __shfl_xor(part, m, 64);
-  if (lane == 0) {
-    p.loss[0] = float(double(p.E) * part);
+  const double total = wave_total(lane < p.E ? double(count) * mean : 0.0);
+  if (lane == 63) {
+    p.loss[0] = float(total * over * p.per_pick);
     p.used[0] = used;
   }
 }
 
-// Partial sums of the balance of one workgroup, [blocks] of each: probabilities, counts, rows.
+// Partial sums of the balance, one of each for every workgroup.
 struct BalanceParts {
-  float* prob;
-  int32_t* counts;
-  int32_t* used;
+  uint2* experts;  // [blocks][kMaxExperts]: sum of probabilities (fp32 bits), picks
+  int32_t* used;   // [blocks]: rows that count
 };
+
+// The next pick of a row, known to all its lanes: the largest key, the lowest index among equals.  It
+// is marked as taken.  `best` is at most kClosed where no open expert is left.
+constexpr uint32_t kTaken = 1;  // no logit's key
+template <int L>
+__device__ __forceinline__ uint32_t next_pick(uint32_t (&key)[8], int first, uint32_t& best) {
+  best = key[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) best = max(best, key[i]);
+  best = row_max<L>(best);
+  uint32_t at = kMaxExperts;  // none
+#pragma unroll
+  for (int i = 7; i >= 0; --i) at = key[i] == best ? first + i : at;
+  at = best > kClosed ? row_min<L>(at) : kMaxExperts;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) key[i] = at == uint32_t(first + i) ? kTaken : key[i];
+  return at;
+}
 
 template <typename T, int L, bool VEC>
 __global__ void __launch_bounds__(kThreads) route_kernel(RouteParams p, BalanceParts parts) {
@@ -142,129 +200,123 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteParams p, BalanceP
     const bool inside = row < p.rows;
     const int64_t at = inside ? row : p.rows - 1;
     float z[8], x[8], over;
-    load_logits<T, VEC>(static_cast<const T*>(p.logits.p) + at * p.logits.ld, first, p.E, z);
-    const bool counts_row = inside && (p.valid == nullptr || p.valid[at] != 0);
     uint32_t key[8];
-    const bool open = softmax8<L>(z, key, x, over) && counts_row;
+    load_logits<T, VEC>(static_cast<const T*>(p.logits.p) + at * p.logits.ld, first, p.E, z);
+    float m;
+    const bool open = softmax8<L>(z, inside && (p.valid == nullptr || p.valid[at] != 0), key, x, m, over);
+    // pick j = q L + l stays on lane l
+    uint32_t pick[8];
+    float e[8], picked = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) key[i] = open ? key[i] : 0u;
-    uint32_t taken = 0;                     // bit i: expert first + i is picked
-    unsigned long long slots = 0;           // byte i: its place among the picks
-    int n = 0;
-    for (int j = 0; j < p.k; ++j) {
-      uint32_t mine = key[0];
+    for (int q = 0; q < 8; ++q) {
+      if (q * L >= p.k) break;
+      uint32_t mine = 0;
+      pick[q] = kMaxExperts;
 #pragma unroll
-      for (int i = 1; i < 8; ++i) mine = max(mine, key[i]);
-      const uint32_t best = row_max<L>(mine);
-      const unsigned long long holders = __ballot(mine == best) >> (lane - l) & ((1ull << L) - 1);
-      n += best != 0;
-      if (best != 0 && __builtin_ctzll(holders) == l) {
-        bool found = false;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (!found && key[i] == best) {
-            found = true;
-            key[i] = 0;
-            taken |= 1u << i;
-            slots |= static_cast<unsigned long long>(j) << (8 * i);
-          }
-        }
+      for (int t = 0; t < L; ++t) {
+        if (q * L + t >= p.k) break;
+        uint32_t best;
+        const uint32_t one = next_pick<L>(key, first, best);
+        pick[q] = t == l ? one : pick[q];
+        mine = t == l ? best : mine;
       }
+      e[q] = pick[q] < kMaxExperts ? expf(value_of_key(mine) - m) : 0.f;
+      picked += e[q];
     }
-    float picked = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) picked += (taken >> i & 1) ? x[i] : 0.f;
     picked = row_sum<L>(picked);
-    const float share = p.renorm ? 1.f / picked : over;
+    const float share = p.renorm ? (open ? 1.f / picked : 0.f) : over;
     if (inside) {
-      int32_t* idx = p.idx + row * p.k;
-      float* gate = p.gate + row * p.k;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (taken >> i & 1) {
-          const int j = int(slots >> (8 * i)) & 0xff;
-          idx[j] = first + i;
-          gate[j] = x[i] * share;
+      for (int q = 0; q < 8; ++q) {
+        const int j = q * L + l;
+        if (q * L >= p.k) break;
+        if (j < p.k) {
+          const bool some = pick[q] < kMaxExperts;
+          p.idx[row * p.k + j] = some ? int32_t(pick[q]) : -1;
+          p.gate[row * p.k + j] = some ? e[q] * share : 0.f;
         }
-      }
-      for (int j = n + l; j < p.k; j += L) {
-        idx[j] = -1;
-        gate[j] = 0.f;
       }
     }
     if (balance) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        probs[i] += open ? x[i] * over : 0.f;
-        counts[i] += taken >> i & 1;
+        probs[i] = fmaf(x[i], over, probs[i]);
+        counts[i] += key[i] == kTaken;
       }
       used += open && l == 0;
     }
   }
   if (!balance) return;
 
-  // the same experts of a wave's rows, then the waves
-  __shared__ float wave_prob[kThreads / 64][kMaxExperts];
-  __shared__ int wave_count[kThreads / 64][kMaxExperts], wave_used[kThreads / 64];
+  // the same experts of 16 lanes' rows, of a wave's four such sets, of the waves
+  constexpr int WAVES = kThreads / 64;
+  __shared__ float set_prob[WAVES][4][kMaxExperts], wave_prob[WAVES][kMaxExperts];
+  __shared__ int set_count[WAVES][4][kMaxExperts], wave_count[WAVES][kMaxExperts], wave_used[WAVES];
   const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-  for (int m = L; m < 64; m <<= 1) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      probs[i] += __shfl_xor(probs[i], m, 64);
-      counts[i] += __shfl_xor(counts[i], m, 64);
-    }
-    used += __shfl_xor(used, m, 64);
+  for (int i = 0; i < 8; ++i) {
+    probs[i] = same_part_sum<L>(probs[i]);
+    counts[i] = same_part_sum<L>(counts[i]);
   }
-  if (lane < L) {
+  if ((lane & 15) < L) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      wave_prob[wave][first + i] = probs[i];
-      wave_count[wave][first + i] = counts[i];
+      set_prob[wave][lane >> 4][first + i] = probs[i];
+      set_count[wave][lane >> 4][first + i] = counts[i];
     }
+  }
+  for (int s = 1; s < 64; s <<= 1) used += __shfl_xor(used, s, 64);
+  __syncthreads();
+  {
+    const float* sp = set_prob[wave][0] + lane;
+    const int* sc = set_count[wave][0] + lane;
+    const bool real = lane < 8 * L;
+    wave_prob[wave][lane] = real ? (sp[0] + sp[64]) + (sp[128] + sp[192]) : 0.f;
+    wave_count[wave][lane] = real ? (sc[0] + sc[64]) + (sc[128] + sc[192]) : 0;
     if (lane == 0) wave_used[wave] = used;
   }
   __syncthreads();
   if (wave != 0) return;
   double sum = 0.0;
   int count = 0, rows = 0;
-  if (lane < 8 * L)
-    for (int w = 0; w < waves; ++w) {
-      sum += wave_prob[w][lane];
-      count += wave_count[w][lane];
-    }
-  for (int w = 0; w < waves; ++w) rows += wave_used[w];
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    if (w >= waves) break;
+    sum += wave_prob[w][lane];
+    count += wave_count[w][lane];
+    rows += wave_used[w];
+  }
   if (gridDim.x == 1) {
     finish_balance(p, lane, count, sum, rows);
   } else {
-    parts.prob[blockIdx.x * kMaxExperts + lane] = float(sum);
-    parts.counts[blockIdx.x * kMaxExperts + lane] = count;
+    parts.experts[blockIdx.x * kMaxExperts + lane] = make_uint2(__float_as_uint(float(sum)), uint32_t(count));
     if (lane == 0) parts.used[blockIdx.x] = rows;
   }
 }
 
-// One workgroup: expert e on lane e of each wave, the parts dealt to the waves.
+// One workgroup: expert e on lane e of each wave, the parts dealt to the waves, all of a lane's loads
+// in flight at once.
 __global__ void __launch_bounds__(kThreads) balance_join_kernel(RouteParams p, BalanceParts parts, int blocks) {
-  __shared__ double wave_prob[kThreads / 64][64];
-  __shared__ int wave_count[kThreads / 64][64], wave_used[kThreads / 64];
+  constexpr int WAVES = kThreads / 64, EACH = kMostBlocks / WAVES;
+  __shared__ double wave_prob[WAVES][64];
+  __shared__ int wave_count[WAVES][64], wave_used[WAVES];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  constexpr int EACH = kMostBlocks / (kThreads / 64);
-  double sum = 0.0;
-  int count = 0, used = 0;
-  float prob[EACH];
-  int counts[EACH], rows[EACH];
-#pragma unroll
-  for (int i = 0; i < EACH; ++i) {  // all loads in flight at once
-    const int b = wave + i * (kThreads / 64);
-    prob[i] = b < blocks ? parts.prob[b * kMaxExperts + lane] : 0.f;
-    counts[i] = b < blocks ? parts.counts[b * kMaxExperts + lane] : 0;
-    rows[i] = b < blocks ? parts.used[b] : 0;
-  }
+  uint2 part[EACH];
 #pragma unroll
   for (int i = 0; i < EACH; ++i) {
-    sum += prob[i];
-    count += counts[i];
-    used += rows[i];
+    const int b = wave + i * WAVES;
+    part[i] = b < blocks && lane < p.E ? parts.experts[b * kMaxExperts + lane] : make_uint2(0, 0);
   }
+  static_assert(kMostBlocks <= kThreads);
+  int used = int(threadIdx.x) < blocks ? parts.used[threadIdx.x] : 0;
+  double sum = 0.0;
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    sum += __uint_as_float(part[i].x);
+    count += int(part[i].y);
+  }
+  for (int s = 1; s < 64; s <<= 1) used += __shfl_xor(used, s, 64);
   wave_prob[wave][lane] = sum;
   wave_count[wave][lane] = count;
   if (lane == 0) wave_used[wave] = used;
@@ -272,7 +324,8 @@ __global__ void __launch_bounds__(kThreads) balance_join_kernel(RouteParams p, B
   if (wave != 0) return;
   sum = 0.0;
   count = used = 0;
-  for (int w = 0; w < kThreads / 64; ++w) {
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
     sum += wave_prob[w][lane];
     count += wave_count[w][lane];
     used += wave_used[w];
@@ -281,38 +334,34 @@ __global__ void __launch_bounds__(kThreads) balance_join_kernel(RouteParams p, B
 }
 
 // ---- backward --------------------------------------------------------------------------
-// Eight of a row's picks, loaded together; past the k-th none (index -1).
-struct Picks {
-  int e[8];
-  float gate[8], dgate[8];
-
-  __device__ __forceinline__ void load(const RouteGradParams& p, int64_t at, int j0) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const bool some = j0 + j < p.k;
-      const int64_t i = at * p.k + (some ? j0 + j : 0);
-      e[j] = some ? p.idx[i] : -1;
-      gate[j] = p.renorm ? p.gate[i] : 1.f;
-      dgate[j] = p.dgate[i];
-    }
-  }
-};
-
-// The lanes of a row read the same picks, and each keeps what falls on its eight experts; an index
-// outside [0, E) is passed over.  The first eight picks stay in registers between the sum over
-// them and its use.
+// The lanes of a row share its picks, add each one's part to the row in LDS (an index outside
+// [0, E) is passed over, one that is there twice is added twice), and take their eight experts' back.
 template <typename T, int L, bool VEC>
 __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradParams p) {
+  __shared__ float at_expert[256][8];  // rows of 8 L, one to L lanes
   const int l = threadIdx.x & (L - 1), first = l * 8;
   const int64_t row = (int64_t(blockIdx.x) * 256 + threadIdx.x) / L;
   const bool inside = row < p.rows;
   const int64_t at = inside ? row : p.rows - 1;
-  float z[8], x[8], over, dp[8], dz[8];
+  float* mine = at_expert[threadIdx.x];
+  float* theirs = at_expert[threadIdx.x - l];
+  float z[8], x[8], m, over, dp[8], dz[8];
   uint32_t key[8];
-  Picks picks;
   load_logits<T, VEC>(static_cast<const T*>(p.logits.p) + at * p.logits.ld, first, p.E, z);
-  const int top = p.idx[at * p.k];
-  if (p.dgate != nullptr) picks.load(p, at, 0);
+  const bool counts = p.idx[at * p.k] >= 0;
+  int e[8];
+  float g[8], d[8];
+  if (p.dgate != nullptr) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      if (q * L >= p.k) break;
+      const bool some = q * L + l < p.k;
+      const int64_t j = at * p.k + (some ? q * L + l : 0);
+      e[q] = some ? p.idx[j] : -1;
+      g[q] = p.renorm ? p.gate[j] : 1.f;
+      d[q] = p.dgate[j];
+    }
+  }
   float per_count = 0.f;
   if (p.dloss != nullptr) {
     const int used = p.used[0];
@@ -323,31 +372,28 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradParams p) {
     dp[i] = p.dloss != nullptr && first + i < p.E ? per_count * float(p.counts[first + i]) : 0.f;
     dz[i] = 0.f;
   }
-  const bool open = softmax8<L>(z, key, x, over) && top >= 0;
+  const bool open = softmax8<L>(z, counts, key, x, m, over);
   if (p.dgate != nullptr) {
     float along = 0.f;
     if (p.renorm) {
-      for (int j0 = 0; j0 < p.k; j0 += 8) {
-        if (j0 > 0) picks.load(p, at, j0);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) along += picks.e[j] >= 0 ? picks.gate[j] * picks.dgate[j] : 0.f;
+      for (int q = 0; q < 8; ++q) {
+        if (q * L >= p.k) break;
+        along += e[q] >= 0 ? g[q] * d[q] : 0.f;
       }
+      along = row_sum<L>(along);
     }
-    for (int j0 = 0; j0 < p.k; j0 += 8) {
-      if (p.k > 8) picks.load(p, at, j0);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int e = picks.e[j] - first;
-        const float d = p.renorm ? picks.gate[j] * (picks.dgate[j] - along) : picks.dgate[j];
+    for (int i = 0; i < 8; ++i) mine[i] = 0.f;
+    __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (p.renorm)
-            dz[i] += e == i ? d : 0.f;
-          else
-            dp[i] += e == i ? d : 0.f;
-        }
-      }
+    for (int q = 0; q < 8; ++q) {
+      if (q * L >= p.k) break;
+      if (e[q] >= 0 && e[q] < p.E) atomicAdd(theirs + e[q], g[q] * (d[q] - along));
     }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) (p.renorm ? dz[i] : dp[i]) += mine[i];
   }
   float along = 0.f;
 #pragma unroll
@@ -383,9 +429,12 @@ struct RouteGrid {
   int threads;
 };
 
+// One workgroup where its waves suffice: it needs no second launch to join the balance (512 x 16: 6.4 us;
+// 1024 x 16 in 16 workgroups and a join 7.3, in one workgroup of two steps 9.4).  Otherwise the rows spread
+// over all CUs, four waves a workgroup or more.
 RouteGrid route_grid(int64_t rows, int E) {
   const int64_t waves = (rows * row_lanes(E) + 63) / 64;
-  if (waves <= ONE) return {1, static_cast<int>(waves < 1 ? 64 : waves < 16 ? 64 * waves : kThreads)};
+  if (waves <= kThreads / 64) return {1, static_cast<int>(waves < 1 ? 64 : 64 * waves)};
   const int64_t each = (waves + kMostBlocks - 1) / kMostBlocks, most = each < 4 ? 4 : each < 16 ? each : 16;
   const int64_t blocks = (waves + most - 1) / most;
   return {static_cast<int>(blocks < kMostBlocks ? blocks : kMostBlocks), static_cast<int>(64 * most)};
@@ -446,9 +495,8 @@ hipError_t launch_route(const RouteParams& p, int dtype, void* ws, hipStream_t s
   const bool join = g.blocks > 1 && p.counts != nullptr;
   BalanceParts parts{};
   if (join) {
-    parts.prob = static_cast<float*>(ws);
-    parts.counts = reinterpret_cast<int32_t*>(parts.prob + g.blocks * kMaxExperts);
-    parts.used = parts.counts + g.blocks * kMaxExperts;
+    parts.experts = static_cast<uint2*>(ws);
+    parts.used = reinterpret_cast<int32_t*>(parts.experts + g.blocks * kMaxExperts);
   }
   const bool vec = vectors(p.logits.p, p.logits.ld, p.E, dtype);
   if (dtype == 1)
