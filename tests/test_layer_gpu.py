@@ -10,6 +10,8 @@ from weight_merge_amd import api as A
 
 DEV = "cuda"
 EPS = 1e-5
+# past the rows at which the backward pass sums rows and columns in one pass
+ONE_PASS = [(700, 24), (900, 136), (700, 264), (800, 520), (1300, 1032), (2100, 1536), (1200, 4096), (1700, 8192)]
 BOTH = pytest.mark.parametrize("dtype", ("fp32", "bf16"))
 # (rows, d): d from one block of eight to the widest, every way a row is shared among lanes, on and
 # off its edges; rows one, few, off the row groups, more than there are workgroups
@@ -99,7 +101,8 @@ def check_norm_backward(rows, d, dtype, kind, p=0.0, dhidden=True, weight=True, 
 
 @pytest.mark.gpu
 @BOTH
-@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("shape", SHAPES + [(2050, 264), (2051, 520), (2048, 1032), (2049, 1536)],
+                         ids=lambda s: "x".join(map(str, s)))
 def test_norm_shapes(shape, dtype):
     check_norm(*shape, dtype, "layer", seed=sum(shape))
     check_norm(*shape, dtype, "rms", p=0.2, seed=sum(shape) + 1)
@@ -107,7 +110,7 @@ def test_norm_shapes(shape, dtype):
 
 @pytest.mark.gpu
 @BOTH
-@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("shape", SHAPES + ONE_PASS, ids=lambda s: "x".join(map(str, s)))
 def test_norm_backward_shapes(shape, dtype):
     check_norm_backward(*shape, dtype, "rms", seed=sum(shape))
     check_norm_backward(*shape, dtype, "layer", p=0.2, seed=sum(shape) + 1)
@@ -125,8 +128,9 @@ def test_norm_operands_on_and_off(kind, p, dtype):
 
 @pytest.mark.gpu
 @BOTH
-def test_gradients_do_not_depend_on_which_are_asked_for(dtype):
-    n, t = made(5, 600, 264, dtype)
+@pytest.mark.parametrize("rows", (300, 900))
+def test_gradients_do_not_depend_on_which_are_asked_for(rows, dtype):
+    n, t = made(5, rows, 264, dtype)
     stats = [torch.tensor(v, dtype=torch.float32, device=DEV) for v in OL.norm(n["res"], None, None, "layer", EPS)[1:]]
     kw = dict(weight=t["w"], dhidden=t["dhidden"], p=0.1, seed=3)
     every = A.ada_norm_backward(t["dy"], t["res"], stats, want_dresidual=True, want_dbias=True, **kw)
@@ -155,6 +159,23 @@ def test_norm_in_place(dtype):
             c = {k: v.clone() for k, v in t.items()}
             got = A.ada_norm_backward(c["dy"], t["res"], stats, dhidden=c["dhidden"], dx=c[x], dresidual=c[r], **kw)
             assert all(torch.equal(a, b) for a, b in zip(got[:3], ref[:3]))
+
+
+@pytest.mark.gpu
+@BOTH
+@pytest.mark.parametrize("shape", [(512, 8192), (900, 264), (200, 16392)], ids=lambda s: "x".join(map(str, s)))
+def test_gradients_in_the_place_of_dy(shape, dtype):
+    """dw and db read dy too, whichever workgroup is the first to write there."""
+    n, t = made(12, *shape, dtype)
+    stats = [torch.tensor(v, dtype=torch.float32, device=DEV) for v in OL.norm(n["res"], None, None, "layer", EPS)[1:]]
+    kw = dict(weight=t["w"], dhidden=t["dhidden"], want_dbias=True)
+    ref = A.ada_norm_backward(t["dy"], t["res"], stats, **kw)
+    for rep in range(10):
+        for where in ("dx", "dresidual"):
+            dy = t["dy"].clone()
+            got = A.ada_norm_backward(dy, t["res"], stats, **{where: dy}, want_dx=where == "dx", **kw)
+            assert torch.equal(got[0 if where == "dx" else 1], ref[0])
+            assert torch.equal(got[2], ref[2]) and torch.equal(got[3], ref[3])
 
 
 @pytest.mark.gpu
@@ -373,6 +394,33 @@ def test_route_ties_closed_experts_and_padding(E, renorm, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype, E, k", (("fp32", 64, 3), ("bf16", 7, 2)))
+def test_route_of_many_rows(dtype, E, k):
+    """More rows than the workgroups take in one step."""
+    rows = {64: 36000, 7: 280000}[E]
+    z = H.logits(5, rows, E, dtype, ties=dtype == "bf16").to(DEV)
+    valid = torch.arange(rows, device=DEV) % 7 != 2
+    got = A.ada_route(z, k, valid=valid)
+    order = torch.sort(z.float(), dim=1, descending=True, stable=True).indices[:, :k]
+    idx = torch.where(valid[:, None], order, -1)
+    assert torch.equal(got.idx.long(), idx) and int(got.used) == int(valid.sum())
+    counts = torch.bincount(idx[valid].flatten(), minlength=E)
+    assert torch.equal(got.counts.long(), counts)
+    p = torch.softmax(z.double(), 1)
+    rel = torch.from_numpy(H.probability_bound(H.f64(z))).to(DEV)
+    mean = p[valid].mean(0)
+    # sums of at most 16 steps of 64 rows on a lane and of 256 workgroups
+    eprob = (rel * p)[valid].mean(0) + (16 + H.DEPTH + 256) * H.U * mean
+    H.assert_within(got.prob, H.f64(mean), H.f64(eprob), "prob")
+    share = counts.double() / (k * valid.sum())
+    loss = E * (share * mean).sum()
+    H.assert_within(got.loss, H.f64(loss[None]), H.f64((E * (share * eprob).sum() + 4 * H.U * loss)[None]), "loss")
+    picked = torch.gather(p, 1, order)
+    ref = torch.where(valid[:, None], picked / picked.sum(1, keepdim=True), 0.0)
+    H.assert_within(got.gate, H.f64(ref), H.f64(rel * ref + H.TINY), "gate")
+
+
+@pytest.mark.gpu
 def test_route_of_nothing():
     z = torch.zeros((4, 8), device=DEV)
     none = torch.zeros(4, dtype=torch.bool, device=DEV)
@@ -540,6 +588,38 @@ def test_inputs_dropped_behind_the_call(dtype):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, ref))
         del others
+
+
+@pytest.mark.gpu
+@BOTH
+def test_calls_on_two_streams_at_once(dtype):
+    _, t = made(13, 1500, 1032, dtype)
+    state = torch.tensor([3, 4], dtype=torch.int64, device=DEV)
+    refs = [training_step(t, state, offset) for offset in (0, 50)]
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for rep in range(5):
+        got = []
+        for side, offset in zip(sides, (0, 50)):
+            with torch.cuda.stream(side):
+                got.append(training_step(t, state, offset))
+        torch.cuda.synchronize()
+        for a, b in zip(got, refs):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.gpu
+def test_another_device_is_refused(monkeypatch):
+    x = torch.zeros((4, 64), device=DEV)
+    z = torch.zeros((4, 8), device=DEV)
+    out = A.ada_route(z, 2)
+    monkeypatch.setattr(A, "_device_now", lambda: 1)
+    stats = (x[:, 0].contiguous(), x[:, 0].contiguous())
+    for call in (lambda: A.ada_norm(x), lambda: A.ada_norm_backward(x, x, stats), lambda: A.ada_dropout(x, 0.1, 1),
+                 lambda: A.ada_dropout_backward(x, 0.1, 1), lambda: A.ada_route(z, 2),
+                 lambda: A.ada_route_backward(z, out, dloss=out.loss)):
+        with pytest.raises(ValueError, match="is current"):
+            call()
 
 
 @pytest.mark.gpu

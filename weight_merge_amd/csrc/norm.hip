@@ -521,9 +521,8 @@ hipError_t forward(const NormParams& p, hipStream_t s) {
 }
 
 template <typename T, int CH, bool DROP>
-hipError_t rows_apart(const NormGradParams& p, const RowShape& r, hipStream_t s) {
-  const int64_t sets = p.dx.p == nullptr && p.dres.p == nullptr ? 0 : (p.rows + r.groups - 1) / r.groups;
-  const int stripes = p.dw == nullptr && p.db == nullptr ? 0 : (p.d + kStripe - 1) / kStripe;
+hipError_t launch_apart(const NormGradParams& p, const RowShape& r, int stripes, int64_t sets, hipStream_t s) {
+  if (stripes + sets == 0) return hipSuccess;
   const dim3 grid(static_cast<unsigned>(stripes + sets)), block(r.lanes * r.groups);
   if (r.lanes > 64)
     hipLaunchKernelGGL((norm_apart_kernel<T, CH, false, true, DROP>), grid, block, 0, s, p, r.lanes, stripes);
@@ -532,6 +531,17 @@ hipError_t rows_apart(const NormGradParams& p, const RowShape& r, hipStream_t s)
   else
     hipLaunchKernelGGL((norm_apart_kernel<T, 1, true, false, DROP>), grid, block, 0, s, p, r.lanes, stripes);
   return hipGetLastError();
+}
+
+template <typename T, int CH, bool DROP>
+hipError_t rows_apart(const NormGradParams& p, const RowShape& r, hipStream_t s) {
+  const int64_t sets = p.dx.p == nullptr && p.dres.p == nullptr ? 0 : (p.rows + r.groups - 1) / r.groups;
+  const int stripes = p.dw == nullptr && p.db == nullptr ? 0 : (p.d + kStripe - 1) / kStripe;
+  // the columns' workgroups read dy: where a gradient takes its place, they go first
+  const bool over_dy = p.dy.p != nullptr && (p.dx.p == p.dy.p || p.dres.p == p.dy.p);
+  if (!over_dy) return launch_apart<T, CH, DROP>(p, r, stripes, sets, s);
+  const hipError_t e = launch_apart<T, CH, DROP>(p, r, stripes, 0, s);
+  return e == hipSuccess ? launch_apart<T, CH, DROP>(p, r, 0, sets, s) : e;
 }
 
 template <typename T, bool DROP>
