@@ -10,7 +10,7 @@ from oracle import layer as OL
 from weight_merge_amd import _lib
 from weight_merge_amd import api as A
 from weight_merge_amd._lib import (ADA_BF16, ADA_EALIGN, ADA_EDTYPE, ADA_EHIP, ADA_EINVAL, ADA_ESHAPE, ADA_F32,
-                                   ADA_NORM_RMS, AdaDrop, AdaDropoutArgs, AdaDropoutGradArgs, AdaNormArgs,
+                                   ADA_NORM_RMS, AdaDropoutArgs, AdaDropoutGradArgs, AdaNormArgs,
                                    AdaNormGradArgs, AdaRouteArgs, AdaRouteGradArgs)
 
 no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="passes fake pointers: runs where no GPU is visible")
@@ -52,15 +52,14 @@ ROUTE = [n for n in SETS if n.startswith("route")]
 
 def call(name, dt=ADA_BF16, ws=64 * MB, ws_bytes=1 << 30, p=0.1, state=None, **kw):
     cls, good = SETS[name]
-    args = cls(**dict(good, **kw))
-    if name in LAYER:
-        args.drop = AdaDrop(p, 1, 2, state)
+    drop = dict(p=p, seed=1, offset=2, state=state) if name in LAYER else {}
+    args = cls(**dict(good, **drop, **kw))
     space = (ws, ws_bytes) if name in ("norm_backward", "route") else ()
     return getattr(_lib.load(), f"ada_{name}")(args, dt, *space, None)
 
 
 def pointers(name):
-    return [f for f, t in SETS[name][0]._fields_ if t is _lib.c_void_p]
+    return [f for f, t in SETS[name][0]._fields_ if t is _lib.c_void_p and f != "state"]
 
 
 def strides(name):

@@ -86,15 +86,15 @@ class AdaGluGradArgs(ctypes.Structure):
     )
 
 
-class AdaDrop(ctypes.Structure):
-    _fields_ = [("p", ctypes.c_double), ("seed", c_uint64), ("offset", c_uint64), ("state", c_void_p)]
+# ada_drop, the last member of the calls' structures
+_DROP = [("p", ctypes.c_double), ("seed", c_uint64), ("offset", c_uint64), ("state", c_void_p)]
 
 
 class AdaDropoutArgs(ctypes.Structure):
     _fields_ = (
         [(n, c_void_p) for n in ("x", "residual", "y")]
         + [(n, c_int64) for n in ("ld_x", "ld_res", "ld_y", "rows")]
-        + [("d", c_int32), ("drop", AdaDrop)]
+        + [("d", c_int32)] + _DROP
     )
 
 
@@ -102,7 +102,7 @@ class AdaDropoutGradArgs(ctypes.Structure):
     _fields_ = (
         [(n, c_void_p) for n in ("dy", "dx")]
         + [(n, c_int64) for n in ("ld_dy", "ld_dx", "rows")]
-        + [("d", c_int32), ("drop", AdaDrop)]
+        + [("d", c_int32)] + _DROP
     )
 
 
@@ -110,7 +110,7 @@ class AdaNormArgs(ctypes.Structure):
     _fields_ = (
         [(n, c_void_p) for n in ("x", "residual", "weight", "bias", "y", "hidden", "mean", "rstd")]
         + [(n, c_int64) for n in ("ld_x", "ld_res", "ld_y", "ld_hidden", "rows")]
-        + [("d", c_int32), ("kind", c_int32), ("eps", c_float), ("drop", AdaDrop)]
+        + [("d", c_int32), ("kind", c_int32), ("eps", c_float)] + _DROP
     )
 
 
@@ -118,7 +118,7 @@ class AdaNormGradArgs(ctypes.Structure):
     _fields_ = (
         [(n, c_void_p) for n in ("dy", "hidden", "dhidden", "weight", "mean", "rstd", "dx", "dresidual", "dweight", "dbias")]
         + [(n, c_int64) for n in ("ld_dy", "ld_hidden", "ld_dhidden", "ld_dx", "ld_dresidual", "rows")]
-        + [("d", c_int32), ("kind", c_int32), ("drop", AdaDrop)]
+        + [("d", c_int32), ("kind", c_int32)] + _DROP
     )
 
 

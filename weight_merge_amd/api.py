@@ -14,7 +14,7 @@ from typing import NamedTuple
 import torch
 
 from . import _lib
-from ._lib import (ADA_BF16, ADA_F32, AdaDrop, AdaDropoutArgs, AdaDropoutGradArgs, AdaGemvProj, AdaGluArgs,
+from ._lib import (ADA_BF16, ADA_F32, AdaDropoutArgs, AdaDropoutGradArgs, AdaGemvProj, AdaGluArgs,
                    AdaGluGradArgs, AdaLinearArgs, AdaLinearGradArgs, AdaLoraProj, AdaNormArgs, AdaNormGradArgs, AdaProj,
                    AdaRouteArgs, AdaRouteGradArgs)
 
@@ -629,7 +629,6 @@ def ada_glu_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_
 # ---- norms, dropout, and the router for many rows ------------------------------------
 _NORMS = {"layer": 0, "rms": 1}
 _M64 = (1 << 64) - 1
-_NO_DROP = AdaDrop()  # p = 0
 
 
 def _kind(kind: str) -> int:
@@ -639,25 +638,33 @@ def _kind(kind: str) -> int:
         raise ValueError(f"unknown norm {kind!r}; expected one of {', '.join(_NORMS)}") from None
 
 
-def _drop(p: float, seed, offset: int, dev: int) -> AdaDrop:
+def _drop(p: float, seed, offset: int, dev: int):
     """The C call's dropout; a seed that is a tensor is the generator's state on the device."""
     if seed is None:
         if p != 0:
             raise ValueError("dropout needs a seed")
-        return _NO_DROP
+        return 0.0, 0, 0, None
     if not isinstance(seed, torch.Tensor):
-        return AdaDrop(p, seed & _M64, offset & _M64, None)
+        return p, seed & _M64, offset & _M64, None
     if seed.dtype is not torch.int64 or seed.shape != (2,) or seed.stride(0) != 1:
         raise TypeError("a seed on the device must be int64 [2]: the seed and the offset's start")
     if seed.get_device() != dev:
         raise ValueError(f"seed is on {seed.device}, not with the other tensors")
-    return AdaDrop(p, 0, offset & _M64, seed.data_ptr())
+    return p, 0, offset & _M64, seed.data_ptr()
 
 
-def _matrix(x: torch.Tensor, name: str):
-    if x.dim() != 2:
+def _shape(x: torch.Tensor, name: str):
+    s = x.shape
+    if len(s) != 2:
         raise ValueError(f"{name} must be [rows, d]")
-    return x.shape
+    return s
+
+
+def _like(t, shape, dt, dev: int, name: str):
+    """Pointer and row stride of a matrix of this shape (as _mat, which it leaves the rest to)."""
+    if t is not None and t.shape == shape and t.dtype is dt and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr(), shape[1]
+    return _mat(t, shape[0], shape[1], dt, dev, name)
 
 
 def ada_dropout(x: torch.Tensor, p: float, seed, offset: int = 0, residual=None, y=None, stream=None):
@@ -670,18 +677,19 @@ def ada_dropout(x: torch.Tensor, p: float, seed, offset: int = 0, residual=None,
     anew whenever that tensor changes.  `stream` as in ada_linear."""
     if stream is not None:
         return _on(stream, ada_dropout, x, p, seed, offset, residual, y)
-    rows, d = _matrix(x, "x")
+    shape = _shape(x, "x")
+    rows, d = shape
     dc, dt, dev = _dtype(x), x.dtype, x.get_device()
-    px, ldx = _mat(x, rows, d, dt, dev, "x")
-    pr, ldr = _mat(residual, rows, d, dt, dev, "residual")
+    px, ldx = _like(x, shape, dt, dev, "x")
+    pr, ldr = _like(residual, shape, dt, dev, "residual")
     if y is not None:
-        py, ldy = _mat(y, rows, d, dt, dev, "y")
+        py, ldy = _like(y, shape, dt, dev, "y")
     drop = _drop(p, seed, offset, dev)
     _current(dev)
     if y is None:
         y = torch.empty((rows, d), dtype=dt, device=x.device)
         py, ldy = y.data_ptr(), d
-    args = AdaDropoutArgs(px, pr, py, ldx, ldr, ldy, rows, d, drop)
+    args = AdaDropoutArgs(px, pr, py, ldx, ldr, ldy, rows, d, *drop)
     _check(_lib.load().ada_dropout(args, dc, _raw_stream(dev)), "ada_dropout")
     return y
 
@@ -691,17 +699,18 @@ def ada_dropout_backward(dy: torch.Tensor, p: float, seed, offset: int = 0, dx=N
     the residual is dy."""
     if stream is not None:
         return _on(stream, ada_dropout_backward, dy, p, seed, offset, dx)
-    rows, d = _matrix(dy, "dy")
+    shape = _shape(dy, "dy")
+    rows, d = shape
     dc, dt, dev = _dtype(dy), dy.dtype, dy.get_device()
-    pdy, lddy = _mat(dy, rows, d, dt, dev, "dy")
+    pdy, lddy = _like(dy, shape, dt, dev, "dy")
     if dx is not None:
-        pdx, lddx = _mat(dx, rows, d, dt, dev, "dx")
+        pdx, lddx = _like(dx, shape, dt, dev, "dx")
     drop = _drop(p, seed, offset, dev)
     _current(dev)
     if dx is None:
         dx = torch.empty((rows, d), dtype=dt, device=dy.device)
         pdx, lddx = dx.data_ptr(), d
-    args = AdaDropoutGradArgs(pdy, pdx, lddy, lddx, rows, d, drop)
+    args = AdaDropoutGradArgs(pdy, pdx, lddy, lddx, rows, d, *drop)
     _check(_lib.load().ada_dropout_backward(args, dc, _raw_stream(dev)), "ada_dropout_backward")
     return dx
 
@@ -716,24 +725,25 @@ def ada_norm(x: torch.Tensor, weight=None, bias=None, residual=None, kind: str =
     x or the residual itself.  p, seed and offset as in ada_dropout, `stream` as in ada_linear."""
     if stream is not None:
         return _on(stream, ada_norm, x, weight, bias, residual, kind, eps, p, seed, offset, y, hidden, stats)
-    rows, d = _matrix(x, "x")
+    shape = _shape(x, "x")
+    rows, d = shape
     code, dc, dt, dev = _kind(kind), _dtype(x), x.dtype, x.get_device()
-    px, ldx = _mat(x, rows, d, dt, dev, "x")
-    pr, ldr = _mat(residual, rows, d, dt, dev, "residual")
+    px, ldx = _like(x, shape, dt, dev, "x")
+    pr, ldr = _like(residual, shape, dt, dev, "residual")
     pw = _vec(weight, d, dt, dev, "weight")
     pb = _vec(bias, d, dt, dev, "bias")
-    ph, ldh = _mat(hidden, rows, d, dt, dev, "hidden")
+    ph, ldh = _like(hidden, shape, dt, dev, "hidden")
     mean, rstd = stats if stats is not None else (None, None)
     pm = _vec(mean, rows, torch.float32, dev, "mean")
     ps = _vec(rstd, rows, torch.float32, dev, "rstd")
     if y is not None:
-        py, ldy = _mat(y, rows, d, dt, dev, "y")
+        py, ldy = _like(y, shape, dt, dev, "y")
     drop = _drop(p, seed, offset, dev)
     _current(dev)
     if y is None:
         y = torch.empty((rows, d), dtype=dt, device=x.device)
         py, ldy = y.data_ptr(), d
-    args = AdaNormArgs(px, pr, pw, pb, py, ph, pm, ps, ldx, ldr, ldy, ldh, rows, d, code, eps, drop)
+    args = AdaNormArgs(px, pr, pw, pb, py, ph, pm, ps, ldx, ldr, ldy, ldh, rows, d, code, eps, *drop)
     _check(_lib.load().ada_norm(args, dc, _raw_stream(dev)), "ada_norm")
     return y
 
@@ -756,19 +766,20 @@ def ada_norm_backward(dy: torch.Tensor, hidden: torch.Tensor, stats, weight=None
     if stream is not None:
         return _on(stream, ada_norm_backward, dy, hidden, stats, weight, dhidden, kind, p, seed, offset, dx, dresidual,
                    dweight, dbias, want_dx, want_dresidual, want_dweight, want_dbias, workspace)
-    rows, d = _matrix(dy, "dy")
+    shape = _shape(dy, "dy")
+    rows, d = shape
     code, dc, dt, dev = _kind(kind), _dtype(dy), dy.dtype, dy.get_device()
     mean, rstd = stats
     if rstd is None or (mean is None and code == 0):
         raise ValueError("stats must hold what ada_norm saved: rstd, and mean unless the norm is rms")
-    pdy, lddy = _mat(dy, rows, d, dt, dev, "dy")
-    ph, ldh = _mat(hidden, rows, d, dt, dev, "hidden")
-    pdh, lddh = _mat(dhidden, rows, d, dt, dev, "dhidden")
+    pdy, lddy = _like(dy, shape, dt, dev, "dy")
+    ph, ldh = _like(hidden, shape, dt, dev, "hidden")
+    pdh, lddh = _like(dhidden, shape, dt, dev, "dhidden")
     pw = _vec(weight, d, dt, dev, "weight")
     pm = _vec(mean, rows, torch.float32, dev, "mean")
     ps = _vec(rstd, rows, torch.float32, dev, "rstd")
-    pdx, lddx = _mat(dx, rows, d, dt, dev, "dx")
-    pdr, lddr = _mat(dresidual, rows, d, dt, dev, "dresidual")
+    pdx, lddx = _like(dx, shape, dt, dev, "dx")
+    pdr, lddr = _like(dresidual, shape, dt, dev, "dresidual")
     pdw = _vec(dweight, d, dt, dev, "dweight")
     pdb = _vec(dbias, d, dt, dev, "dbias")
     drop = _drop(p, seed, offset, dev)
@@ -787,7 +798,7 @@ def ada_norm_backward(dy: torch.Tensor, hidden: torch.Tensor, stats, weight=None
         pdb = dbias.data_ptr()
     ws, nbytes, _keep = _workspace(_workspace_bytes("ada_norm_backward_workspace", rows, d, dc), workspace, dev)
     args = AdaNormGradArgs(pdy, ph, pdh, pw, pm, ps, pdx, pdr, pdw, pdb, lddy, ldh, lddh, lddx, lddr, rows, d, code,
-                           drop)
+                           *drop)
     _check(_lib.load().ada_norm_backward(args, dc, ws, nbytes, _raw_stream(dev)), "ada_norm_backward")
     return dx, dresidual, dweight, dbias
 
@@ -835,7 +846,7 @@ def ada_route(logits: torch.Tensor, k: int, renorm: bool = True, valid=None, bal
     index -1 and gate 0.  `out` is a Routing (or six tensors) to write to; `stream` as in ada_linear."""
     if stream is not None:
         return _on(stream, ada_route, logits, k, renorm, valid, balance, out, workspace)
-    rows, E = _matrix(logits, "logits")
+    rows, E = _shape(logits, "logits")
     dc, dev = _dtype(logits), logits.get_device()
     pl, ld = _logits(logits, rows, E, logits.dtype, dev, "logits")
     pv = None
@@ -875,7 +886,7 @@ def ada_route_backward(logits: torch.Tensor, out, dgate=None, dloss=None, renorm
     are constants."""
     if stream is not None:
         return _on(stream, ada_route_backward, logits, out, dgate, dloss, renorm, dlogits)
-    rows, E = _matrix(logits, "logits")
+    rows, E = _shape(logits, "logits")
     dc, dt, dev = _dtype(logits), logits.dtype, logits.get_device()
     idx, gate, counts, _, _, used = out
     i32, f32 = torch.int32, torch.float32
