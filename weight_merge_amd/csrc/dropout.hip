@@ -11,10 +11,7 @@
 namespace ada {
 namespace {
 
-#ifndef ADA_DROPOUT_BLOCKS
-#define ADA_DROPOUT_BLOCKS 4
-#endif
-constexpr int kBlocks = ADA_DROPOUT_BLOCKS;
+constexpr int kBlocks = 4;
 constexpr int kThreads = 256;
 
 // Where block g of a matrix with row stride ld begins.  DENSE: rows follow each other.
@@ -29,7 +26,7 @@ __device__ __forceinline__ int64_t block_at(uint64_t g, uint32_t per_row, uint64
 }
 
 // y may be x or the residual: a block's elements are read and written by one lane, reads first.
-template <typename T, bool DENSE, bool RES>
+template <typename T, bool DENSE, bool RES, bool STREAM>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(DropoutParams p, uint64_t blocks, uint32_t per_row,
                                                            uint64_t inv) {
   const uint64_t g0 = uint64_t(blockIdx.x) * (kThreads * kBlocks) + threadIdx.x;
@@ -42,8 +39,8 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(DropoutParams p, uint
   for (int u = 0; u < kBlocks; ++u) {
     const uint64_t g = g0 + u * kThreads;
     if (g >= blocks) continue;
-    in[u] = load_eight<true>(x + block_at<DENSE>(g, per_row, inv, p.x.ld));
-    if constexpr (RES) add[u] = load_eight<true>(res + block_at<DENSE>(g, per_row, inv, p.res.ld));
+    in[u] = load_eight<STREAM>(x + block_at<DENSE>(g, per_row, inv, p.x.ld));
+    if constexpr (RES) add[u] = load_eight<STREAM>(res + block_at<DENSE>(g, per_row, inv, p.res.ld));
   }
 #pragma unroll
   for (int u = 0; u < kBlocks; ++u) {
@@ -58,11 +55,11 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(DropoutParams p, uint
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] += r[i];
     }
-    store_eight<true>(y + block_at<DENSE>(g, per_row, inv, p.y.ld), f);
+    store_eight(y + block_at<DENSE>(g, per_row, inv, p.y.ld), f);
   }
 }
 
-template <typename T, bool RES>
+template <typename T, bool RES, bool STREAM>
 hipError_t launch(const DropoutParams& p, hipStream_t s) {
   const uint32_t per_row = uint32_t(p.d / 8);
   const uint64_t blocks = uint64_t(p.rows) * per_row;
@@ -71,9 +68,9 @@ hipError_t launch(const DropoutParams& p, hipStream_t s) {
   // at most 2^32 blocks: 2^22 workgroups
   const dim3 grid(static_cast<unsigned>((blocks + kThreads * kBlocks - 1) / (kThreads * kBlocks)));
   if (dense)
-    hipLaunchKernelGGL((dropout_kernel<T, true, RES>), grid, dim3(kThreads), 0, s, p, blocks, per_row, inv);
+    hipLaunchKernelGGL((dropout_kernel<T, true, RES, STREAM>), grid, dim3(kThreads), 0, s, p, blocks, per_row, inv);
   else
-    hipLaunchKernelGGL((dropout_kernel<T, false, RES>), grid, dim3(kThreads), 0, s, p, blocks, per_row, inv);
+    hipLaunchKernelGGL((dropout_kernel<T, false, RES, STREAM>), grid, dim3(kThreads), 0, s, p, blocks, per_row, inv);
   return hipGetLastError();
 }
 
@@ -82,8 +79,9 @@ hipError_t launch(const DropoutParams& p, hipStream_t s) {
 hipError_t launch_dropout(const DropoutParams& p, int dtype, hipStream_t s) {
   if (p.rows == 0) return hipSuccess;
   const bool res = p.res.p != nullptr;
-  if (dtype == 1) return res ? launch<uint16_t, true>(p, s) : launch<uint16_t, false>(p, s);
-  return res ? launch<float, true>(p, s) : launch<float, false>(p, s);
+  if (dtype != 1) return res ? launch<float, true, false>(p, s) : launch<float, false, false>(p, s);
+  if (streams(p.rows * p.d, dtype)) return res ? launch<uint16_t, true, true>(p, s) : launch<uint16_t, false, true>(p, s);
+  return res ? launch<uint16_t, true, false>(p, s) : launch<uint16_t, false, false>(p, s);
 }
 
 }  // namespace ada

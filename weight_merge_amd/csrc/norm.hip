@@ -55,7 +55,7 @@ __device__ __forceinline__ void row_totals(float (&v)[N], int lanes, float (*slo
 // first sum's mean, and that sum's rounding is taken out of both with the mean of h - m
 // (Chan, Golub, LeVeque, "Algorithms for computing the sample variance", 1983), so rows far from
 // zero keep their accuracy.  y and hidden may be x or the residual: a lane reads what it writes.
-template <typename T, int CH>
+template <typename T, int CH, bool STREAM>
 struct NormRow {
   Eight<T> x[CH], res[CH];
 
@@ -68,14 +68,14 @@ struct NormRow {
       zero_eight(x[c]);
       zero_eight(res[c]);
       if (row < p.rows && g < per_row) {
-        x[c] = load_eight<true>(px + g * 8);
-        if (p.res.p != nullptr) res[c] = load_eight<true>(pr + g * 8);
+        x[c] = load_eight<STREAM>(px + g * 8);
+        if (p.res.p != nullptr) res[c] = load_eight<STREAM>(pr + g * 8);
       }
     }
   }
 };
 
-template <typename T, int CH, bool SUB, bool WIDE, bool DROP>
+template <typename T, int CH, bool SUB, bool WIDE, bool DROP, bool STREAM>
 __global__ void __launch_bounds__(1024) norm_kernel(NormParams p, int lanes) {
   __shared__ float mean_slot[kMaxWaves][1];
   __shared__ float square_slot[kMaxWaves][2];
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p, int lanes) {
   DropKey key{};
   if constexpr (DROP) key = drop_key(p.drop);
 
-  NormRow<T, CH> now;
+  NormRow<T, CH, STREAM> now;
   const int64_t step = int64_t(gridDim.x) * groups;
   int64_t row = int64_t(blockIdx.x) * groups + group;
   now.load(p, row, lane, lanes, per_row);
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p, int lanes) {
       for (int c = 0; c < CH; ++c) {
         const int g = lane + c * lanes;
         if (g >= per_row) continue;
-        if (p.hidden.p != nullptr) store_eight<true>(hidden + g * 8, h[c]);
+        if (p.hidden.p != nullptr) store_eight<STREAM>(hidden + g * 8, h[c]);
         float out[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) out[i] = (h[c][i] - mean - rest) * rstd;
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p, int lanes) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) out[i] += v[i];
         }
-        store_eight<true>(y + g * 8, out);
+        store_eight(y + g * 8, out);
       }
       if (lane == 0) {
         if (p.mean != nullptr) p.mean[row] = mean + rest;
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p, int lanes) {
 
 // ---- backward --------------------------------------------------------------------------
 // Eight columns of a row's operands.
-template <typename T>
+template <typename T, bool STREAM>
 struct GradBlock {
   Eight<T> dy, h, add;
 
@@ -177,17 +177,17 @@ struct GradBlock {
     zero_eight(h);
     zero_eight(add);
     if (!live) return;
-    dy = load_eight<true>(static_cast<const T*>(p.dy.p) + row * p.dy.ld + g * 8);
-    h = load_eight<true>(static_cast<const T*>(p.hidden.p) + row * p.hidden.ld + g * 8);
+    dy = load_eight<STREAM>(static_cast<const T*>(p.dy.p) + row * p.dy.ld + g * 8);
+    h = load_eight<STREAM>(static_cast<const T*>(p.hidden.p) + row * p.hidden.ld + g * 8);
     if (p.dhidden.p != nullptr)
-      add = load_eight<true>(static_cast<const T*>(p.dhidden.p) + row * p.dhidden.ld + g * 8);
+      add = load_eight<STREAM>(static_cast<const T*>(p.dhidden.p) + row * p.dhidden.ld + g * 8);
   }
 };
 
 // A lane's part of a row; a row past the end adds zeros.
-template <typename T, int CH>
+template <typename T, int CH, bool STREAM>
 struct GradRow {
-  GradBlock<T> c[CH];
+  GradBlock<T, STREAM> c[CH];
   float mean, rstd;
 
   __device__ __forceinline__ void load(const NormGradParams& p, int64_t row, int lane, int lanes, int per_row) {
@@ -213,13 +213,13 @@ struct GradRow {
 };
 
 // What a row's gradient goes to; dx and dres may be dy or dhidden: a lane has read what it writes.
-template <typename T, bool DROP>
+template <typename T, bool DROP, bool STREAM, bool STREAM_DX>
 __device__ __forceinline__ void store_gradient(const NormGradParams& p, int64_t row, int g, const DropKey& key,
                                                float (&dh)[8]) {
-  if (p.dres.p != nullptr) store_eight<true>(static_cast<T*>(p.dres.p) + row * p.dres.ld + g * 8, dh);
+  if (p.dres.p != nullptr) store_eight<STREAM>(static_cast<T*>(p.dres.p) + row * p.dres.ld + g * 8, dh);
   if (p.dx.p == nullptr) return;
   if constexpr (DROP) drop_eight(dh, uint32_t(row * (p.d >> 3) + g), key, p.drop.least, p.drop.scale);
-  store_eight<true>(static_cast<T*>(p.dx.p) + row * p.dx.ld + g * 8, dh);
+  store_eight<STREAM_DX>(static_cast<T*>(p.dx.p) + row * p.dx.ld + g * 8, dh);
 }
 
 template <typename T>
@@ -236,7 +236,7 @@ __device__ __forceinline__ void load_weight(const void* w, int g, bool live, flo
 // gridDim.x-th set of rows, keeps the sums dw and db of a lane's eight columns in registers over all
 // of them, and writes them once: part[0][block][d] and part[1][block][d], which norm_join_kernel
 // adds up in a fixed order.  The next row's loads are in flight while this one is summed.
-template <typename T, bool SUB, bool WIDE, bool DROP>
+template <typename T, bool SUB, bool WIDE, bool DROP, bool STREAM>
 __global__ void __launch_bounds__(1024) norm_grad_kernel(NormGradParams p, int lanes, float* part) {
   __shared__ float slot[2][kMaxWaves][2];
   __shared__ f32x4 meet[2 * kGradThreads];  // where the groups of a workgroup meet
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(NormGradParams p, int l
   zero_eight(weight);
   if (p.w != nullptr && inside) weight = load_eight(static_cast<const T*>(p.w) + lane * 8);
 
-  const auto take = [&](const GradRow<T, 1>& now, int64_t row, float (*totals)[2]) {
+  const auto take = [&](const GradRow<T, 1, STREAM>& now, int64_t row, float (*totals)[2]) {
     float sums[2] = {0.f, 0.f}, dy[8], h[8], w[8];
     unpack(weight, w);
     if (p.w == nullptr) {
@@ -271,10 +271,10 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(NormGradParams p, int l
     row_totals<2, SUB, WIDE>(sums, lanes, totals);
     if (row < p.rows && inside) {
       now.gradient(0, w, p.mean != nullptr ? sums[0] * over : 0.f, sums[1] * over, h);
-      store_gradient<T, DROP>(p, row, lane, key, h);
+      store_gradient<T, DROP, STREAM, false>(p, row, lane, key, h);
     }
   };
-  GradRow<T, 1> now, next;
+  GradRow<T, 1, STREAM> now, next;
   const int64_t step = int64_t(gridDim.x) * groups;
   int64_t row = int64_t(blockIdx.x) * groups + group;
   now.load(p, row, lane, lanes, per_row);
@@ -310,9 +310,10 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(NormGradParams p, int l
 // given.  The first `stripes` workgroups sum 64 columns each over all rows, eight columns a lane, the
 // rows dealt to sets of eight lanes; the others take a set of rows each.  dy and h are read twice,
 // but there are no partial sums to write and join, so few rows need one launch; and a row is only
-// held until it is summed, so wide ones fit the registers.
+// held until it is summed, so wide ones fit the registers.  Large calls stream dx too: what stays in the
+// caches is dy and h for their second reading (1170 x 28672: 98 us, with dx kept 111).
 constexpr int kStripe = 64;
-template <typename T, int CH, bool SUB, bool WIDE, bool DROP>
+template <typename T, int CH, bool SUB, bool WIDE, bool DROP, bool STREAM>
 __global__ void __launch_bounds__(1024) norm_apart_kernel(NormGradParams p, int lanes, int stripes) {
   const int per_row = p.d >> 3;
   if (int(blockIdx.x) < stripes) {
@@ -383,7 +384,7 @@ __global__ void __launch_bounds__(1024) norm_apart_kernel(NormGradParams p, int 
   DropKey key{};
   if constexpr (DROP) key = drop_key(p.drop);
   const int64_t row = int64_t(blockIdx.x - stripes) * groups + group;
-  GradRow<T, CH> now;
+  GradRow<T, CH, STREAM> now;
   now.load(p, row, lane, lanes, per_row);
   float sums[2] = {0.f, 0.f};
 #pragma unroll
@@ -410,7 +411,7 @@ __global__ void __launch_bounds__(1024) norm_apart_kernel(NormGradParams p, int 
     float w[8], dh[8];
     load_weight<T>(p.w, g, true, w);
     now.gradient(c, w, c1, c2, dh);
-    store_gradient<T, DROP>(p, row, g, key, dh);
+    store_gradient<T, DROP, STREAM, STREAM>(p, row, g, key, dh);
   }
 }
 
@@ -497,70 +498,70 @@ int norm_grad_blocks(int64_t rows, int d) {
   return static_cast<int>(sets < kGradBlocks ? sets : kGradBlocks);
 }
 
-template <typename T, int CH, bool DROP>
+template <typename T, int CH, bool DROP, bool STREAM>
 hipError_t forward(const NormParams& p, const RowShape& r, hipStream_t s) {
   const int64_t sets = (p.rows + r.groups - 1) / r.groups, most = 1 << 20;
   const dim3 grid(static_cast<unsigned>(sets < most ? sets : most)), block(r.lanes * r.groups);
   // three blocks a lane are a wave's only, four a wide row's
   if (r.lanes < 64)
-    hipLaunchKernelGGL((norm_kernel<T, 1, true, false, DROP>), grid, block, 0, s, p, r.lanes);
+    hipLaunchKernelGGL((norm_kernel<T, 1, true, false, DROP, STREAM>), grid, block, 0, s, p, r.lanes);
   else if (CH < 4 && r.lanes == 64)
-    hipLaunchKernelGGL((norm_kernel<T, CH < 4 ? CH : 1, false, false, DROP>), grid, block, 0, s, p, r.lanes);
+    hipLaunchKernelGGL((norm_kernel<T, CH < 4 ? CH : 1, false, false, DROP, STREAM>), grid, block, 0, s, p, r.lanes);
   else
-    hipLaunchKernelGGL((norm_kernel<T, CH != 3 ? CH : 1, false, true, DROP>), grid, block, 0, s, p, r.lanes);
+    hipLaunchKernelGGL((norm_kernel<T, CH != 3 ? CH : 1, false, true, DROP, STREAM>), grid, block, 0, s, p, r.lanes);
   return hipGetLastError();
 }
 
-template <typename T, bool DROP>
+template <typename T, bool DROP, bool STREAM>
 hipError_t forward(const NormParams& p, hipStream_t s) {
   const RowShape r = forward_shape(p.rows, p.d);
-  if (r.chunks == 1) return forward<T, 1, DROP>(p, r, s);
-  if (r.chunks == 2) return forward<T, 2, DROP>(p, r, s);
-  if (r.chunks == 3) return forward<T, 3, DROP>(p, r, s);
-  return forward<T, 4, DROP>(p, r, s);
+  if (r.chunks == 1) return forward<T, 1, DROP, STREAM>(p, r, s);
+  if (r.chunks == 2) return forward<T, 2, DROP, STREAM>(p, r, s);
+  if (r.chunks == 3) return forward<T, 3, DROP, STREAM>(p, r, s);
+  return forward<T, 4, DROP, STREAM>(p, r, s);
 }
 
-template <typename T, int CH, bool DROP>
+template <typename T, int CH, bool DROP, bool STREAM>
 hipError_t launch_apart(const NormGradParams& p, const RowShape& r, int stripes, int64_t sets, hipStream_t s) {
   if (stripes + sets == 0) return hipSuccess;
   const dim3 grid(static_cast<unsigned>(stripes + sets)), block(r.lanes * r.groups);
   if (r.lanes > 64)
-    hipLaunchKernelGGL((norm_apart_kernel<T, CH, false, true, DROP>), grid, block, 0, s, p, r.lanes, stripes);
+    hipLaunchKernelGGL((norm_apart_kernel<T, CH, false, true, DROP, STREAM>), grid, block, 0, s, p, r.lanes, stripes);
   else if (r.lanes == 64)
-    hipLaunchKernelGGL((norm_apart_kernel<T, 1, false, false, DROP>), grid, block, 0, s, p, r.lanes, stripes);
+    hipLaunchKernelGGL((norm_apart_kernel<T, 1, false, false, DROP, STREAM>), grid, block, 0, s, p, r.lanes, stripes);
   else
-    hipLaunchKernelGGL((norm_apart_kernel<T, 1, true, false, DROP>), grid, block, 0, s, p, r.lanes, stripes);
+    hipLaunchKernelGGL((norm_apart_kernel<T, 1, true, false, DROP, STREAM>), grid, block, 0, s, p, r.lanes, stripes);
   return hipGetLastError();
 }
 
-template <typename T, int CH, bool DROP>
+template <typename T, int CH, bool DROP, bool STREAM>
 hipError_t rows_apart(const NormGradParams& p, const RowShape& r, hipStream_t s) {
   const int64_t sets = p.dx.p == nullptr && p.dres.p == nullptr ? 0 : (p.rows + r.groups - 1) / r.groups;
   const int stripes = p.dw == nullptr && p.db == nullptr ? 0 : (p.d + kStripe - 1) / kStripe;
   // the columns' workgroups read dy: where a gradient takes its place, they go first
   const bool over_dy = p.dy.p != nullptr && (p.dx.p == p.dy.p || p.dres.p == p.dy.p);
-  if (!over_dy) return launch_apart<T, CH, DROP>(p, r, stripes, sets, s);
-  const hipError_t e = launch_apart<T, CH, DROP>(p, r, stripes, 0, s);
-  return e == hipSuccess ? launch_apart<T, CH, DROP>(p, r, 0, sets, s) : e;
+  if (!over_dy) return launch_apart<T, CH, DROP, STREAM>(p, r, stripes, sets, s);
+  const hipError_t e = launch_apart<T, CH, DROP, STREAM>(p, r, stripes, 0, s);
+  return e == hipSuccess ? launch_apart<T, CH, DROP, STREAM>(p, r, 0, sets, s) : e;
 }
 
-template <typename T, bool DROP>
+template <typename T, bool DROP, bool STREAM>
 hipError_t backward(const NormGradParams& p, float* part, hipStream_t s) {
   if (apart(p.rows, p.d)) {
     const RowShape r = apart_shape(p.d);
-    if (r.chunks == 1) return rows_apart<T, 1, DROP>(p, r, s);
-    if (r.chunks == 2) return rows_apart<T, 2, DROP>(p, r, s);
-    return rows_apart<T, 4, DROP>(p, r, s);
+    if (r.chunks == 1) return rows_apart<T, 1, DROP, STREAM>(p, r, s);
+    if (r.chunks == 2) return rows_apart<T, 2, DROP, STREAM>(p, r, s);
+    return rows_apart<T, 4, DROP, STREAM>(p, r, s);
   }
   const RowShape r = row_shape(p.d / 8, 1, kGradThreads);
   const int blocks = norm_grad_blocks(p.rows, p.d);
   const dim3 grid(blocks), block(r.lanes * r.groups);
   if (r.lanes > 64)
-    hipLaunchKernelGGL((norm_grad_kernel<T, false, true, DROP>), grid, block, 0, s, p, r.lanes, part);
+    hipLaunchKernelGGL((norm_grad_kernel<T, false, true, DROP, STREAM>), grid, block, 0, s, p, r.lanes, part);
   else if (r.lanes == 64)
-    hipLaunchKernelGGL((norm_grad_kernel<T, false, false, DROP>), grid, block, 0, s, p, r.lanes, part);
+    hipLaunchKernelGGL((norm_grad_kernel<T, false, false, DROP, STREAM>), grid, block, 0, s, p, r.lanes, part);
   else
-    hipLaunchKernelGGL((norm_grad_kernel<T, true, false, DROP>), grid, block, 0, s, p, r.lanes, part);
+    hipLaunchKernelGGL((norm_grad_kernel<T, true, false, DROP, STREAM>), grid, block, 0, s, p, r.lanes, part);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || (p.dw == nullptr && p.db == nullptr)) return e;
   hipLaunchKernelGGL(norm_join_kernel<T>, dim3((p.d + 31) / 32, 2), dim3(256), 0, s, part, blocks, p.d,
@@ -573,8 +574,9 @@ hipError_t backward(const NormGradParams& p, float* part, hipStream_t s) {
 hipError_t launch_norm(const NormParams& p, int dtype, hipStream_t s) {
   if (p.rows == 0) return hipSuccess;
   const bool drop = p.drop.least != 0;
-  if (dtype == 1) return drop ? forward<uint16_t, true>(p, s) : forward<uint16_t, false>(p, s);
-  return drop ? forward<float, true>(p, s) : forward<float, false>(p, s);
+  if (dtype != 1) return drop ? forward<float, true, false>(p, s) : forward<float, false, false>(p, s);
+  if (streams(p.rows * p.d, dtype)) return drop ? forward<uint16_t, true, true>(p, s) : forward<uint16_t, false, true>(p, s);
+  return drop ? forward<uint16_t, true, false>(p, s) : forward<uint16_t, false, false>(p, s);
 }
 
 int64_t norm_grad_workspace(int64_t rows, int32_t d) {
@@ -586,8 +588,10 @@ hipError_t launch_norm_grad(const NormGradParams& p, int dtype, void* ws, hipStr
   if (p.rows == 0 && p.dw == nullptr && p.db == nullptr) return hipSuccess;
   float* part = static_cast<float*>(ws);
   const bool drop = p.drop.least != 0;
-  if (dtype == 1) return drop ? backward<uint16_t, true>(p, part, s) : backward<uint16_t, false>(p, part, s);
-  return drop ? backward<float, true>(p, part, s) : backward<float, false>(p, part, s);
+  if (dtype != 1) return drop ? backward<float, true, false>(p, part, s) : backward<float, false, false>(p, part, s);
+  if (streams(p.rows * p.d, dtype))
+    return drop ? backward<uint16_t, true, true>(p, part, s) : backward<uint16_t, false, true>(p, part, s);
+  return drop ? backward<uint16_t, true, false>(p, part, s) : backward<uint16_t, false, false>(p, part, s);
 }
 
 }  // namespace ada
