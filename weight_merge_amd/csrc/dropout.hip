@@ -34,28 +34,35 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(DropoutParams p, uint
   const T* res = static_cast<const T*>(p.res.p);
   T* y = static_cast<T*>(p.y.p);
   const DropKey key = drop_key(p.drop);
-  Eight<T> in[kBlocks], add[kBlocks];
-#pragma unroll
-  for (int u = 0; u < kBlocks; ++u) {
-    const uint64_t g = g0 + u * kThreads;
-    if (g >= blocks) continue;
-    in[u] = load_eight<STREAM>(x + block_at<DENSE>(g, per_row, inv, p.x.ld));
-    if constexpr (RES) add[u] = load_eight<STREAM>(res + block_at<DENSE>(g, per_row, inv, p.res.ld));
-  }
-#pragma unroll
-  for (int u = 0; u < kBlocks; ++u) {
-    const uint64_t g = g0 + u * kThreads;
-    if (g >= blocks) continue;
+  const auto one = [&](uint64_t g, const Eight<T>& in, const Eight<T>& add) {
     float f[8];
-    unpack(in[u], f);
+    unpack(in, f);
     drop_eight(f, uint32_t(g), key, p.drop.least, p.drop.scale);
     if constexpr (RES) {
       float r[8];
-      unpack(add[u], r);
+      unpack(add, r);
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] += r[i];
     }
     store_eight(y + block_at<DENSE>(g, per_row, inv, p.y.ld), f);
+  };
+  if (uint64_t(blockIdx.x + 1) * (kThreads * kBlocks) <= blocks) {
+    Eight<T> in[kBlocks], add[kBlocks];
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) {
+      const uint64_t g = g0 + u * kThreads;
+      in[u] = load_eight<STREAM>(x + block_at<DENSE>(g, per_row, inv, p.x.ld));
+      if constexpr (RES) add[u] = load_eight<STREAM>(res + block_at<DENSE>(g, per_row, inv, p.res.ld));
+    }
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) one(g0 + u * kThreads, in[u], add[u]);
+    return;
+  }
+  for (uint64_t g = g0; g < blocks; g += kThreads) {  // the last workgroup
+    Eight<T> in, add;
+    in = load_eight<STREAM>(x + block_at<DENSE>(g, per_row, inv, p.x.ld));
+    if constexpr (RES) add = load_eight<STREAM>(res + block_at<DENSE>(g, per_row, inv, p.res.ld));
+    one(g, in, add);
   }
 }
 

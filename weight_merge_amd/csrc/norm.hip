@@ -45,8 +45,12 @@ __device__ __forceinline__ void row_totals(float (&v)[N], int lanes, float (*slo
       for (int i = 0; i < N; ++i) slot[wave][i] = v[i];
     }
     __syncthreads();
+    const float* at = slot[first + (from < waves ? from : 0)];
+    float part[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = row16_total(from < waves ? slot[first + from][i] : 0.f);
+    for (int i = 0; i < N; ++i) part[i] = at[i];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = row16_total(from < waves ? part[i] : 0.f);
   }
 }
 
@@ -198,6 +202,18 @@ struct GradRow {
     rstd = live ? p.rstd[row] : 0.f;
   }
 
+  // Makes the loads' results wanted here.
+  __device__ __forceinline__ void arrived() {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+#pragma unroll
+      for (unsigned j = 0; j < sizeof(T) / 2; ++j) {
+        asm volatile("" : "+v"(c[i].dy.v[j]), "+v"(c[i].h.v[j]), "+v"(c[i].add.v[j]));
+      }
+    }
+    asm volatile("" : "+v"(mean), "+v"(rstd));
+  }
+
   // The eight values of dh from block i, given the means of t and of t xhat.
   __device__ __forceinline__ void gradient(int i, const float (&w)[8], float c1, float c2, float (&dh)[8]) const {
     float dy[8], add[8];
@@ -222,11 +238,11 @@ __device__ __forceinline__ void store_gradient(const NormGradParams& p, int64_t 
   store_eight<STREAM_DX>(static_cast<T*>(p.dx.p) + row * p.dx.ld + g * 8, dh);
 }
 
+// Eight weights; ones where there are none.
 template <typename T>
-__device__ __forceinline__ void load_weight(const void* w, int g, bool live, float (&f)[8]) {
-  if (w != nullptr && live) {
-    unpack(load_eight(static_cast<const T*>(w) + g * 8), f);
-  } else {
+__device__ __forceinline__ void weight_of(const void* w, const Eight<T>& raw, float (&f)[8]) {
+  unpack(raw, f);
+  if (w == nullptr) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = 1.f;
   }
@@ -251,13 +267,15 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(NormGradParams p, int l
   zero_eight(weight);
   if (p.w != nullptr && inside) weight = load_eight(static_cast<const T*>(p.w) + lane * 8);
 
-  const auto take = [&](const GradRow<T, 1, STREAM>& now, int64_t row, float (*totals)[2]) {
+  GradRow<T, 1, STREAM> now, next;
+  const int64_t step = int64_t(gridDim.x) * groups;
+  int64_t row = int64_t(blockIdx.x) * groups + group;
+  now.load(p, row, lane, lanes, per_row);
+  int turn = 0;
+  for (int64_t row0 = row - group; row0 < p.rows; row0 += step, row += step, turn ^= 1) {
+    next.load(p, row + step, lane, lanes, per_row);
     float sums[2] = {0.f, 0.f}, dy[8], h[8], w[8];
-    unpack(weight, w);
-    if (p.w == nullptr) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = 1.f;
-    }
+    weight_of(p.w, weight, w);
     unpack(now.c[0].dy, dy);
     unpack(now.c[0].h, h);
 #pragma unroll
@@ -268,21 +286,13 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(NormGradParams p, int l
       dw[i] = fmaf(dy[i], xhat, dw[i]);
       db[i] += dy[i];
     }
-    row_totals<2, SUB, WIDE>(sums, lanes, totals);
-    if (row < p.rows && inside) {
-      now.gradient(0, w, p.mean != nullptr ? sums[0] * over : 0.f, sums[1] * over, h);
-      store_gradient<T, DROP, STREAM, false>(p, row, lane, key, h);
-    }
-  };
-  GradRow<T, 1, STREAM> now, next;
-  const int64_t step = int64_t(gridDim.x) * groups;
-  int64_t row = int64_t(blockIdx.x) * groups + group;
-  now.load(p, row, lane, lanes, per_row);
-  int turn = 0;
-  for (int64_t row0 = row - group; row0 < p.rows; row0 += step, row += step, turn ^= 1) {
-    next.load(p, row + step, lane, lanes, per_row);
-    take(now, row, slot[turn]);
+    row_totals<2, SUB, WIDE>(sums, lanes, slot[turn]);
+    now.gradient(0, w, p.mean != nullptr ? sums[0] * over : 0.f, sums[1] * over, h);
+    // the next row's loads are waited for before this row's stores: the counter holds both, and behind
+    // the stores the wait would be for them too
     now = next;
+    now.arrived();
+    if (row < p.rows && inside) store_gradient<T, DROP, STREAM, false>(p, row, lane, key, h);
   }
 
   for (int which = 0; which < 2; ++which) {
@@ -311,7 +321,7 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(NormGradParams p, int l
 // rows dealt to sets of eight lanes; the others take a set of rows each.  dy and h are read twice,
 // but there are no partial sums to write and join, so few rows need one launch; and a row is only
 // held until it is summed, so wide ones fit the registers.  Large calls stream dx too: what stays in the
-// caches is dy and h for their second reading (1170 x 28672: 98 us, with dx kept 111).
+// caches is dy and h for their second reading (1170 x 28672: 96 us, with dx kept 111).
 constexpr int kStripe = 64;
 template <typename T, int CH, bool SUB, bool WIDE, bool DROP, bool STREAM>
 __global__ void __launch_bounds__(1024) norm_apart_kernel(NormGradParams p, int lanes, int stripes) {
@@ -320,28 +330,24 @@ __global__ void __launch_bounds__(1024) norm_apart_kernel(NormGradParams p, int 
     __shared__ f32x4 meet[kMaxWaves][8][4];
     const int quad = threadIdx.x & 7, sets = blockDim.x >> 3, g = blockIdx.x * 8 + quad;
     const bool inside = g < per_row;
-    const T* dyp = static_cast<const T*>(p.dy.p) + g * 8;
-    const T* hp = static_cast<const T*>(p.hidden.p) + g * 8;
+    const T* dyp = static_cast<const T*>(p.dy.p) + (inside ? g : 0) * 8;
+    const T* hp = static_cast<const T*>(p.hidden.p) + (inside ? g : 0) * 8;
     f32x4 sum[4] = {};  // dw, dw, db, db
     constexpr int U = 4;
     for (int64_t row0 = threadIdx.x >> 3; row0 < p.rows; row0 += int64_t(sets) * U) {
       Eight<T> a[U], b[U];
       float mean[U], rstd[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t row = row0 + int64_t(u) * sets;
-        zero_eight(a[u]);
-        zero_eight(b[u]);
-        mean[u] = rstd[u] = 0.f;
-        if (row < p.rows && inside) {
-          a[u] = load_eight(dyp + row * p.dy.ld);
-          b[u] = load_eight(hp + row * p.hidden.ld);
-          if (p.mean != nullptr) mean[u] = p.mean[row];
-          rstd[u] = p.rstd[row];
-        }
+      for (int u = 0; u < U; ++u) {  // past the last row the last again, and nothing of it is added
+        const int64_t at = row0 + int64_t(u) * sets, row = at < p.rows ? at : p.rows - 1;
+        a[u] = load_eight(dyp + row * p.dy.ld);
+        b[u] = load_eight(hp + row * p.hidden.ld);
+        mean[u] = p.mean != nullptr ? p.mean[row] : 0.f;
+        rstd[u] = p.rstd[row];
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
+        if (row0 + int64_t(u) * sets >= p.rows) break;
         float dy[8], h[8];
         unpack(a[u], dy);
         unpack(b[u], h);
@@ -385,15 +391,28 @@ __global__ void __launch_bounds__(1024) norm_apart_kernel(NormGradParams p, int 
   if constexpr (DROP) key = drop_key(p.drop);
   const int64_t row = int64_t(blockIdx.x - stripes) * groups + group;
   GradRow<T, CH, STREAM> now;
+  // the weights come with the row and stay for its second use; of the widest rows they are read twice
+  constexpr bool HOLD = CH < 4;
+  Eight<T> held[HOLD ? CH : 1];
+  const auto load_weight = [&](int c) {
+    const int g = lane + c * lanes;
+    Eight<T> w;
+    zero_eight(w);
+    if (p.w != nullptr) w = load_eight(static_cast<const T*>(p.w) + (g < per_row ? g : 0) * 8);
+    return w;
+  };
+  if constexpr (HOLD) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) held[c] = load_weight(c);
+  }
   now.load(p, row, lane, lanes, per_row);
   float sums[2] = {0.f, 0.f};
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    const int g = lane + c * lanes;
     float dy[8], h[8], w[8];
     unpack(now.c[c].dy, dy);
     unpack(now.c[c].h, h);
-    load_weight<T>(p.w, g, g < per_row, w);
+    weight_of(p.w, HOLD ? held[HOLD ? c : 0] : load_weight(c), w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float t = dy[i] * w[i];
@@ -409,7 +428,7 @@ __global__ void __launch_bounds__(1024) norm_apart_kernel(NormGradParams p, int 
     const int g = lane + c * lanes;
     if (g >= per_row) continue;
     float w[8], dh[8];
-    load_weight<T>(p.w, g, true, w);
+    weight_of(p.w, HOLD ? held[HOLD ? c : 0] : load_weight(c), w);
     now.gradient(c, w, c1, c2, dh);
     store_gradient<T, DROP, STREAM, STREAM>(p, row, g, key, dh);
   }
@@ -422,27 +441,34 @@ constexpr int kJoinSets = 32;
 template <typename T>
 __global__ void __launch_bounds__(256) norm_join_kernel(const float* part, int parts, int d, T* dw, T* db) {
   constexpr int EACH = (kGradBlocks + kJoinSets - 1) / kJoinSets;
-  __shared__ f32x4 meet[kJoinSets][8];
+  __shared__ f32x4 meet[4][8];
   T* out = blockIdx.y == 0 ? dw : db;
   if (out == nullptr) return;
-  const float* from = part + int64_t(blockIdx.y) * parts * d;
   const int quad = threadIdx.x & 7, set = threadIdx.x >> 3, col = blockIdx.x * 32 + quad * 4;
+  const float* from = part + int64_t(blockIdx.y) * parts * d + (col < d ? col : 0);
   f32x4 v[EACH];
 #pragma unroll
   for (int i = 0; i < EACH; ++i) {
     const int r = set + i * kJoinSets;
-    v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (col < d && r < parts) v[i] = *reinterpret_cast<const f32x4*>(from + int64_t(r) * d + col);
+    v[i] = *reinterpret_cast<const f32x4*>(from + int64_t(r < parts ? r : 0) * d);
   }
+  f32x4 sum{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 1; i < EACH; ++i) v[0] += v[i];
-  meet[set][quad] = v[0];
+  for (int i = 0; i < EACH; ++i) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] += set + i * kJoinSets < parts ? v[i][e] : 0.f;
+  }
+  // the eight sets of a wave, then the waves
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    for (int m = 8; m < 64; m <<= 1) sum[e] += __shfl_xor(sum[e], m, 64);
+  }
+  if ((threadIdx.x & 63) < 8) meet[threadIdx.x >> 6][quad] = sum;
   __syncthreads();
   const int c = blockIdx.x * 32 + threadIdx.x;
   if (threadIdx.x < 32 && c < d) {
-    float sum = 0.f;
-#pragma unroll
-    for (int q = 0; q < kJoinSets; ++q) sum += meet[q][threadIdx.x >> 2][threadIdx.x & 3];
+    const int q = threadIdx.x >> 2, e = threadIdx.x & 3;
+    const float sum = (meet[0][q][e] + meet[1][q][e]) + (meet[2][q][e] + meet[3][q][e]);
     if constexpr (sizeof(T) == 2)
       out[c] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(sum));
     else
@@ -480,10 +506,11 @@ RowShape forward_shape(int64_t rows, int d) {
 }
 
 // Rows and columns apart, or in one pass.  Apart reads 7 matrices for 5 but has no partial sums and
-// one launch: 512 x 4096 bf16 9.6 against 14.9 us, 1024 x 4096 14.8 against 17.4, 2048 x 4096 26 against
-// 22; 1024 x 1032 14.2 against 12.1, 1024 x 8192 20.4 against 26.9, 4096 x 8192 67 against 55.  Past 8192
+// one launch; it is the faster up to 550 to 1400 rows, more with more columns: 512 x 4096 bf16 8.0
+// against 13.6 us, 1024 x 4096 14.7 against 15.9, 1536 x 4096 20.3 against 17.7; 512 x 1032 7.4 against
+// 8.4, 1024 x 1032 11.3 against 9.8; 1024 x 8192 19.7 against 22.9, 4096 x 8192 67 against 54.  Past 8192
 // columns a lane of the one pass would hold two blocks or more with their sums, which spilled:
-// 1170 x 28672 in 98 us apart, 218 in one pass.
+// 1170 x 28672 in 96 us apart, 218 in one pass.
 bool apart(int64_t rows, int d) { return d > 8192 || rows <= 512 + d / 8; }
 
 // The rows' part, as the forward pass; at least 512 threads for the columns' part.

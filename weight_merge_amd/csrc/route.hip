@@ -212,9 +212,8 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteParams p, BalanceP
       if (q * L >= p.k) break;
       uint32_t mine = 0;
       pick[q] = kMaxExperts;
-#pragma unroll
-      for (int t = 0; t < L; ++t) {
-        if (q * L + t >= p.k) break;
+#pragma unroll 1  // little code: a workgroup walks through it once or twice, and every line of it is fetched
+      for (int t = 0; t < L && q * L + t < p.k; ++t) {
         uint32_t best;
         const uint32_t one = next_pick<L>(key, first, best);
         pick[q] = t == l ? one : pick[q];
@@ -305,7 +304,8 @@ __global__ void __launch_bounds__(kThreads) balance_join_kernel(RouteParams p, B
 #pragma unroll
   for (int i = 0; i < EACH; ++i) {
     const int b = wave + i * WAVES;
-    part[i] = b < blocks && lane < p.E ? parts.experts[b * kMaxExperts + lane] : make_uint2(0, 0);
+    if (i * WAVES >= blocks) break;
+    part[i] = parts.experts[(b < blocks ? b : 0) * kMaxExperts + lane];
   }
   static_assert(kMostBlocks <= kThreads);
   int used = int(threadIdx.x) < blocks ? parts.used[threadIdx.x] : 0;
@@ -313,8 +313,10 @@ __global__ void __launch_bounds__(kThreads) balance_join_kernel(RouteParams p, B
   int count = 0;
 #pragma unroll
   for (int i = 0; i < EACH; ++i) {
-    sum += __uint_as_float(part[i].x);
-    count += int(part[i].y);
+    if (i * WAVES >= blocks) break;
+    const bool some = wave + i * WAVES < blocks;
+    sum += some ? __uint_as_float(part[i].x) : 0.f;
+    count += some ? int(part[i].y) : 0;
   }
   for (int s = 1; s < 64; s <<= 1) used += __shfl_xor(used, s, 64);
   wave_prob[wave][lane] = sum;
