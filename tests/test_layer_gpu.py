@@ -435,6 +435,30 @@ def test_route_of_nothing():
 
 
 @pytest.mark.gpu
+def test_rows_that_lie_on_each_other_are_refused():
+    """Rows broadcast from one, or closer than their length: no row stride the calls take."""
+    for z in (torch.zeros((1, 16), device=DEV).expand(5, 16), torch.zeros(100, device=DEV).as_strided((5, 16), (8, 1))):
+        out = A.ada_route(torch.zeros((5, 16), device=DEV), 2)
+        stats = (torch.zeros(5, device=DEV), torch.ones(5, device=DEV))
+        for call in (lambda: A.ada_route(z, 2), lambda: A.ada_route_backward(z, out, dloss=out.loss), lambda: A.ada_norm(z),
+                     lambda: A.ada_norm(torch.zeros((5, 16), device=DEV), residual=z), lambda: A.ada_dropout(z, 0.1, 1),
+                     lambda: A.ada_dropout_backward(z, 0.1, 1), lambda: A.ada_norm_backward(z, z, stats),
+                     lambda: A.ada_dropout(torch.zeros((5, 16), device=DEV), 0.1, 1, y=z),
+                     lambda: A.ada_route_backward(out.gate.new_zeros((5, 16)), out, dloss=out.loss, dlogits=z)):
+            with pytest.raises(A.AdaError):
+                call()
+
+
+@pytest.mark.gpu
+def test_no_balance_into_the_buffers_of_one_that_had_it():
+    z = H.logits(1, 9, 12, "fp32").to(DEV)
+    out = A.ada_route(z, 3)
+    bare = A.ada_route(z, 2, balance=False, out=(torch.empty_like(out.idx[:, :2]).contiguous(),
+                                                 torch.empty_like(out.gate[:, :2]).contiguous(), *out[2:]))
+    assert bare[2:] == (None,) * 4 and torch.equal(bare.idx, out.idx[:, :2])
+
+
+@pytest.mark.gpu
 def test_route_of_the_largest_and_lowest_logits():
     """The type's lowest value is an open expert of no probability, not a closed one; equal
     zeros of either sign tie; NaN and +inf are picked and stay in their row, out of range never."""

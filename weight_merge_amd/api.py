@@ -814,12 +814,6 @@ class Routing(NamedTuple):
     used: torch.Tensor     # int32 [1]: the rows that count
 
 
-def _logits(t: torch.Tensor, rows: int, E: int, dt, dev: int, name: str):
-    """Pointer and row stride of [rows, E] logits, which may begin anywhere."""
-    p, ld = _mat(t, rows, E, dt, dev, name)
-    return p, max(ld, E)
-
-
 def _table(t: torch.Tensor, shape, dt, dev: int, name: str):
     """Pointer of a contiguous table."""
     if t is None:
@@ -848,7 +842,7 @@ def ada_route(logits: torch.Tensor, k: int, renorm: bool = True, valid=None, bal
         return _on(stream, ada_route, logits, k, renorm, valid, balance, out, workspace)
     rows, E = _shape(logits, "logits")
     dc, dev = _dtype(logits), logits.get_device()
-    pl, ld = _logits(logits, rows, E, logits.dtype, dev, "logits")
+    pl, ld = _mat(logits, rows, E, logits.dtype, dev, "logits")
     pv = None
     if valid is not None:
         if valid.dtype not in (torch.bool, torch.uint8):
@@ -867,7 +861,9 @@ def ada_route(logits: torch.Tensor, k: int, renorm: bool = True, valid=None, bal
     pi = _table(out.idx, (rows, k), i32, dev, "idx")
     pg = _table(out.gate, (rows, k), f32, dev, "gate")
     pc = pp = po = pu = None
-    if balance:
+    if not balance:
+        out = Routing(out.idx, out.gate, None, None, None, None)
+    else:
         pc = _vec(out.counts, E, i32, dev, "counts")
         pp = _vec(out.prob, E, f32, dev, "prob")
         po = _vec(out.loss, 1, f32, dev, "loss")
@@ -895,7 +891,7 @@ def ada_route_backward(logits: torch.Tensor, out, dgate=None, dloss=None, renorm
     k = idx.shape[1]
     if dgate is None and dloss is None:
         raise ValueError("dgate or dloss is needed")
-    pl, ld = _logits(logits, rows, E, dt, dev, "logits")
+    pl, ld = _mat(logits, rows, E, dt, dev, "logits")
     pi = _table(idx, (rows, k), i32, dev, "idx")
     pg = _table(gate, (rows, k), f32, dev, "gate")
     pdg = _table(dgate, (rows, k), f32, dev, "dgate")
@@ -907,7 +903,7 @@ def ada_route_backward(logits: torch.Tensor, out, dgate=None, dloss=None, renorm
         pu = _vec(used, 1, i32, dev, "used")
         pdl = _vec(dloss, 1, f32, dev, "dloss")
     if dlogits is not None:
-        po, ldo = _logits(dlogits, rows, E, dt, dev, "dlogits")
+        po, ldo = _mat(dlogits, rows, E, dt, dev, "dlogits")
     _current(dev)
     if dlogits is None:
         dlogits = torch.empty((rows, E), dtype=dt, device=logits.device)
