@@ -392,7 +392,7 @@ def _vec(t, n: int, dt, dev: int, name: str):
     """Pointer of an [n] vector."""
     if t is None:
         return None
-    if t.shape != (n,) or t.dtype is not dt or t.get_device() != dev or t.stride(0) != 1:
+    if t.shape != (n,) or t.dtype is not dt or t.get_device() != dev or not t.is_contiguous():
         _refuse(t, (n,), dt, dev, name)
     return t.data_ptr()
 
@@ -820,7 +820,8 @@ def _table(t: torch.Tensor, shape, dt, dev: int, name: str):
         return None
     if t.shape != shape or t.dtype is not dt or t.get_device() != dev:
         _refuse(t, shape, dt, dev, name)
-    _contig(t, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
