@@ -421,6 +421,28 @@ def test_route_of_many_rows(dtype, E, k):
 
 
 @pytest.mark.gpu
+@BOTH
+@pytest.mark.parametrize("E", (8, 16, 21))
+def test_route_of_logits_that_begin_anywhere(E, dtype):
+    """Columns of a wider product from an odd one on, and rows from an odd one on: no vector is aligned."""
+    z = H.logits(6, 70, E, dtype, closed=0.2)
+    ref = A.ada_route(z.to(DEV), 3)
+    g = H.normal(7, (70, 3), 0.3, "fp32").to(DEV)
+    dref = A.ada_route_backward(z.to(DEV), ref, dgate=g, dloss=ref.loss)
+    wide = torch.full((71, E + 16), float("nan"), dtype=H.TD[dtype], device=DEV)
+    for first, at in ((1, 0), (3, 1), (0, 1)):
+        view, dview = wide[at:at + 70, first:first + E], wide.clone()[at:at + 70, first:first + E]
+        view.copy_(z)
+        got = A.ada_route(view, 3)
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
+        A.ada_route_backward(view, got, dgate=g, dloss=got.loss, dlogits=dview)
+        assert torch.equal(dview, dref)
+    flat = torch.empty(70 * E + 1, dtype=H.TD[dtype], device=DEV)[1:].view(70, E)
+    flat.copy_(z)
+    assert all(torch.equal(a, b) for a, b in zip(A.ada_route(flat, 3), ref))
+
+
+@pytest.mark.gpu
 def test_route_of_nothing():
     z = torch.zeros((4, 8), device=DEV)
     none = torch.zeros(4, dtype=torch.bool, device=DEV)

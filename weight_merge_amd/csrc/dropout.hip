@@ -5,7 +5,8 @@
 //
 // Bound by memory: 2 (3 with a residual) values moved an element.  A lane takes blocks of eight
 // elements, one 16-byte vector in bf16 and one draw of the generator; kBlocks of them a workgroup
-// apart, all loads in flight before the first draw.
+// apart, all loads in flight before the first draw.  4096 x 28672 bf16: 78.5 us, 6.0 TB/s (with one
+// round of the generator instead of ten 1 us less, so its instructions hide behind the stream).
 #include "elements.h"
 
 namespace ada {
