@@ -24,10 +24,16 @@ def test_layer_host_code_under_address_and_undefined_behaviour_sanitizers(tmp_pa
         host_only += ["-Xarch_host", f"-fsanitize={f}"]
     host_only += ["-Xarch_host", "-fno-sanitize-recover=undefined,float-cast-overflow", "-Xarch_host",
                   "-fno-omit-frame-pointer"]
-    flags = [f if f != "-O3" else "-O1" for f in build.FLAGS]
-    cmd = [build.HIPCC, *flags, *host_only, "-I", os.path.join(ROOT, "include"), "-I", os.path.join(build.PKG, "csrc"),
-           *build.sources(), "-o", lib]
-    res = subprocess.run(cmd, capture_output=True, text=True)
+    flags = [f if f != "-O3" else "-O1" for f in build.FLAGS if f != "-shared"]
+    paths = ["-I", os.path.join(ROOT, "include"), "-I", os.path.join(build.PKG, "csrc")]
+    objects = [str(tmp_path / (os.path.basename(s) + ".o")) for s in build.sources()]
+    runs = [subprocess.Popen([build.HIPCC, *flags, *host_only, *paths, "-c", s, "-o", o], stdout=subprocess.DEVNULL,
+                             stderr=subprocess.PIPE, text=True) for s, o in zip(build.sources(), objects)]
+    for run in runs:
+        err = run.communicate()[1]
+        assert run.returncode == 0, err[-3000:]
+    res = subprocess.run([build.HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *host_only, *objects, "-o", lib],
+                         capture_output=True, text=True)
     assert res.returncode == 0, res.stderr[-3000:]
     syms = subprocess.run(["nm", "-D", "--undefined-only", lib], capture_output=True, text=True).stdout
     assert "__asan_" in syms and "__ubsan_" in syms, "the host code was not instrumented"
