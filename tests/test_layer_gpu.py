@@ -311,6 +311,25 @@ def test_dropout_past_32_bits_of_elements():
     assert torch.equal(A.ada_dropout(far, 0.3, 1, y=far), A.ada_dropout(near, 0.3, 1))
 
 
+@pytest.mark.gpu
+def test_more_rows_than_workgroups():
+    """Workgroups of the norm that take a second row, with the dropout's place of it."""
+    rows, d = 2 ** 20 + 3, 2056
+    x = torch.empty((rows, d), dtype=torch.bfloat16, device=DEV)
+    x.view(-1)[: 1 << 24].normal_()
+    x.view(-1)[1 << 24:].copy_(x.view(-1)[: 1 << 24].repeat(rows * d // (1 << 24) + 1)[: rows * d - (1 << 24)])
+    w = (1 + H.normal(1, (d,), 0.1, "fp32")).to(H.TD["bf16"]).to(DEV)
+    for first in (0, 2 ** 20 - 2, rows - 2):
+        at = x[first:first + 2]
+        kept = torch.from_numpy(OL.dropout_mask(2, d, 0.5, 3, 4, first_row=first)[0]).to(DEV)
+        part = torch.where(kept, at * 2, 0.0)
+        expect = (part.clone(), A.ada_norm(part, w))
+        if first == 0:
+            hidden = torch.empty_like(x)
+            y = A.ada_norm(x, w, p=0.5, seed=3, offset=4, hidden=hidden)
+        assert torch.equal(hidden[first:first + 2], expect[0]) and torch.equal(y[first:first + 2], expect[1])
+
+
 # ---- the router ------------------------------------------------------------------------
 # (rows, experts, k): one lane to eight lanes a row, experts on and off multiples of eight, every
 # number of picks, rows that fill no, one and several workgroups
