@@ -118,6 +118,24 @@ def test_norm_backward_shapes(shape, dtype):
 
 @pytest.mark.gpu
 @BOTH
+@pytest.mark.parametrize("shape", [(17000, 248), (2051, 2056), (520, 8136), (257, 16392)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_matrices_past_the_caches(shape, dtype):
+    """From 2^22 elements on, some accesses are of another kind."""
+    rows, d = shape
+    assert rows * d >= 2 ** 22
+    check_norm(*shape, dtype, "layer", p=0.2, pad=8, seed=3)
+    check_norm_backward(*shape, dtype, "layer", p=0.2, pad=8, seed=4)
+    n, t = made(5, *shape, dtype, pad=8)
+    y = empty(*shape, dtype=dtype, pad=8)
+    A.ada_dropout(t["x"], 0.2, 6, 7, residual=t["res"], y=y)
+    dropped = OL.dropout(n["x"], 0.2, 6, 7)
+    H.assert_within(y, dropped + n["res"], H.dropout_bound(dropped + n["res"], dropped, n["res"], dtype), "dropout")
+    gaps_untouched(y)
+
+
+@pytest.mark.gpu
+@BOTH
 @pytest.mark.parametrize("kind", ("layer", "rms"))
 @pytest.mark.parametrize("p", (0.0, 0.3))
 def test_norm_operands_on_and_off(kind, p, dtype):

@@ -15,19 +15,31 @@ template <typename T>
 struct Eight {
   u32x4 v[sizeof(T) / 2];  // bf16: one vector, fp32: two
 };
+template <typename T>
+constexpr int kVectors = sizeof(T) / 2;  // of a block
+template <typename T>
+constexpr int kVector = 16 / sizeof(T);  // elements of a vector
 
 // STREAM: past the caches' ordinary policy (streams() below).
-template <bool STREAM = false, typename T>
+template <bool STREAM>
+__device__ __forceinline__ u32x4 load_vector(const u32x4* p) {
+  if constexpr (STREAM) return __builtin_nontemporal_load(p);
+  return *p;
+}
+template <bool STREAM>
+__device__ __forceinline__ void store_vector(u32x4* p, u32x4 v) {
+  if constexpr (STREAM)
+    __builtin_nontemporal_store(v, p);
+  else
+    *p = v;
+}
+
+// Eight elements in a row.
+template <typename T>
 __device__ __forceinline__ Eight<T> load_eight(const T* p) {
   Eight<T> e;
 #pragma unroll
-  for (unsigned i = 0; i < sizeof(T) / 2; ++i) {
-    const u32x4* v = reinterpret_cast<const u32x4*>(p) + i;
-    if constexpr (STREAM)
-      e.v[i] = __builtin_nontemporal_load(v);
-    else
-      e.v[i] = *v;
-  }
+  for (int i = 0; i < kVectors<T>; ++i) e.v[i] = load_vector<false>(reinterpret_cast<const u32x4*>(p) + i);
   return e;
 }
 
@@ -66,16 +78,49 @@ __device__ __forceinline__ Eight<uint16_t> pack(const float (&f)[8], uint16_t) {
   return e;
 }
 
-template <bool STREAM = false, typename T>
+template <typename T>
 __device__ __forceinline__ void store_eight(T* p, const float (&f)[8]) {
   const Eight<T> e = pack(f, T());
 #pragma unroll
-  for (unsigned i = 0; i < sizeof(T) / 2; ++i) {
-    u32x4* v = reinterpret_cast<u32x4*>(p) + i;
-    if constexpr (STREAM)
-      __builtin_nontemporal_store(e.v[i], v);
-    else
-      *v = e.v[i];
+  for (int i = 0; i < kVectors<T>; ++i) store_vector<false>(reinterpret_cast<u32x4*>(p) + i, e.v[i]);
+}
+
+// Eight elements of a row that `lanes` lanes share, the lane's block c: in bf16 vector c lanes + lane of
+// the row's, in fp32 vectors 2 c lanes + lane and (2 c + 1) lanes + lane, so that an instruction's lanes
+// lie side by side in either.  Vectors past the row's `vectors` are zero, and are not stored.
+template <typename T>
+__device__ __forceinline__ int vector_of(int lane, int lanes, int c, int i) {
+  return lane + (c * kVectors<T> + i) * lanes;
+}
+template <bool STREAM = false, typename T>
+__device__ __forceinline__ Eight<T> load_block(const T* row, int lane, int lanes, int c, int vectors) {
+  Eight<T> e;
+#pragma unroll
+  for (int i = 0; i < kVectors<T>; ++i) {
+    const int v = vector_of<T>(lane, lanes, c, i);
+    e.v[i] = u32x4{0, 0, 0, 0};
+    if (v < vectors) e.v[i] = load_vector<STREAM>(reinterpret_cast<const u32x4*>(row) + v);
+  }
+  return e;
+}
+// The same with some vector in place of one past the end: no branch.
+template <typename T>
+__device__ __forceinline__ Eight<T> load_anyway(const T* row, int lane, int lanes, int c, int vectors) {
+  Eight<T> e;
+#pragma unroll
+  for (int i = 0; i < kVectors<T>; ++i) {
+    const int v = vector_of<T>(lane, lanes, c, i);
+    e.v[i] = reinterpret_cast<const u32x4*>(row)[v < vectors ? v : 0];
+  }
+  return e;
+}
+template <bool STREAM = false, typename T>
+__device__ __forceinline__ void store_block(T* row, int lane, int lanes, int c, int vectors, const float (&f)[8]) {
+  const Eight<T> e = pack(f, T());
+#pragma unroll
+  for (int i = 0; i < kVectors<T>; ++i) {
+    const int v = vector_of<T>(lane, lanes, c, i);
+    if (v < vectors) store_vector<STREAM>(reinterpret_cast<u32x4*>(row) + v, e.v[i]);
   }
 }
 
@@ -83,10 +128,9 @@ __device__ __forceinline__ void store_eight(T* p, const float (&f)[8]) {
 // inputs, the residual stream and that stream's gradient, but not y and dx, which the next call reads.
 // Between products (norm, projection, norm, ..) of 4096 columns ordinary accesses throughout take 33.6 us
 // a layer at 509 rows (streamed: 33.6; with y too 35.0), 81.6 at 2047 (79.6; 80.9), 1800 at 16384 rows
-// of 8192 columns (1776; 1814); the backward pass at 509 rows 35.2 (37.5).  In fp32 a lane's two
-// vectors are an instruction each, either of which fills half of every line that it touches: ordinary
-// accesses only.
-inline bool streams(int64_t elements, int dtype) { return dtype == 1 && elements >= int64_t(1) << 22; }
+// of 8192 columns (1776; 1814); the backward pass at 509 rows 35.2 (37.5).  The same number in fp32:
+// dropout of 4096 x 14336 85.4 us ordinary, 77.9 streamed, of 2047 x 1032 5.2 and 6.8.
+inline bool streams(int64_t elements) { return elements >= int64_t(1) << 22; }
 
 // ---- dropout ---------------------------------------------------------------------------
 // Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3",
@@ -127,14 +171,43 @@ __device__ __forceinline__ u32x4 philox(uint32_t g, const DropKey& key) {
   return u32x4{c0, c1, c2, c3};
 }
 
-// Block g of eight elements: kept ones times the scale, dropped ones zero whatever they were.
-__device__ __forceinline__ void drop_eight(float (&f)[8], uint32_t g, const DropKey& key, uint32_t least,
-                                           float scale) {
-  const u32x4 w = philox(g, key);
+// Four elements with the numbers of two words: kept ones times the scale, dropped ones zero whatever
+// they were.
+__device__ __forceinline__ void drop_four(float* f, uint32_t w0, uint32_t w1, uint32_t least, float scale) {
+  f[0] = (w0 & 0xffffu) >= least ? f[0] * scale : 0.f;
+  f[1] = (w0 >> 16) >= least ? f[1] * scale : 0.f;
+  f[2] = (w1 & 0xffffu) >= least ? f[2] * scale : 0.f;
+  f[3] = (w1 >> 16) >= least ? f[3] * scale : 0.f;
+}
+
+// Block c of a lane (as load_block) of a row whose first eight elements are the matrix's block g0.  In
+// fp32 a lane holds halves of two of the generator's blocks, whose other halves its neighbour holds: the
+// even lane draws for the first, the odd one for the second, and they exchange two words each (`lanes`
+// is even, and so is a row's number of vectors: a pair holds or lacks a vector together).  APART: fewer
+// lanes, each draws for both.
+template <bool APART, typename T>
+__device__ __forceinline__ void drop_block(float (&f)[8], uint32_t g0, int lane, int lanes, int c, const DropKey& key,
+                                           uint32_t least, float scale) {
+  if constexpr (sizeof(T) == 2) {
+    const u32x4 w = philox(g0 + vector_of<T>(lane, lanes, c, 0), key);
+    drop_four(f, w[0], w[1], least, scale);
+    drop_four(f + 4, w[2], w[3], least, scale);
+  } else if constexpr (APART) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = (w[i] & 0xffffu) >= least ? f[2 * i] * scale : 0.f;
-    f[2 * i + 1] = (w[i] >> 16) >= least ? f[2 * i + 1] * scale : 0.f;
+    for (int i = 0; i < 2; ++i) {
+      const int v = vector_of<T>(lane, lanes, c, i);
+      const u32x4 w = philox(g0 + (v >> 1), key);
+      drop_four(f + 4 * i, v & 1 ? w[2] : w[0], v & 1 ? w[3] : w[1], least, scale);
+    }
+  } else {
+    const bool odd = lane & 1;
+    const u32x4 w = philox(g0 + (vector_of<T>(lane, lanes, c, odd) >> 1), key);
+    const auto theirs = [](uint32_t v) {  // quad_perm [1, 0, 3, 2]
+      return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0xB1, 0xf, 0xf, true));
+    };
+    const uint32_t t0 = theirs(odd ? w[0] : w[2]), t1 = theirs(odd ? w[1] : w[3]);
+    drop_four(f, odd ? t0 : w[0], odd ? t1 : w[1], least, scale);
+    drop_four(f + 4, odd ? w[2] : t0, odd ? w[3] : t1, least, scale);
   }
 }
 

@@ -64,17 +64,19 @@ template <typename T, int CH, bool STREAM>
 struct NormRow {
   Eight<T> x[CH], res[CH];
 
-  __device__ __forceinline__ void load(const NormParams& p, int64_t row, int lane, int lanes, int per_row) {
+  __device__ __forceinline__ void load(const NormParams& p, int64_t row, int lane, int lanes, int vectors) {
     const T* px = static_cast<const T*>(p.x.p) + row * p.x.ld;
     const T* pr = static_cast<const T*>(p.res.p) + row * p.res.ld;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int g = lane + c * lanes;
       zero_eight(x[c]);
       zero_eight(res[c]);
-      if (row < p.rows && g < per_row) {
-        x[c] = load_eight<STREAM>(px + g * 8);
-        if (p.res.p != nullptr) res[c] = load_eight<STREAM>(pr + g * 8);
+#pragma unroll
+      for (int i = 0; i < kVectors<T>; ++i) {
+        const int v = vector_of<T>(lane, lanes, c, i);
+        if (row >= p.rows || v >= vectors) continue;
+        x[c].v[i] = load_vector<STREAM>(reinterpret_cast<const u32x4*>(px) + v);
+        if (p.res.p != nullptr) res[c].v[i] = load_vector<STREAM>(reinterpret_cast<const u32x4*>(pr) + v);
       }
     }
   }
@@ -85,7 +87,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p, int lanes) {
   __shared__ float mean_slot[kMaxWaves][1];
   __shared__ float square_slot[kMaxWaves][2];
   const int group = threadIdx.x / lanes, lane = threadIdx.x - group * lanes, groups = blockDim.x / lanes;
-  const int per_row = p.d >> 3;
+  const int per_row = p.d >> 3, vectors = p.d / kVector<T>;
   const T* w = static_cast<const T*>(p.w);
   const T* b = static_cast<const T*>(p.b);
   const float over = 1.f / float(p.d);
@@ -96,24 +98,23 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p, int lanes) {
   // (16384 x 2048: 46.8 against 49.3 us); of two it costs more waves than it saves
   constexpr bool HOLD = CH == 1;
   Eight<T> wheld[HOLD ? CH : 1], bheld[HOLD ? CH : 1];
-  const auto load_vector = [&](const T* v, int c) {
-    const int g = lane + c * lanes;
+  const auto load_affine = [&](const T* v, int c) {
     Eight<T> e;
     zero_eight(e);
-    if (v != nullptr) e = load_eight(v + (g < per_row ? g : 0) * 8);
+    if (v != nullptr) e = load_anyway(v, lane, lanes, c, vectors);
     return e;
   };
   if constexpr (HOLD) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      wheld[c] = load_vector(w, c);
-      bheld[c] = load_vector(b, c);
+      wheld[c] = load_affine(w, c);
+      bheld[c] = load_affine(b, c);
     }
   }
   NormRow<T, CH, STREAM> now;
   const int64_t step = int64_t(gridDim.x) * groups;
   int64_t row = int64_t(blockIdx.x) * groups + group;
-  now.load(p, row, lane, lanes, per_row);
+  now.load(p, row, lane, lanes, vectors);
   for (int64_t row0 = row - group; row0 < p.rows; row0 += step, row += step) {
     T* y = static_cast<T*>(p.y.p) + row * p.y.ld;
     T* hidden = static_cast<T*>(p.hidden.p) + row * p.hidden.ld;
@@ -122,7 +123,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p, int lanes) {
     for (int c = 0; c < CH; ++c) {
       unpack(now.x[c], h[c]);
       if constexpr (DROP)
-        drop_eight(h[c], uint32_t(row * per_row + lane + c * lanes), key, p.drop.least, p.drop.scale);
+        drop_block<SUB, T>(h[c], uint32_t(row * per_row), lane, lanes, c, key, p.drop.least, p.drop.scale);
       if (p.res.p != nullptr) {
         float r[8];
         unpack(now.res[c], r);
@@ -140,9 +141,11 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p, int lanes) {
     float second[2] = {0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      if (lane + c * lanes < per_row) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+      for (int v = 0; v < kVectors<T>; ++v) {
+        if (vector_of<T>(lane, lanes, c, v) >= vectors) continue;
+#pragma unroll
+        for (int i = v * kVector<T>; i < (v + 1) * kVector<T>; ++i) {
           const float a = h[c][i] - mean;
           second[0] = fmaf(a, a, second[0]);
           second[1] += a;
@@ -160,63 +163,54 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p, int lanes) {
     if (row < p.rows) {
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const int g = lane + c * lanes;
-        if (g >= per_row) continue;
-        if (p.hidden.p != nullptr) store_eight<STREAM>(hidden + g * 8, h[c]);
+        if (vector_of<T>(lane, lanes, c, 0) >= vectors) continue;
+        if (p.hidden.p != nullptr) store_block<STREAM>(hidden, lane, lanes, c, vectors, h[c]);
         float out[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) out[i] = (h[c][i] - mean - rest) * rstd;
         if (w != nullptr) {
           float v[8];
-          unpack(HOLD ? wheld[HOLD ? c : 0] : load_vector(w, c), v);
+          unpack(HOLD ? wheld[HOLD ? c : 0] : load_affine(w, c), v);
 #pragma unroll
           for (int i = 0; i < 8; ++i) out[i] *= v[i];
         }
         if (b != nullptr) {
           float v[8];
-          unpack(HOLD ? bheld[HOLD ? c : 0] : load_vector(b, c), v);
+          unpack(HOLD ? bheld[HOLD ? c : 0] : load_affine(b, c), v);
 #pragma unroll
           for (int i = 0; i < 8; ++i) out[i] += v[i];
         }
-        store_eight(y + g * 8, out);
+        store_block(y, lane, lanes, c, vectors, out);
       }
       if (lane == 0) {
         if (p.mean != nullptr) p.mean[row] = mean + rest;
         if (p.rstd != nullptr) p.rstd[row] = rstd;
       }
     }
-    now.load(p, row + step, lane, lanes, per_row);
+    now.load(p, row + step, lane, lanes, vectors);
   }
 }
 
 // ---- backward --------------------------------------------------------------------------
-// Eight columns of a row's operands.
-template <typename T, bool STREAM>
-struct GradBlock {
-  Eight<T> dy, h, add;
-
-  __device__ __forceinline__ void load(const NormGradParams& p, int64_t row, int g, bool live) {
-    zero_eight(dy);
-    zero_eight(h);
-    zero_eight(add);
-    if (!live) return;
-    dy = load_eight<STREAM>(static_cast<const T*>(p.dy.p) + row * p.dy.ld + g * 8);
-    h = load_eight<STREAM>(static_cast<const T*>(p.hidden.p) + row * p.hidden.ld + g * 8);
-    if (p.dhidden.p != nullptr)
-      add = load_eight<STREAM>(static_cast<const T*>(p.dhidden.p) + row * p.dhidden.ld + g * 8);
-  }
-};
-
-// A lane's part of a row; a row past the end adds zeros.
+// A lane's part of a row's operands; a row past the end adds zeros.
 template <typename T, int CH, bool STREAM>
 struct GradRow {
-  GradBlock<T, STREAM> c[CH];
+  struct {
+    Eight<T> dy, h, add;
+  } c[CH];
   float mean, rstd;
 
-  __device__ __forceinline__ void load(const NormGradParams& p, int64_t row, int lane, int lanes, int per_row) {
+  __device__ __forceinline__ void load(const NormGradParams& p, int64_t row, int lane, int lanes, int vectors) {
     const bool live = row < p.rows;
+    const int in_row = live ? vectors : 0;
 #pragma unroll
-    for (int i = 0; i < CH; ++i) c[i].load(p, row, lane + i * lanes, live && lane + i * lanes < per_row);
+    for (int i = 0; i < CH; ++i) {
+      c[i].dy = load_block<STREAM>(static_cast<const T*>(p.dy.p) + row * p.dy.ld, lane, lanes, i, in_row);
+      c[i].h = load_block<STREAM>(static_cast<const T*>(p.hidden.p) + row * p.hidden.ld, lane, lanes, i, in_row);
+      zero_eight(c[i].add);
+      if (p.dhidden.p != nullptr)
+        c[i].add = load_block<STREAM>(static_cast<const T*>(p.dhidden.p) + row * p.dhidden.ld, lane, lanes, i, in_row);
+    }
     mean = live && p.mean != nullptr ? p.mean[row] : 0.f;
     rstd = live ? p.rstd[row] : 0.f;
   }
@@ -247,14 +241,18 @@ struct GradRow {
   }
 };
 
-// What a row's gradient goes to; dx and dres may be dy or dhidden: a lane has read what it writes.
-template <typename T, bool DROP, bool STREAM, bool STREAM_DX>
-__device__ __forceinline__ void store_gradient(const NormGradParams& p, int64_t row, int g, const DropKey& key,
-                                               float (&dh)[8]) {
-  if (p.dres.p != nullptr) store_eight<STREAM>(static_cast<T*>(p.dres.p) + row * p.dres.ld + g * 8, dh);
+// What block c of a row's gradient goes to; dx and dres may be dy or dhidden: a lane has read what it
+// writes.
+template <typename T, bool SUB, bool DROP, bool STREAM, bool STREAM_DX>
+__device__ __forceinline__ void store_gradient(const NormGradParams& p, int64_t row, int lane, int lanes, int c,
+                                               const DropKey& key, float (&dh)[8]) {
+  const int vectors = p.d / kVector<T>;
+  if (p.dres.p != nullptr)
+    store_block<STREAM>(static_cast<T*>(p.dres.p) + row * p.dres.ld, lane, lanes, c, vectors, dh);
   if (p.dx.p == nullptr) return;
-  if constexpr (DROP) drop_eight(dh, uint32_t(row * (p.d >> 3) + g), key, p.drop.least, p.drop.scale);
-  store_eight<STREAM_DX>(static_cast<T*>(p.dx.p) + row * p.dx.ld + g * 8, dh);
+  if constexpr (DROP)
+    drop_block<SUB, T>(dh, uint32_t(row * (p.d >> 3)), lane, lanes, c, key, p.drop.least, p.drop.scale);
+  store_block<STREAM_DX>(static_cast<T*>(p.dx.p) + row * p.dx.ld, lane, lanes, c, vectors, dh);
 }
 
 // Eight weights; ones where there are none.
@@ -276,23 +274,22 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(NormGradParams p, int l
   __shared__ float slot[2][kMaxWaves][2];
   __shared__ f32x4 meet[2 * kGradThreads];  // where the groups of a workgroup meet
   const int group = threadIdx.x / lanes, lane = threadIdx.x - group * lanes, groups = blockDim.x / lanes;
-  const int per_row = p.d >> 3;
+  const int vectors = p.d / kVector<T>;
   const float over = 1.f / float(p.d);
-  const bool inside = lane < per_row;
   DropKey key{};
   if constexpr (DROP) key = drop_key(p.drop);
   float dw[8] = {}, db[8] = {};
   Eight<T> weight;  // unpacked anew for each row (2047 x 4096: 20 us; held as floats 24)
   zero_eight(weight);
-  if (p.w != nullptr && inside) weight = load_eight(static_cast<const T*>(p.w) + lane * 8);
+  if (p.w != nullptr) weight = load_block(static_cast<const T*>(p.w), lane, lanes, 0, vectors);
 
   GradRow<T, 1, STREAM> now, next;
   const int64_t step = int64_t(gridDim.x) * groups;
   int64_t row = int64_t(blockIdx.x) * groups + group;
-  now.load(p, row, lane, lanes, per_row);
+  now.load(p, row, lane, lanes, vectors);
   int turn = 0;
   for (int64_t row0 = row - group; row0 < p.rows; row0 += step, row += step, turn ^= 1) {
-    next.load(p, row + step, lane, lanes, per_row);
+    next.load(p, row + step, lane, lanes, vectors);
     float sums[2] = {0.f, 0.f}, dy[8], h[8], w[8];
     weight_of(p.w, weight, w);
     unpack(now.c[0].dy, dy);
@@ -311,7 +308,7 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(NormGradParams p, int l
     // the stores the wait would be for them too
     now = next;
     now.arrived();
-    if (row < p.rows && inside) store_gradient<T, DROP, STREAM, false>(p, row, lane, key, h);
+    if (row < p.rows) store_gradient<T, SUB, DROP, STREAM, false>(p, row, lane, lanes, 0, key, h);
   }
 
   for (int which = 0; which < 2; ++which) {
@@ -331,7 +328,15 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(NormGradParams p, int l
         }
       }
     }
-    if (group == 0 && inside) store_eight(part + (int64_t(which) * gridDim.x + blockIdx.x) * p.d + lane * 8, v);
+    if (group != 0) continue;
+    float* to = part + (int64_t(which) * gridDim.x + blockIdx.x) * p.d;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {  // the lane's columns, four at a time: of one vector in bf16, of two in fp32
+      const int at = vector_of<T>(lane, lanes, 0, q * kVectors<T> / 2);
+      if (at < vectors)
+        *reinterpret_cast<f32x4*>(to + at * kVector<T> + (kVectors<T> == 1 ? 4 * q : 0)) =
+            f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+    }
   }
 }
 
@@ -344,7 +349,7 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(NormGradParams p, int l
 constexpr int kStripe = 64;
 template <typename T, int CH, bool SUB, bool WIDE, bool DROP, bool STREAM>
 __global__ void __launch_bounds__(1024) norm_apart_kernel(NormGradParams p, int lanes, int stripes) {
-  const int per_row = p.d >> 3;
+  const int per_row = p.d >> 3, vectors = p.d / kVector<T>;
   if (int(blockIdx.x) < stripes) {
     __shared__ f32x4 meet[kMaxWaves][8][4];
     const int quad = threadIdx.x & 7, sets = blockDim.x >> 3, g = blockIdx.x * 8 + quad;
@@ -414,17 +419,16 @@ __global__ void __launch_bounds__(1024) norm_apart_kernel(NormGradParams p, int 
   constexpr bool HOLD = CH < 4;
   Eight<T> held[HOLD ? CH : 1];
   const auto load_weight = [&](int c) {
-    const int g = lane + c * lanes;
     Eight<T> w;
     zero_eight(w);
-    if (p.w != nullptr) w = load_eight(static_cast<const T*>(p.w) + (g < per_row ? g : 0) * 8);
+    if (p.w != nullptr) w = load_anyway(static_cast<const T*>(p.w), lane, lanes, c, vectors);
     return w;
   };
   if constexpr (HOLD) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) held[c] = load_weight(c);
   }
-  now.load(p, row, lane, lanes, per_row);
+  now.load(p, row, lane, lanes, vectors);
   float sums[2] = {0.f, 0.f};
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
@@ -444,12 +448,11 @@ __global__ void __launch_bounds__(1024) norm_apart_kernel(NormGradParams p, int 
   const float c1 = p.mean != nullptr ? sums[0] * over : 0.f, c2 = sums[1] * over;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    const int g = lane + c * lanes;
-    if (g >= per_row) continue;
+    if (vector_of<T>(lane, lanes, c, 0) >= vectors) continue;
     float w[8], dh[8];
     weight_of(p.w, HOLD ? held[HOLD ? c : 0] : load_weight(c), w);
     now.gradient(c, w, c1, c2, dh);
-    store_gradient<T, DROP, STREAM, STREAM>(p, row, g, key, dh);
+    store_gradient<T, SUB, DROP, STREAM, STREAM>(p, row, lane, lanes, c, key, dh);
   }
 }
 
@@ -620,9 +623,11 @@ hipError_t backward(const NormGradParams& p, float* part, hipStream_t s) {
 hipError_t launch_norm(const NormParams& p, int dtype, hipStream_t s) {
   if (p.rows == 0) return hipSuccess;
   const bool drop = p.drop.least != 0;
-  if (dtype != 1) return drop ? forward<float, true, false>(p, s) : forward<float, false, false>(p, s);
-  if (streams(p.rows * p.d, dtype)) return drop ? forward<uint16_t, true, true>(p, s) : forward<uint16_t, false, true>(p, s);
-  return drop ? forward<uint16_t, true, false>(p, s) : forward<uint16_t, false, false>(p, s);
+  const bool stream = streams(p.rows * p.d);
+  if (dtype == 1 && stream) return drop ? forward<uint16_t, true, true>(p, s) : forward<uint16_t, false, true>(p, s);
+  if (dtype == 1) return drop ? forward<uint16_t, true, false>(p, s) : forward<uint16_t, false, false>(p, s);
+  if (stream) return drop ? forward<float, true, true>(p, s) : forward<float, false, true>(p, s);
+  return drop ? forward<float, true, false>(p, s) : forward<float, false, false>(p, s);
 }
 
 int64_t norm_grad_workspace(int64_t rows, int32_t d) {
@@ -634,10 +639,13 @@ hipError_t launch_norm_grad(const NormGradParams& p, int dtype, void* ws, hipStr
   if (p.rows == 0 && p.dw == nullptr && p.db == nullptr) return hipSuccess;
   float* part = static_cast<float*>(ws);
   const bool drop = p.drop.least != 0;
-  if (dtype != 1) return drop ? backward<float, true, false>(p, part, s) : backward<float, false, false>(p, part, s);
-  if (streams(p.rows * p.d, dtype))
+  const bool stream = streams(p.rows * p.d);
+  if (dtype == 1 && stream)
     return drop ? backward<uint16_t, true, true>(p, part, s) : backward<uint16_t, false, true>(p, part, s);
-  return drop ? backward<uint16_t, true, false>(p, part, s) : backward<uint16_t, false, false>(p, part, s);
+  if (dtype == 1)
+    return drop ? backward<uint16_t, true, false>(p, part, s) : backward<uint16_t, false, false>(p, part, s);
+  if (stream) return drop ? backward<float, true, true>(p, part, s) : backward<float, false, true>(p, part, s);
+  return drop ? backward<float, true, false>(p, part, s) : backward<float, false, false>(p, part, s);
 }
 
 }  // namespace ada

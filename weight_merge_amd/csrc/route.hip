@@ -78,7 +78,8 @@ __device__ __forceinline__ uint32_t row_min(uint32_t v) {
 template <int L, typename V>
 __device__ __forceinline__ V same_part_sum(V v) {
   const auto turned = [](auto ctrl, V a) {
-    return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, a), decltype(ctrl)::value, 0xf, 0xf, true));
+    return __builtin_bit_cast(
+        V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, a), decltype(ctrl)::value, 0xf, 0xf, true));
   };
   if constexpr (L <= 1) v += turned(Int<0x121>(), v);
   if constexpr (L <= 2) v += turned(Int<0x122>(), v);
@@ -136,8 +137,9 @@ __device__ __forceinline__ bool softmax8(const float (&z)[8], bool counts, uint3
 __device__ __forceinline__ double wave_total(double v) {
   const auto part = [&](auto ctrl, auto rows) {
     const uint64_t u = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = __builtin_amdgcn_update_dpp(0, int(uint32_t(u)), decltype(ctrl)::value, decltype(rows)::value, 0xf, true);
-    const uint32_t hi = __builtin_amdgcn_update_dpp(0, int(u >> 32), decltype(ctrl)::value, decltype(rows)::value, 0xf, true);
+    constexpr int CTRL = decltype(ctrl)::value, ROWS = decltype(rows)::value;
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, int(uint32_t(u)), CTRL, ROWS, 0xf, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, int(u >> 32), CTRL, ROWS, 0xf, true);
     return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
   };
   v += part(Int<0x111>(), Int<0xf>());
