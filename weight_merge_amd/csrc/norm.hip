@@ -28,7 +28,8 @@ struct RowShape {
 
 // ---- sums over the lanes of a row ------------------------------------------------------
 // N sums at once, the same on every lane of the row.  `slot` is LDS of kMaxWaves x N floats that
-// nothing else uses until after the next barrier; WIDE: several waves share a row.
+// nothing else uses until after the next barrier, not even the next row's sums: a wave may be there
+// while others still read.  WIDE: several waves share a row.
 template <int N, bool SUB, bool WIDE>
 __device__ __forceinline__ void row_totals(float (&v)[N], int lanes, float (*slot)[N]) {
   if constexpr (SUB) {
@@ -85,7 +86,7 @@ struct NormRow {
 template <typename T, int CH, bool SUB, bool WIDE, bool DROP, bool STREAM>
 __global__ void __launch_bounds__(1024) norm_kernel(NormParams p, int lanes) {
   __shared__ float mean_slot[kMaxWaves][1];
-  __shared__ float square_slot[kMaxWaves][2];
+  __shared__ float square_slot[2][kMaxWaves][2];  // by turns: rms has no other barrier between two rows' sums
   const int group = threadIdx.x / lanes, lane = threadIdx.x - group * lanes, groups = blockDim.x / lanes;
   const int per_row = p.d >> 3, vectors = p.d / kVector<T>;
   const T* w = static_cast<const T*>(p.w);
@@ -115,7 +116,8 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p, int lanes) {
   const int64_t step = int64_t(gridDim.x) * groups;
   int64_t row = int64_t(blockIdx.x) * groups + group;
   now.load(p, row, lane, lanes, vectors);
-  for (int64_t row0 = row - group; row0 < p.rows; row0 += step, row += step) {
+  int turn = 0;
+  for (int64_t row0 = row - group; row0 < p.rows; row0 += step, row += step, turn ^= 1) {
     T* y = static_cast<T*>(p.y.p) + row * p.y.ld;
     T* hidden = static_cast<T*>(p.hidden.p) + row * p.hidden.ld;
     float h[CH][8], sum[1] = {0.f};
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p, int lanes) {
         }
       }
     }
-    row_totals<2, SUB, WIDE>(second, lanes, square_slot);
+    row_totals<2, SUB, WIDE>(second, lanes, square_slot[turn]);
     float square = second[0] * over;
     if (!p.rms) {
       rest = second[1] * over;
