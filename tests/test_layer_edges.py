@@ -45,3 +45,30 @@ def test_rows_that_a_workgroup_takes_second(d, dtype, kind):
         ref = OL.norm(h, H.f64(w), None, kind, EPS)[0]
         bound = H.norm_bounds(h, np.zeros_like(h), H.f64(w), None, kind, EPS, dtype)[0]
         H.assert_within(y[first:first + 2], ref, bound, f"rows {first}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("renorm", (True, False))
+@pytest.mark.parametrize("E, k", ((5, 3), (12, 3), (30, 7), (64, 9)))
+def test_a_pick_out_of_range_has_no_part_in_its_row_s_gradient(E, k, renorm):
+    """Whatever its gate and its gate's gradient: neither at an expert nor in the sum over the row's picks."""
+    rows = 40
+    z = H.logits(1, rows, E, "fp32").to(DEV)
+    out = A.ada_route(z, k, renorm=renorm)
+    idx, gate = out.idx.clone(), out.gate.clone()
+    idx[2, 1], idx[3, k - 1], idx[4, 1], idx[5, 0], idx[6, 1] = 1 << 30, E, -7, E + 1, -1
+    gate[7, 2], idx[7, 2] = float("nan"), 2 ** 31 - 1
+    g = H.normal(2, (rows, k), 1.0, "fp32").to(DEV)
+    got = A.ada_route_backward(z, out._replace(idx=idx, gate=gate), dgate=g, renorm=renorm)
+    n, ni, ng, nz = H.f64(g), idx.cpu().numpy(), H.f64(gate), H.f64(z)
+    ref = OL.route_backward(nz, ni, ng, None, rows, n, None, renorm)
+    inside = (ni >= 0) & (ni < E)
+    p, rel = OL.softmax_rows(nz), H.probability_bound(nz)
+    part = np.where(inside, np.abs(ng) * (np.abs(n) + np.sum(np.where(inside, np.abs(ng * n), 0.0), axis=1, keepdims=True))
+                    if renorm else np.abs(n), 0.0)
+    mag = np.zeros((rows, E))
+    np.add.at(mag, (np.arange(rows)[:, None], np.where(inside, ni, 0)), part)
+    if not renorm:
+        mag = p * (mag + np.sum(p * mag, axis=1, keepdims=True))
+    # as for picks in range: the probabilities enter twice, sums are over k + 8 + 3 terms
+    H.assert_within(got, ref, H.rounded((2 * rel + (k + 16) * H.U) * mag, ref, "fp32"), "dlogits")

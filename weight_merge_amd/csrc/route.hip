@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradParams p) {
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         if (q * L >= p.k) break;
-        along += e[q] >= 0 ? g[q] * d[q] : 0.f;
+        along += uint32_t(e[q]) < uint32_t(p.E) ? g[q] * d[q] : 0.f;
       }
       along = row_sum<L>(along);
     }
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradParams p) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       if (q * L >= p.k) break;
-      if (e[q] >= 0 && e[q] < p.E) atomicAdd(theirs + e[q], g[q] * (d[q] - along));
+      if (uint32_t(e[q]) < uint32_t(p.E)) atomicAdd(theirs + e[q], g[q] * (d[q] - along));
     }
     __syncthreads();
 #pragma unroll
