@@ -537,7 +537,8 @@ typedef struct {
  */
 int ada_norm_backward(const ada_norm_grad_args* args, int32_t dtype, void* workspace, int64_t workspace_bytes,
                       void* stream);
-/* Bytes of workspace (as for the linear products); negative status on bad sizes. */
+/* Bytes of workspace (as for the linear products; none is needed without dweight and dbias); negative
+ * status on bad sizes. */
 int64_t ada_norm_backward_workspace(int64_t rows, int32_t d, int32_t dtype);
 
 typedef struct {
@@ -568,7 +569,7 @@ typedef struct {
  * NaN; the indices stay in range.
  */
 int ada_route(const ada_route_args* args, int32_t dtype, void* workspace, int64_t workspace_bytes, void* stream);
-/* Bytes of workspace; negative status on bad sizes. */
+/* Bytes of workspace (none is needed without balance); negative status on bad sizes. */
 int64_t ada_route_workspace(int64_t rows, int32_t E);
 
 typedef struct {

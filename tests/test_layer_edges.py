@@ -1,10 +1,13 @@
 """Norm, dropout and router calls at the edges of what their documentation allows."""
+import types
+
 import numpy as np
 import pytest
 import torch
 
 import layer_helpers as H
 from oracle import layer as OL
+from weight_merge_amd import _lib
 from weight_merge_amd import api as A
 
 DEV = "cuda"
@@ -72,3 +75,56 @@ def test_a_pick_out_of_range_has_no_part_in_its_row_s_gradient(E, k, renorm):
         mag = p * (mag + np.sum(p * mag, axis=1, keepdims=True))
     # as for picks in range: the probabilities enter twice, sums are over k + 8 + 3 terms
     H.assert_within(got, ref, H.rounded((2 * rel + (k + 16) * H.U) * mag, ref, "fp32"), "dlogits")
+
+
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="passes fake pointers: runs where no GPU is visible")
+
+
+@no_gpu
+@pytest.mark.parametrize("dt, rows, d", ((_lib.ADA_BF16, 5000, 64), (_lib.ADA_F32, 4096, 8192)))
+def test_norm_backward_of_rows_alone_needs_no_workspace(dt, rows, d):
+    """Only the sums over rows go through it."""
+    lib = _lib.load()
+    need = lib.ada_norm_backward_workspace(rows, d, dt)
+    assert need > 0
+    at = {n: (i + 1) << 36 for i, n in enumerate(("dy", "hidden", "dhidden", "weight", "mean", "rstd", "dx", "dresidual",
+                                                  "dweight", "dbias"))}
+    lds = dict.fromkeys(("ld_dy", "ld_hidden", "ld_dhidden", "ld_dx", "ld_dresidual"), d)
+
+    def call(ws, nbytes, **kw):
+        return lib.ada_norm_backward(_lib.AdaNormGradArgs(**{**at, **lds, "rows": rows, "d": d, **kw}), dt, ws, nbytes, None)
+
+    # with no GPU a call that passes the checks ends at its first HIP call
+    assert call(None, 0, dweight=None, dbias=None) == _lib.ADA_EHIP
+    assert call(8, 0, dweight=None, dbias=None) == _lib.ADA_EALIGN
+    for one in ("dweight", "dbias"):
+        assert call(None, 0, **{one: None}) == _lib.ADA_EINVAL
+        assert call(1 << 46, need - 1, **{one: None}) == _lib.ADA_ESHAPE
+        assert call(1 << 46, need, **{one: None}) == _lib.ADA_EHIP
+
+
+def test_norm_backward_allocates_no_workspace_for_rows_alone(monkeypatch):
+    needs = []
+    monkeypatch.setattr(A, "_current", lambda dev: None)
+    monkeypatch.setattr(A, "_raw_stream", lambda dev: 0)
+    monkeypatch.setattr(A, "_workspace", lambda need, ws, dev: needs.append(need) or (None, 0, None))
+    monkeypatch.setattr(A, "_workspace_bytes", lambda *a: 4096)
+    monkeypatch.setattr(A._lib, "load", lambda: types.SimpleNamespace(ada_norm_backward=lambda *a: 0))
+    x, stats = torch.zeros(2000, 24), (torch.zeros(2000), torch.zeros(2000))
+    A.ada_norm_backward(x, x, stats, want_dweight=False)
+    A.ada_norm_backward(x, x, stats)
+    A.ada_norm_backward(x, x, stats, want_dweight=False, want_dbias=True)
+    A.ada_norm_backward(x, x, stats, want_dweight=False, dbias=torch.zeros(24))
+    assert needs == [0, 4096, 4096, 4096]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ("fp32", "bf16"))
+@pytest.mark.parametrize("rows, d", ((900, 264), (2047, 4096)))
+def test_gradients_of_rows_alone_are_those_of_the_whole_call(rows, d, dtype):
+    dy, h, dhidden = (H.normal(i, (rows, d), 1.0, dtype).to(DEV) for i in (1, 2, 3))
+    stats = [torch.tensor(v, dtype=torch.float32, device=DEV) for v in OL.norm(H.f64(h), None, None, "layer", EPS)[1:]]
+    kw = dict(dhidden=dhidden, p=0.1, seed=3, want_dresidual=True)
+    dx, dr, dw, _ = A.ada_norm_backward(dy, h, stats, **kw)
+    got = A.ada_norm_backward(dy, h, stats, want_dweight=False, **kw)
+    assert torch.equal(got[0], dx) and torch.equal(got[1], dr) and got[2] is None

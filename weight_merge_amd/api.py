@@ -749,7 +749,7 @@ def ada_norm(x: torch.Tensor, weight=None, bias=None, residual=None, kind: str =
 
 
 def norm_backward_workspace_bytes(rows: int, d: int, dtype: torch.dtype) -> int:
-    """Bytes of workspace ada_norm_backward needs at these sizes."""
+    """Bytes of workspace ada_norm_backward needs at these sizes (none without dweight and dbias)."""
     return _workspace_bytes("ada_norm_backward_workspace", rows, d, _DT[dtype])
 
 
@@ -796,7 +796,8 @@ def ada_norm_backward(dy: torch.Tensor, hidden: torch.Tensor, stats, weight=None
     if dbias is None and want_dbias:
         dbias = torch.empty(d, dtype=dt, device=dy.device)
         pdb = dbias.data_ptr()
-    ws, nbytes, _keep = _workspace(_workspace_bytes("ada_norm_backward_workspace", rows, d, dc), workspace, dev)
+    need = 0 if dweight is None and dbias is None else _workspace_bytes("ada_norm_backward_workspace", rows, d, dc)
+    ws, nbytes, _keep = _workspace(need, workspace, dev)
     args = AdaNormGradArgs(pdy, ph, pdh, pw, pm, ps, pdx, pdr, pdw, pdb, lddy, ldh, lddh, lddx, lddr, rows, d, code,
                            *drop)
     _check(_lib.load().ada_norm_backward(args, dc, ws, nbytes, _raw_stream(dev)), "ada_norm_backward")

@@ -919,7 +919,7 @@ int ada_norm_backward(const ada_norm_grad_args* q, int32_t dtype, void* workspac
                       bytes_of(q->dbias, d, esz, true),
                       bytes_of(q->drop.state, 2, 8, false)};
   if (bytes_overlap(m, 11, {{0, 2}, {1, 2}, {0, 3}, {1, 3}})) return ADA_EINVAL;
-  const int64_t need = ada::norm_grad_workspace(rows, q->d);
+  const int64_t need = q->dweight != nullptr || q->dbias != nullptr ? ada::norm_grad_workspace(rows, q->d) : 0;
   if (int st = check_workspace(workspace, workspace_bytes, need, m, 11, 1); st != ADA_OK) return st;
   p.dy = {q->dy, q->ld_dy};
   p.hidden = {q->hidden, q->ld_hidden};
