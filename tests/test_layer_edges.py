@@ -128,3 +128,20 @@ def test_gradients_of_rows_alone_are_those_of_the_whole_call(rows, d, dtype):
     dx, dr, dw, _ = A.ada_norm_backward(dy, h, stats, **kw)
     got = A.ada_norm_backward(dy, h, stats, want_dweight=False, **kw)
     assert torch.equal(got[0], dx) and torch.equal(got[1], dr) and got[2] is None
+
+
+def test_a_balance_needs_somewhere_to_go():
+    """A Routing of a call without balance is not written to by one that is asked for it."""
+    z = torch.zeros(4, 6)
+    bare = (torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2), None, None, None, None)
+    full = (*bare[:2], torch.zeros(6, dtype=torch.int32), torch.zeros(6), torch.zeros(1), torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="no tensors for the balance"):
+        A.ada_route(z, 2, out=bare)
+    with pytest.raises(ValueError, match="no tensors for the balance"):
+        A.ada_route(z, 2, out=A.Routing(*bare), balance=True)
+    for i in range(2, 6):
+        with pytest.raises(ValueError, match="no tensors for the balance"):
+            A.ada_route(z, 2, out=full[:i] + (None,) + full[i + 1:])
+    for kw in (dict(out=full), dict(out=bare, balance=False), dict(out=full, balance=False)):
+        with pytest.raises(ValueError, match="must be on the device"):  # the next thing that is wrong
+            A.ada_route(z, 2, **kw)

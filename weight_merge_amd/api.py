@@ -870,6 +870,8 @@ def ada_route(logits: torch.Tensor, k: int, renorm: bool = True, valid=None, bal
         pp = _vec(out.prob, E, f32, dev, "prob")
         po = _vec(out.loss, 1, f32, dev, "loss")
         pu = _vec(out.used, 1, i32, dev, "used")
+        if pc is None or pp is None or po is None or pu is None:
+            raise ValueError("out has no tensors for the balance: counts, prob, loss and used are needed")
     _current(dev)
     ws, nbytes, _keep = _workspace(_workspace_bytes("ada_route_workspace", rows, E) if balance else 0, workspace, dev)
     args = AdaRouteArgs(pl, pv, pi, pg, pc, pp, po, pu, ld, rows, E, k, bool(renorm))
