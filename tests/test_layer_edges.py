@@ -145,3 +145,19 @@ def test_a_balance_needs_somewhere_to_go():
     for kw in (dict(out=full), dict(out=bare, balance=False), dict(out=full, balance=False)):
         with pytest.raises(ValueError, match="must be on the device"):  # the next thing that is wrong
             A.ada_route(z, 2, **kw)
+
+
+def test_seeds_and_offsets_are_whole_numbers_of_any_kind():
+    """Python's and NumPy's alike, modulo 2^64."""
+    m = 2 ** 64
+    for v in (0, 7, -1, 2 ** 31 - 1, -2 ** 31):
+        for kind in (int, np.int64, np.int32) + ((np.uint64, np.uint32) if v >= 0 else ()):
+            assert A._drop(0.1, kind(v), kind(v), -1) == (0.1, v % m, v % m, None)
+    assert A._drop(0.1, np.uint64(m - 1), np.int64(-2 ** 63), -1) == (0.1, m - 1, 2 ** 63, None)
+    state = torch.zeros(2, dtype=torch.int64)
+    assert A._drop(0.1, state, np.int64(-3), -1) == (0.1, 0, m - 3, state.data_ptr())
+    for bad in (1.0, "1", np.float64(2)):
+        with pytest.raises(TypeError):
+            A._drop(0.1, bad, 0, -1)
+        with pytest.raises(TypeError):
+            A._drop(0.1, 1, bad, -1)

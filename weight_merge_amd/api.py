@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+from operator import index
 from typing import NamedTuple
 
 import torch
@@ -645,12 +646,12 @@ def _drop(p: float, seed, offset: int, dev: int):
             raise ValueError("dropout needs a seed")
         return 0.0, 0, 0, None
     if not isinstance(seed, torch.Tensor):
-        return p, seed & _M64, offset & _M64, None
+        return p, index(seed) & _M64, index(offset) & _M64, None
     if seed.dtype is not torch.int64 or seed.shape != (2,) or seed.stride(0) != 1:
         raise TypeError("a seed on the device must be int64 [2]: the seed and the offset's start")
     if seed.get_device() != dev:
         raise ValueError(f"seed is on {seed.device}, not with the other tensors")
-    return p, 0, offset & _M64, seed.data_ptr()
+    return p, 0, index(offset) & _M64, seed.data_ptr()
 
 
 def _shape(x: torch.Tensor, name: str):
