@@ -502,8 +502,8 @@ typedef struct {
 /*
  * h = residual + dropout(x);  per row: mean of h, rstd = 1 / sqrt(mean of (h - mean)^2 + eps),
  * y = (h - mean) rstd weight + bias.  ADA_NORM_RMS: the same with 0 for the mean.  The norm reads
- * h before it is rounded to the storage type.  Squares are fp32: a row whose sum of squares
- * passes 3.4e38 gets rstd 0.
+ * h before it is rounded to the storage type.  Sums are fp32: a row whose sum of (h - mean)^2 passes
+ * 3.4e38 gets rstd 0 and y = bias; one whose sum of h does, on its way too, gets NaN (ADA_NORM_LAYER).
  */
 int ada_norm(const ada_norm_args* args, int32_t dtype, void* stream);
 

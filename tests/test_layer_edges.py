@@ -161,3 +161,29 @@ def test_seeds_and_offsets_are_whole_numbers_of_any_kind():
             A._drop(0.1, bad, 0, -1)
         with pytest.raises(TypeError):
             A._drop(0.1, 1, bad, -1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ("fp32", "bf16"))
+@pytest.mark.parametrize("d", (8, 264, 4104, 16392))
+def test_rows_whose_sums_pass_the_type_s_range(d, dtype):
+    """Finite rows: squares that overflow are a deviation without end, rstd 0; a sum that does leaves no mean. The rows
+    beside them are as without them."""
+    low = torch.finfo(H.TD[dtype]).min
+    x = H.normal(1, (6, d), 1.0, dtype)
+    sign = torch.where(torch.arange(d) % 2 == 0, 1.0, -1.0).to(H.TD[dtype])
+    ref = {kind: A.ada_norm(x.to(DEV), kind=kind) for kind in ("layer", "rms")}
+    x[1], x[3], x[5] = 2.0 ** 65 * sign, low, 2.0 ** 65
+    x, w, b = x.to(DEV), H.normal(2, (d,), 1.0, dtype).to(DEV), H.normal(3, (d,), 1.0, dtype).to(DEV)
+    for kind in ("layer", "rms"):
+        rstd, mean = torch.empty(6, device=DEV), torch.empty(6, device=DEV)
+        y = A.ada_norm(x, kind=kind, eps=EPS, stats=(mean, rstd))
+        assert torch.equal(y[::2], ref[kind][::2])
+        affine = A.ada_norm(x, w, bias=b, kind=kind, eps=EPS)
+        assert (y[1] == 0).all() and rstd[1] == 0 and torch.equal(affine[1], b)
+        if kind == "rms":
+            assert (y[3] == 0).all() and rstd[3] == 0 and torch.equal(affine[3], b)
+            assert (y[5] == 0).all() and rstd[5] == 0
+        else:
+            assert y[3].isnan().all() and rstd[3].isnan()
+            assert (y[5] == 0).all() and mean[5] == 2.0 ** 65  # a constant row: powers of two are exact
