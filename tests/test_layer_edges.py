@@ -187,3 +187,23 @@ def test_rows_whose_sums_pass_the_type_s_range(d, dtype):
         else:
             assert y[3].isnan().all() and rstd[3].isnan()
             assert (y[5] == 0).all() and mean[5] == 2.0 ** 65  # a constant row: powers of two are exact
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows, d, chains", ((1 << 18, 8200, 40), (1 << 18, 8192, 256), (1 << 20, 2056, 768), (1 << 22, 264, 4096)))
+def test_sums_over_many_rows_keep_what_is_small(rows, d, chains):
+    """dw and db in fp32 of ones in the first rows, one for each lane that sums a column, and 2^-25 in all others, each
+    of which alone vanishes beside a one. A lane puts its sum aside every 256 rows: in the run that holds the one 255 of the
+    small ones may be lost, 2^-17 in all, later runs are exact (multiples of 2^-25 below 2^-16). The lanes' sums meet in
+    fewer than 64 roundings one after the other, 2^-18 of the total."""
+    dy = torch.full((rows, d), 2.0 ** -25, device=DEV)
+    dy[:chains] = 1.0
+    h = torch.ones((rows, d), device=DEV)
+    stats = (None, torch.ones(rows, device=DEV))
+    _, _, dw, db = A.ada_norm_backward(dy, h, stats, kind="rms", want_dx=False, want_dbias=True)
+    small = (rows - chains) * 2.0 ** -25
+    true = chains + small
+    bound = chains * 2.0 ** -17 + true * 2.0 ** -18
+    assert small > 2 * bound
+    for name, got in (("dw", dw), ("db", db)):
+        H.assert_within(got, np.full(d, true), np.full(d, bound), name)

@@ -18,6 +18,9 @@ namespace {
 constexpr int kMaxWaves = 16;
 constexpr int kGradThreads = 1024;  // of a workgroup of norm_grad_kernel, about
 constexpr int kGradBlocks = 256;    // one a CU: twice as many write and join twice the partial sums
+// Rows that a lane's sums for dw and db take one after the other before they are put aside: fp32 sums of
+// hundreds of terms, and of hundreds of such, instead of one of up to 10^5 (2^20 x 8200 fp32: error of db 3e-7, else 3e-6)
+constexpr int kRun = 256;
 
 // Lanes that share a row: `lanes` below 64 is a power of two, otherwise a multiple of 64.
 struct RowShape {
@@ -274,7 +277,7 @@ __device__ __forceinline__ void weight_of(const void* w, const Eight<T>& raw, fl
 template <typename T, bool SUB, bool WIDE, bool DROP, bool STREAM>
 __global__ void __launch_bounds__(1024) norm_grad_kernel(NormGradParams p, int lanes, float* part) {
   __shared__ float slot[2][kMaxWaves][2];
-  __shared__ f32x4 meet[2 * kGradThreads];  // where the groups of a workgroup meet
+  __shared__ f32x4 meet[4 * kGradThreads];  // sums put aside, then where the groups of a workgroup meet
   const int group = threadIdx.x / lanes, lane = threadIdx.x - group * lanes, groups = blockDim.x / lanes;
   const int vectors = p.d / kVector<T>;
   const float over = 1.f / float(p.d);
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(NormGradParams p, int l
   int64_t row = int64_t(blockIdx.x) * groups + group;
   now.load(p, row, lane, lanes, vectors);
   int turn = 0;
-  for (int64_t row0 = row - group; row0 < p.rows; row0 += step, row += step, turn ^= 1) {
+  for (int64_t row0 = row - group; row0 < p.rows; row0 += step, row += step, ++turn) {
     next.load(p, row + step, lane, lanes, vectors);
     float sums[2] = {0.f, 0.f}, dy[8], h[8], w[8];
     weight_of(p.w, weight, w);
@@ -304,13 +307,31 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(NormGradParams p, int l
       dw[i] = fmaf(dy[i], xhat, dw[i]);
       db[i] += dy[i];
     }
-    row_totals<2, SUB, WIDE>(sums, lanes, slot[turn]);
+    row_totals<2, SUB, WIDE>(sums, lanes, slot[turn & 1]);
     now.gradient(0, w, p.mean != nullptr ? sums[0] * over : 0.f, sums[1] * over, h);
     // the next row's loads are waited for before this row's stores: the counter holds both, and behind
     // the stores the wait would be for them too
     now = next;
     now.arrived();
     if (row < p.rows) store_gradient<T, SUB, DROP, STREAM, false>(p, row, lane, lanes, 0, key, h);
+    if (turn % kRun == kRun - 1) {
+      const f32x4 sum[4] = {{dw[0], dw[1], dw[2], dw[3]}, {dw[4], dw[5], dw[6], dw[7]},
+                            {db[0], db[1], db[2], db[3]}, {db[4], db[5], db[6], db[7]}};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f32x4& at = meet[j * blockDim.x + threadIdx.x];
+        at = turn < kRun ? sum[j] : at + sum[j];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dw[i] = db[i] = 0.f;
+    }
+  }
+  if (turn >= kRun) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      dw[i] += meet[(i >> 2) * blockDim.x + threadIdx.x][i & 3];
+      db[i] += meet[(2 + (i >> 2)) * blockDim.x + threadIdx.x][i & 3];
+    }
   }
 
   for (int which = 0; which < 2; ++which) {
@@ -360,6 +381,9 @@ __global__ void __launch_bounds__(1024) norm_apart_kernel(NormGradParams p, int 
     const T* hp = static_cast<const T*>(p.hidden.p) + (inside ? g : 0) * 8;
     f32x4 sum[4] = {};  // dw, dw, db, db
     constexpr int U = 4;
+    constexpr bool LONG = CH == 4;  // of those alone more than kRun rows a lane come here (apart())
+    f32x4 aside[4] = {};
+    int run = 0;
     for (int64_t row0 = threadIdx.x >> 3; row0 < p.rows; row0 += int64_t(sets) * U) {
       Eight<T> a[U], b[U];
       float mean[U], rstd[U];
@@ -383,6 +407,21 @@ __global__ void __launch_bounds__(1024) norm_apart_kernel(NormGradParams p, int 
           sum[2 + (i >> 2)][i & 3] += dy[i];
         }
       }
+      if constexpr (LONG) {
+        run += U;
+        if (run == kRun) {
+          run = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            aside[j] += sum[j];
+            sum[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+          }
+        }
+      }
+    }
+    if constexpr (LONG) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum[j] += aside[j];
     }
     // the eight sets of a wave, then the waves
 #pragma unroll
