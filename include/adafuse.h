@@ -423,8 +423,9 @@ int64_t ada_glu_backward_workspace(int64_t rows, int32_t d_out, int32_t d_in, in
  *     elements, 0 <= rows <= 2^22 (with rows = 0 the matrices may be NULL); columns are a
  *     multiple of 8.  Vectors of fp32 or int32 are contiguous and 4-byte aligned.
  *   - Statistics, sums, gates and losses are fp32 (or wider); each result is rounded to the
- *     storage type once.  No atomics: equal calls give equal bits, and a gradient's do not depend
- *     on which others are asked for.
+ *     storage type once.  Equal calls give equal bits, and a gradient's do not depend on which
+ *     others are asked for (but for an expert that a row given to ada_route_backward names three
+ *     times or more, as ada_route never does: its parts are added in any order).
  *   - An output may not overlap an input or another output (ADA_EINVAL), but for the outputs that
  *     may be an input itself (same pointer and row stride), named at each call.
  */
@@ -592,8 +593,9 @@ typedef struct {
 /*
  * With p = softmax(logits) and dp_e = dloss E counts_e / (k n^2), to which dgate is added at the
  * picked experts without renorm: dlogits = p (dp - sum p dp), plus gate (dgate - sum gate dgate)
- * at the picked with renorm.  The counts are constants.  Rows that did not count (idx -1 in
- * their first slot) get zeros; an index outside [0, E) is passed over.
+ * at the picked with renorm.  The counts are constants.  Rows that did not count (idx below 0 in
+ * their first slot) get zeros; an index outside [0, E) is passed over, with its gate and its gate's
+ * gradient, and one that is named several times gets every part.
  */
 int ada_route_backward(const ada_route_grad_args* args, int32_t dtype, void* stream);
 

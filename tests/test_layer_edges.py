@@ -207,3 +207,28 @@ def test_sums_over_many_rows_keep_what_is_small(rows, d, chains):
     assert small > 2 * bound
     for name, got in (("dw", dw), ("db", db)):
         H.assert_within(got, np.full(d, true), np.full(d, bound), name)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("renorm", (True, False))
+@pytest.mark.parametrize("E, k", ((5, 3), (16, 4), (64, 9)))
+def test_an_expert_that_a_row_names_twice_gets_both_parts(E, k, renorm):
+    """In slots of one lane and of two; equal calls give equal bits."""
+    rows = 300
+    z = H.logits(3, rows, E, "fp32").to(DEV)
+    out = A.ada_route(z, k, renorm=renorm)
+    idx = out.idx.clone()
+    idx[::2, 1], idx[1::2, k - 1] = idx[::2, 0], idx[1::2, 0]
+    g = H.normal(4, (rows, k), 1.0, "fp32").to(DEV)
+    got = [A.ada_route_backward(z, out._replace(idx=idx), dgate=g, renorm=renorm) for _ in range(4)]
+    assert all(torch.equal(v, got[0]) for v in got)
+    n, ni, ng, nz = H.f64(g), idx.cpu().numpy(), H.f64(out.gate), H.f64(z)
+    ref = OL.route_backward(nz, ni, ng, None, rows, n, None, renorm)
+    p, rel = OL.softmax_rows(nz), H.probability_bound(nz)
+    part = np.abs(ng) * (np.abs(n) + np.sum(np.abs(ng * n), axis=1, keepdims=True)) if renorm else np.abs(n)
+    mag = np.zeros((rows, E))
+    np.add.at(mag, (np.arange(rows)[:, None], ni), part)
+    if not renorm:
+        mag = p * (mag + np.sum(p * mag, axis=1, keepdims=True))
+    # as for picks named once: the probabilities enter twice, sums are over k + 8 + 3 terms
+    H.assert_within(got[0], ref, H.rounded((2 * rel + (k + 16) * H.U) * mag, ref, "fp32"), "dlogits")

@@ -17,8 +17,9 @@ constexpr int kBlocks = 4;
 constexpr int kThreads = 256;
 
 // Where block g of a matrix with row stride ld begins.  The row is g / per_row, by the reciprocal
-// `inv` = ceil(2^64 / per_row) (0: per_row is 1): exact, for its error, below g per_row / 2^64, stays
-// under 1 / per_row with g < 2^32 and per_row <= 2^19.
+// `inv` = ceil(2^64 / per_row) (0: per_row is 1): inv is above 2^64 / per_row by less than one, so the product
+// above g / per_row by less than g / 2^64 < 2^-32, while g / per_row is below the next whole number by
+// 1 / per_row >= 2^-19 or more: exact.
 __device__ __forceinline__ int64_t block_at(uint64_t g, uint32_t per_row, uint64_t inv, int64_t ld) {
   const uint64_t row = inv == 0 ? g : __umul64hi(g, inv);
   return int64_t(row) * ld + int64_t(g - row * per_row) * 8;

@@ -125,7 +125,8 @@ __device__ __forceinline__ void store_block(T* row, int lane, int lanes, int c, 
 }
 
 // Whether a call on matrices of this many elements streams what it will not need again soon: its
-// inputs, the residual stream and that stream's gradient, but not y and dx, which the next call reads.
+// inputs, the residual stream and that stream's gradient, but not y and dx, which the next call reads
+// (norm_apart_kernel streams dx, so that dy and h stay for its second reading of them).
 // Between products (norm, projection, norm, ..) of 4096 columns ordinary accesses throughout take 33.6 us
 // a layer at 509 rows (streamed: 33.6; with y too 35.0), 81.6 at 2047 (79.6; 80.9), 1800 at 16384 rows
 // of 8192 columns (1776; 1814); the backward pass at 509 rows 35.2 (37.5).  The same number in fp32:

@@ -6,10 +6,14 @@
 //   ("rms": without mean(t)); dresidual = dh, dx = dropout(dh), dw = sum over rows of dy xhat,
 //   db = sum over rows of dy
 //
-// Bound by memory: every matrix is read once and written once.  A row lives in the registers of
+// Bound by memory: every matrix is read once and written once, but for dy and h of the backward pass
+// for few or wide rows (norm_apart_kernel), which reads them twice.  A row lives in the registers of
 // one group of lanes from its load to its store, in blocks of eight elements a lane: a power of
 // two of lanes for rows of up to 256 elements, otherwise whole waves, whose sums meet in LDS.
-// 4096 x 8192 bf16 with residual and dropout: forward 46.8 us, backward 59.0, 5.7 TB/s either way.
+// 4096 x 8192 bf16 with residual and dropout: forward 46.8 us, backward 58.9, 5.7 TB/s either way.
+// Four fp32 blocks a lane are the exception: a bound of 1024 threads leaves 128 registers, and 36 bytes a
+// lane go to scratch (forward; 100 with dropout, 80 and 112 in the backward pass): 585 x 28672 writes 151 MB
+// for 134 in 58 us, and 106 for 67 in 84.
 #include "elements.h"
 
 namespace ada {
@@ -569,14 +573,17 @@ RowShape forward_shape(int64_t rows, int d) {
 }
 
 // Rows and columns apart, or in one pass.  Apart reads 7 matrices for 5 but has no partial sums and
-// one launch; it is the faster up to 550 to 1400 rows, more with more columns: 512 x 4096 bf16 8.0
+// one launch; it is the faster from 512 up to 550 to 1400 rows, more with more columns: 512 x 4096 bf16 8.0
 // against 13.6 us, 1024 x 4096 14.7 against 15.9, 1536 x 4096 20.3 against 17.7; 512 x 1032 7.4 against
 // 8.4, 1024 x 1032 11.3 against 9.8; 1024 x 8192 19.7 against 22.9, 4096 x 8192 67 against 54.  Past 8192
-// columns a lane of the one pass would hold two blocks or more with their sums, which spilled:
-// 1170 x 28672 in 96 us apart, 218 in one pass.
+// columns a lane of the one pass, 1024 threads to a workgroup, would hold two blocks or more with their sums in
+// the 128 registers that leaves, which spilled: 1170 x 28672 in 96 us apart, 218 in one pass.  So there is a step
+// behind 8192 columns, the larger the more rows: 8192 and 8200 columns bf16 11.7 and 15.3 us at 512 rows,
+// 31 and 46 at 2048, 54 and 85 at 4096, 182 and 321 at 16384.
 bool apart(int64_t rows, int d) { return d > 8192 || rows <= 512 + d / 8; }
 
-// The rows' part, as the forward pass; at least 512 threads for the columns' part.
+// The rows' part as in the forward pass, in workgroups of as many rows as 512 threads hold, one at least: 320
+// (2056 to 2560 columns, and twice and four times that) to 1024 threads, for the columns' part too.
 RowShape apart_shape(int d) {
   const int per_row = d / 8;
   return row_shape(per_row, per_row <= 512 ? 1 : per_row <= 1024 ? 2 : 4, 512);

@@ -14,7 +14,7 @@
 // lane (bf16) brings a wave 8 to 64 rows and the softmax needs at most three steps across
 // lanes.  A pick is a maximum over a lane's eight keys and the row's lanes, then the lowest index that
 // holds it.  Bound by launches and latency up to some ten thousand rows (16384 rows of 64 experts
-// are 5 MB), by the picks' instructions past that (262144 x 64, eight picks: 40 us for 84 MB).
+// are 5 MB), by the picks' instructions past that (262144 x 64 fp32, eight picks: 41 us for 84 MB, 48 with the balance).
 #include "elements.h"
 
 namespace ada {
@@ -339,7 +339,10 @@ __global__ void __launch_bounds__(kThreads) balance_join_kernel(RouteParams p, B
 
 // ---- backward --------------------------------------------------------------------------
 // The lanes of a row share its picks, add each one's part to the row in LDS (an index outside
-// [0, E) is passed over, one that is there twice is added twice), and take their eight experts' back.
+// [0, E) is passed over, one that is there twice is added twice), and take their eight experts' back.  The
+// additions are atomic: of two parts their order does not matter, of three, which the forward pass never
+// writes, it would.  262144 x 64 fp32, eight picks: 47 us for 159 MB; a lane's eight logits in a row
+// make each 16-byte access touch half of every line (bf16, whole lines: 38 us for 92 MB).
 template <typename T, int L, bool VEC>
 __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradParams p) {
   __shared__ float at_expert[256][8];  // rows of 8 L, one to L lanes
