@@ -672,7 +672,7 @@ def ada_dropout(x: torch.Tensor, p: float, seed, offset: int = 0, residual=None,
     """y = residual + dropout(x) for x [rows, d]: an element is zero with probability p (to the nearest 2^-16),
     else divided by 1 - p.  y may be x or the residual itself.
 
-    The mask is a function of (seed, offset) and the element's place, and is not stored: give the
+    The mask is a function of (seed, offset), whole numbers, and the element's place, and is not stored: give the
     backward pass the same numbers, and every call of a step an offset of its own.  `seed` may be
     an int64 [2] tensor on the device, (seed, start of the offset): a captured call then draws
     anew whenever that tensor changes.  `stream` as in ada_linear."""
@@ -840,7 +840,8 @@ def ada_route(logits: torch.Tensor, k: int, renorm: bool = True, valid=None, bal
 
     A logit of -inf closes its expert to the row.  `valid` (bool or uint8 [rows]) marks the rows that
     count; the others, rows with every expert closed, and slots without an open expert left get
-    index -1 and gate 0.  `out` is a Routing (or six tensors) to write to; `stream` as in ada_linear."""
+    index -1 and gate 0.  `out` is a Routing (or six tensors; without balance the last four may be None) to write
+    to; `stream` as in ada_linear."""
     if stream is not None:
         return _on(stream, ada_route, logits, k, renorm, valid, balance, out, workspace)
     rows, E = _shape(logits, "logits")

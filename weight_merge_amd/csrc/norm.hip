@@ -10,7 +10,7 @@
 // for few or wide rows (norm_apart_kernel), which reads them twice.  A row lives in the registers of
 // one group of lanes from its load to its store, in blocks of eight elements a lane: a power of
 // two of lanes for rows of up to 256 elements, otherwise whole waves, whose sums meet in LDS.
-// 4096 x 8192 bf16 with residual and dropout: forward 46.8 us, backward 58.9, 5.7 TB/s either way.
+// 4096 x 8192 bf16 with residual and dropout: forward 47.0 us, backward 58.9, 5.7 TB/s either way.
 // Four fp32 blocks a lane are the exception: a bound of 1024 threads leaves 128 registers, and 36 bytes a
 // lane go to scratch (forward; 100 with dropout, 80 and 112 in the backward pass): 585 x 28672 writes 151 MB
 // for 134 in 58 us, and 106 for 67 in 84.
